@@ -26,7 +26,7 @@ __all__ = [
     "qz_gemm_w4a16_nvfp4", "qz_gemm_w4a16_mxfp4", "qz_col_amax", "qz_smooth_factors", "qz_quantize_int8_rows",
     "qz_gemm_int8", "qz_gemm_fp8_block_quant", "qz_gemm_nvfp4_quant", "qz_gemm_mxfp4_quant", "SMOOTH_NONE",
     "SMOOTH_DIVIDE",
-    "SMOOTH_MULTIPLY",
+    "SMOOTH_MULTIPLY", "PagedKV", "qz_block_tables", "qz_kv_append_fp8_paged", "qz_attn_fp8_paged",
 ]
 
 F32, BF16 = 0, 1
@@ -36,6 +36,7 @@ OP_QUANTIZE_FP8, OP_QUANTIZE_NVFP4, OP_KV_WRITE_FP8 = 0, 1, 2
 OP_GEMM_W4A16, OP_GEMM_FP8_BLOCK, OP_GEMM_NVFP4, OP_GEMM_MXFP4 = 3, 4, 5, 6
 OP_GEMM_NVFP4_GROUPED, OP_PREPARE_FP4_SCALES, OP_QUANTIZE_NVFP4_GROUPED = 7, 8, 9
 OP_KV_WRITE_FP8_PER_HEAD, OP_KV_WRITE_FP8_CHANNEL_ZP, OP_COL_AMAX = 10, 11, 12
+OP_ATTN_FP8_PAGED = 13
 SMOOTH_NONE, SMOOTH_DIVIDE, SMOOTH_MULTIPLY = 0, 1, 2
 
 if not os.path.exists(LIB):
@@ -60,6 +61,11 @@ class _Nvfp4Problem(ctypes.Structure):
 class _Nvfp4Tensor(ctypes.Structure):
     _fields_ = [("x", _P), ("rows", _I64), ("cols", _I64), ("codes", _P), ("scale_e4m3", _P),
                 ("global_scale", _P)]
+
+
+class _PagedKV(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scale", _P), ("v_scale", _P), ("page_stride", _I64),
+                ("num_pages", _I), ("page_size", _I), ("heads", _I), ("head_dim", _I)]
 
 
 _SIGS = {
@@ -93,6 +99,10 @@ _SIGS = {
     "qz_gemm_int8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "qz_gemm_fp8_block_quant": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "qz_gemm_nvfp4_quant": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "qz_block_tables": (_I, [_P, _P, _I, _I, _P, _I, _I64, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "qz_kv_append_fp8_paged": (_I, [_P, _P, _I, _I64, _I64, _I64, _P, ctypes.POINTER(_PagedKV), _P]),
+    "qz_attn_fp8_paged": (_I, [_P, _I64, _I64, _I, _P, _I, _I, ctypes.POINTER(_PagedKV), _P, _I, _I64, _P,
+                               ctypes.c_float, _I, _P, _I64, _P, _P, _SZ, _P]),
     "qz_gemm_mxfp4_quant": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -755,3 +765,137 @@ def qz_gemm_fp8_block_quant(qA, sA, qB, sB, Y=None, y_codes=None, y_scales=None,
             _arg(y_codes, "y_codes", d, 1, M * N), _arg(y_scales, "y_scales", d, torch.float32, M * (N // 128)))
     _check(lib.qz_gemm_fp8_block_quant(*args, M, N, K, _stream(stream)), "qz_gemm_fp8_block_quant")
     return y_codes, y_scales, Y
+
+
+# ------------------------------------------------------- paged FP8 KV cache
+
+class PagedKV:
+    """A paged FP8 KV cache: E4M3 codes [pages, heads, page_size, head_dim] (uint8) of K and of V
+    and one fp32 scale per (page, head) of each, all allocated by the caller. The pages of the
+    two code tensors may lie further apart than dense (one equal stride(0)), so K and V can share one
+    allocation. Made once with the cache; its tensors are checked here."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale):
+        if k_codes.dim() != 4 or k_codes.shape != v_codes.shape:
+            raise ValueError("k_codes and v_codes must be [pages, heads, page_size, head_dim] tensors of one shape")
+        n, h, p, d = k_codes.shape
+        dev = k_codes.get_device()
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            if t.get_device() != dev or t.element_size() != 1 or t.stride()[1:] != (p * d, d, 1):
+                raise ValueError(f"{name}: expected a 1-byte tensor on one device, dense within each page, got "
+                                 f"{t.dtype} with strides {tuple(t.stride())}")
+        stride = k_codes.stride(0) if n > 1 else h * p * d
+        if n > 1 and v_codes.stride(0) != stride:
+            raise ValueError("k_codes and v_codes must have the same stride between pages")
+        ks = _arg(k_scale, "k_scale", dev, torch.float32, n * h)
+        vs = _arg(v_scale, "v_scale", dev, torch.float32, n * h)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.head_dim = n, h, p, d
+        self.device = dev
+        self._c = _PagedKV(k_codes.data_ptr(), v_codes.data_ptr(), ks, vs, stride, n, p, h, d)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages, heads, page_size, head_dim, device=None):
+        """A cache of uninitialised pages."""
+        dev = torch.device("cuda", _device()) if device is None else device
+        codes = torch.empty((2, pages, heads, page_size, head_dim), dtype=torch.uint8, device=dev)
+        scales = torch.empty((2, pages, heads), dtype=torch.float32, device=dev)
+        return cls(codes[0], codes[1], scales[0], scales[1])
+
+
+def _table(t, name, dev):
+    if t.get_device() != dev or t.dtype is not torch.int32 or t.dim() != 2 or (t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a 2-D int32 tensor on cuda:{dev} with dense rows, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    rows, cols = t.shape
+    return t.data_ptr(), rows, cols, (t.stride(0) if rows > 1 else cols)
+
+
+def _rows3(t, name, dev, heads, head_dim):
+    """[tokens, heads, head_dim] with dense heads; returns the stride between tokens."""
+    if (t.dim() != 3 or t.get_device() != dev or (heads is not None and t.shape[1] != heads)
+            or t.shape[2] != head_dim):
+        raise ValueError(f"{name}: expected [tokens, {heads if heads is not None else 'heads'}, {head_dim}] on "
+                         f"cuda:{dev}, got {tuple(t.shape)}")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if t.numel() and (s2 != 1 or (h > 1 and s1 != d)):
+        raise ValueError(f"{name}: the heads of a token must be dense, got strides {(s0, s1, s2)}")
+    return s0 if n > 1 else h * d
+
+
+def qz_block_tables(ctx_lens, new_lens, block_table, free_pages, free_head, page_size: int, n_slots: int, kv_lens=None,
+                    cu_new=None, slot_map=None, positions=None, free_head_out=None, stream=None):
+    """Block tables and slot maps of one step on the GPU: pages from free_pages[free_head:] go to the
+    requests whose ctx_lens + new_lens tokens need them (block_table is updated in place). All
+    tensors int32. Returns (slot_map [n_slots], positions [n_slots], cu_new [B + 1], kv_lens [B],
+    free_head_out [1]); tokens of requests that could not be admitted have slot -1."""
+    d = _device()
+    tab, B, blocks, ld = _table(block_table, "block_table", d)
+    i32, dev = torch.int32, block_table.device
+    slot_map = torch.empty((n_slots,), dtype=i32, device=dev) if slot_map is None else slot_map
+    positions = torch.empty((n_slots,), dtype=i32, device=dev) if positions is None else positions
+    cu_new = torch.empty((B + 1,), dtype=i32, device=dev) if cu_new is None else cu_new
+    kv_lens = torch.empty((B,), dtype=i32, device=dev) if kv_lens is None else kv_lens
+    free_head_out = torch.empty((1,), dtype=i32, device=dev) if free_head_out is None else free_head_out
+    _check(lib.qz_block_tables(
+        _arg(ctx_lens, "ctx_lens", d, i32, B), _arg(new_lens, "new_lens", d, i32, B), B, page_size, tab, blocks, ld,
+        _arg(free_pages, "free_pages", d, i32), free_pages.numel(), _arg(free_head, "free_head", d, i32, 1),
+        _arg(kv_lens, "kv_lens", d, i32, B), _arg(cu_new, "cu_new", d, i32, B + 1),
+        _arg(slot_map, "slot_map", d, i32, n_slots), _arg(positions, "positions", d, i32, n_slots), n_slots,
+        _arg(free_head_out, "free_head_out", d, i32, 1), _stream(stream)), "qz_block_tables")
+    return slot_map, positions, cu_new, kv_lens, free_head_out
+
+
+def _on_cache(cache, d):
+    if cache.device != d:
+        raise ValueError(f"cache: expected a PagedKV on cuda:{d}, got one on "
+                         + ("cpu" if cache.device < 0 else f"cuda:{cache.device}"))
+
+
+def qz_kv_append_fp8_paged(k, v, slot_map, cache: PagedKV, stream=None):
+    """Quantize new tokens k, v [tokens, heads, head_dim] (fp32 or bf16; tokens may be strided, as
+    slices of a fused projection are) into the cache at slot_map [tokens] int32, with one scale
+    per (page, head). A page's older tokens are encoded anew where its scale grows."""
+    d = _device()
+    _on_cache(cache, d)
+    ldk = _rows3(k, "k", d, cache.heads, cache.head_dim)
+    ldv = _rows3(v, "v", d, cache.heads, cache.head_dim)
+    if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same number of tokens and dtype")
+    n = k.shape[0]
+    _check(lib.qz_kv_append_fp8_paged(k.data_ptr(), v.data_ptr(), _dtype_code(k), n, ldk, ldv,
+                                      _arg(slot_map, "slot_map", d, torch.int32, n), cache._ref, _stream(stream)),
+           "qz_kv_append_fp8_paged")
+
+
+def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int, scale: float, causal: bool = True,
+                      out=None, lse=None, ws=None, stream=None):
+    """Attention of q [tokens, heads_q, head_dim] (bf16; request b's tokens are cu_q[b]:cu_q[b+1], at
+    most max_q) over the first kv_lens[b] tokens of the cache pages block_table[b]. causal: the last
+    query of a request sees all its keys; otherwise every query does (cross attention). Returns
+    (out bf16 like q, lse); lse=True allocates fp32 [tokens, heads_q], None leaves it out."""
+    d = _device()
+    _on_cache(cache, d)
+    ldq = _rows3(q, "q", d, None, cache.head_dim)
+    tokens, hq, dim = q.shape
+    if q.dtype is not torch.bfloat16:
+        raise TypeError(f"qz_attn_fp8_paged takes bfloat16 queries, got {q.dtype}")
+    tab, B, blocks, ld = _table(block_table, "block_table", d)
+    if out is None:
+        out = torch.empty((tokens, hq, dim), dtype=torch.bfloat16, device=q.device)
+        ldo = hq * dim
+    else:
+        ldo = _rows3(out, "out", d, hq, dim)
+        if out.shape[0] != tokens or out.dtype is not torch.bfloat16:
+            raise ValueError(f"out: expected bfloat16 {(tokens, hq, dim)}, got {out.dtype} {tuple(out.shape)}")
+    if lse is True:
+        lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device)
+    args = (_arg(kv_lens, "kv_lens", d, torch.int32, B), float(scale), int(bool(causal)), out.data_ptr(), ldo,
+            _opt(lse, "lse", d, torch.float32, tokens * hq))
+    buf, nb = _ws(ws, qz_workspace_size(OP_ATTN_FP8_PAGED, max_q * (hq // cache.heads), dim), d)
+    _check(lib.qz_attn_fp8_paged(q.data_ptr(), ldq, tokens, hq, _arg(cu_q, "cu_q", d, torch.int32, B + 1), B, max_q,
+                                 cache._ref, tab, blocks, ld, *args, _ptr(buf), nb, _stream(stream)),
+           "qz_attn_fp8_paged")
+    return out, lse

@@ -86,7 +86,9 @@ typedef enum qz_op {
     QZ_OP_QUANTIZE_NVFP4_GROUPED = 9, /* d0 = tensor count                   */
     QZ_OP_KV_WRITE_FP8_PER_HEAD = 10, /* d0 = B*H, d1 = T*D                   */
     QZ_OP_KV_WRITE_FP8_CHANNEL_ZP = 11, /* d0 = B*H, d1 = T, d2 = D           */
-    QZ_OP_COL_AMAX = 12                 /* d0 = rows, d1 = cols               */
+    QZ_OP_COL_AMAX = 12,                /* d0 = rows, d1 = cols               */
+    QZ_OP_ATTN_FP8_PAGED = 13           /* d0 = query rows of the largest request per KV
+                                           head (max_q * heads_q / heads), d1 = head_dim */
 } qz_op;
 
 typedef enum qz_smooth_op {
@@ -499,6 +501,88 @@ qz_status qz_gemm_mxfp4_quant(const uint8_t* qA, const uint8_t* eA, const uint8_
 qz_status qz_gemm_nvfp4_noalloc(const uint8_t* qA, const uint8_t* sA, const float* gA,
                                 const uint8_t* qB, const uint8_t* sB, const float* gB,
                                 uint16_t* Y, int M, int N, int K, void* stream);
+
+/* ------------------------------------------------- paged FP8 KV cache
+ * A cache of pages of page_size tokens: E4M3 codes [num_pages, heads, page_size,
+ * head_dim] for K and for V and one fp32 scale per (page, head) of each
+ * ("量化部署实战", KV Cache 量化: FP8 codes with a scale per head; here per head
+ * and block of tokens). The value of a code is E4M3value(code) * scale. */
+typedef struct qz_paged_kv {
+    uint8_t* k_codes;         /* 16 B aligned */
+    uint8_t* v_codes;
+    float* k_scale;           /* [num_pages, heads], dense */
+    float* v_scale;
+    int64_t page_stride;      /* bytes from one page to the next in k_codes and in v_codes:
+                                 >= heads * page_size * head_dim, a multiple of 16 */
+    int num_pages;            /* num_pages * page_size < 2^31 */
+    int page_size;            /* 16, 32, 64 or 128 */
+    int heads;                /* KV heads, 1..32767 */
+    int head_dim;             /* 64 or 128 */
+} qz_paged_kv;
+
+/* Block tables and slot maps of one step, from the requests' lengths. Request b
+ * holds ctx_lens[b] tokens and gets new_lens[b] more (negative lengths count as
+ * 0). With have = ceil(ctx / page_size), want = ceil((ctx + new) / page_size) and
+ * need = want - have (0 where want > max_blocks: refused), pages are taken from
+ * free_pages in request order, from entry *free_head on: request b is admitted if
+ * want <= max_blocks and (need == 0 or *free_head + need[0] + ... + need[b] <= n_free).
+ *   block_table[b, have .. want-1] <- the pages taken (admitted requests; the rest
+ *     of the table is left as it is; row stride ld_table >= max_blocks)
+ *   cu_new[B + 1]   exclusive sums of new_lens (tokens of a step are packed)
+ *   kv_lens[b]      ctx + new, or ctx where refused
+ *   slot_map[t]     page * page_size + offset of token t, -1 where its request was
+ *                   refused and for t past the last token (padding of a fixed-size step)
+ *   positions[t]    position of token t in its request (nullable; 0 in the padding)
+ *   free_head_out   the first entry of free_pages still free
+ * n_slots: entries of slot_map and positions; tokens past it are not mapped, but
+ * their pages are taken. Sums of lengths and of pages must stay below 2^31. Apart
+ * from block_table, outputs must not overlap inputs. B = 0 writes cu_new[0],
+ * free_head_out and the padding. Shapes: page_size 16, 32, 64 or 128. */
+qz_status qz_block_tables(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size,
+                          int32_t* block_table, int max_blocks, int64_t ld_table,
+                          const int32_t* free_pages, int n_free, const int32_t* free_head,
+                          int32_t* kv_lens, int32_t* cu_new, int32_t* slot_map, int32_t* positions, int n_slots,
+                          int32_t* free_head_out, void* stream);
+
+/* Write of new tokens into the cache. k, v: [tokens, heads, head_dim] of type xt,
+ * rows ldk and ldv elements apart (>= heads * head_dim; the heads of a token dense).
+ * slot_map[t]: token t's slot, as qz_block_tables gives it; slots outside the cache
+ * are skipped. The tokens of a page follow one another in slot_map, and no page is
+ * named by two such runs. Per page and head, for K and for V:
+ *   f = max(amax over the new tokens, 1e-12) / 448
+ *   first new offset 0: s = f; otherwise s = max(scale, f), and where that is larger
+ *   than scale the older codes c (offsets below it) become E4M3(clamp(x / s)) of
+ *   x = fl(E4M3value(c) * scale), the value they stood for
+ *   code = E4M3(clamp(x / s, +-448)); scale = s
+ * so a page's values never saturate whatever order they came in. Alignment: k, v 16 B,
+ * ldk and ldv multiples of 16 bytes. No workspace. tokens == 0 is a no-op. */
+qz_status qz_kv_append_fp8_paged(const void* k, const void* v, qz_dtype xt, int64_t tokens, int64_t ldk, int64_t ldv,
+                                 const int32_t* slot_map, const qz_paged_kv* cache, void* stream);
+
+/* Attention over the cache. Tokens cu_q[b] .. cu_q[b+1]-1 of q are request b's, its
+ * keys and values the first kv_lens[b] tokens of the pages block_table[b, :]. Query
+ * head a reads KV head a / (heads_q / heads). With n = cu_q[b+1] - cu_q[b], L = kv_lens[b]:
+ *   x[i, j] = sm_scale * sum_d q[i, d] * K[j, d]
+ *   seen: j < L, and for causal j <= L - n + i (the last query sees every key)
+ *   O[i] = sum_j softmax_j(x[i, j]) V[j];  lse[i] = ln sum_j exp(x[i, j])
+ * A row that sees nothing gives O = 0 and lse = -inf. Not causal: a cross
+ * attention to states of another length. Numerics: q enters as two E4M3 parts whose
+ * sum keeps 8 significant bits (exact for elements above 2^-10 of their row's amax),
+ * sums in fp32; the probabilities are rounded to 8 significant bits or more before
+ * they meet V; O is rounded once to bf16.
+ * q: bf16 [tokens, heads_q, head_dim], rows ldq elements apart; out: bf16, rows ldo
+ * apart; lse: nullable fp32 [tokens, heads_q]. max_q: the largest n; longer requests
+ * are cut off there. Entries of block_table past a request's pages are not read;
+ * entries outside the cache count as keys that are not seen. What lies in a page
+ * behind the last token may hold any codes. Inf and NaN in q or a scale reach their
+ * own request's rows only.
+ * Shapes: heads_q % heads == 0, heads_q / heads <= 256, max_blocks * page_size < 2^31.
+ * Alignment: q, out 16 B, ldq, ldo multiples of 8.
+ * ws: qz_workspace_size(QZ_OP_ATTN_FP8_PAGED, max_q * heads_q / heads, head_dim, 0). */
+qz_status qz_attn_fp8_paged(const uint16_t* q, int64_t ldq, int64_t tokens, int heads_q, const int32_t* cu_q, int B,
+                            int max_q, const qz_paged_kv* cache, const int32_t* block_table, int max_blocks,
+                            int64_t ld_table, const int32_t* kv_lens, float sm_scale, int causal, uint16_t* out,
+                            int64_t ldo, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
