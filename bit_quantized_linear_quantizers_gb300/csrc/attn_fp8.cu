@@ -16,7 +16,7 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32)
-attn_simple_kernel(const AttnArgs a, int shift) {
+attn_simple_kernel(const AttnArgs a, int shift, int min_rows) {
     constexpr int C = D / 32;                     // channels per lane
     pdl_wait();
     const int64_t t = blockIdx.x;
@@ -27,7 +27,7 @@ attn_simple_kernel(const AttnArgs a, int shift) {
         if (__ldg(a.cu_q + mid) <= t) lo = mid; else hi = mid - 1;
     }
     const int n = min(__ldg(a.cu_q + lo + 1) - __ldg(a.cu_q + lo), a.max_q), i = (int)(t - __ldg(a.cu_q + lo));
-    if (i < 0 || i >= n) return;
+    if (i < 0 || i >= n || n * (a.heads_q / a.kv.heads) < min_rows) return;
     const int L = (int)min((int64_t)max(__ldg(a.kv_lens + lo), 0), (int64_t)a.max_blocks << shift);
     const int seen = a.causal ? min(L, max(L - n + i + 1, 0)) : L;
     const int G = a.heads_q / a.kv.heads, mask = (1 << shift) - 1;
@@ -67,12 +67,16 @@ attn_simple_kernel(const AttnArgs a, int shift) {
 
 } // namespace
 
-size_t ws_attn_paged(int64_t, int64_t) { return 0; }
+constexpr int kDecodeRows = 64;                   // rows per KV head up to which a request takes the decode kernel
 
-qz_status attn_paged_launch(const AttnArgs& a, void*, cudaStream_t st) {
+size_t ws_attn_paged(int64_t, int64_t) { return ws_attn_decode(); }
+
+qz_status attn_paged_launch(const AttnArgs& a, void* ws, cudaStream_t st) {
+    QZ_TRY(attn_decode_launch(a, kDecodeRows, ws, st));
+    if ((int64_t)a.max_q * (a.heads_q / a.kv.heads) <= kDecodeRows) return QZ_OK;
     const int P = a.kv.page_size, shift = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
     auto* fn = a.kv.head_dim == 64 ? attn_simple_kernel<64> : attn_simple_kernel<128>;
-    return launch_pdl(fn, dim3((unsigned)a.tokens, a.kv.heads), dim3(kWarps * 32), 0, st, a, shift);
+    return launch_pdl(fn, dim3((unsigned)a.tokens, a.kv.heads), dim3(kWarps * 32), 0, st, a, shift, kDecodeRows + 1);
 }
 
 } // namespace qz

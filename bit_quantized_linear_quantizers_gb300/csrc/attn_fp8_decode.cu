@@ -1,0 +1,772 @@
+// attn_fp8_decode.cu -- attention over the paged FP8 KV cache for few query rows
+// per KV head (single tokens, a few tokens each): the keys and values are read
+// once, so HBM is the bound.
+//
+// The codes go into the FP8 tensor products as stored. A bf16 query is the sum of
+// two E4M3 numbers, hi = E4M3(q) and lo = E4M3(q - hi), 4 + 4 significant bits,
+// after its row is scaled by a power of two that brings the row's amax into
+// [128, 256): exact for elements above 2^-10 of the amax, off by at most 2^-17 of
+// the amax below (steps of E4M3's subnormals). The probabilities are split the
+// same way, so nothing widens the cache. With up to 8 query rows per KV head, hi
+// sits in rows 0-7 of the 16-row product and lo in rows 8-15: one
+// mma.sync.m16n8k32 does both (measured 1.26 cycles per SM, against 2.0 for the
+// bf16 form at half the depth).
+//
+// The value scale of a page goes into the exponent instead of into V:
+//   t_j = x_j log2(e) + log2 sv_j,  m = max t,  p_j = 2^(t_j - m + 8)
+//   O = sum_j p_j c_j,  l = sum_j p_j / sv_j,  result O / l,
+// since p_j = 2^(x_j log2 e) sv_j up to a factor common to O and l. p lies in
+// (0, 256] and its two parts step by 2^-9 at the finest, so p keeps 8 bits down to 2^-9 of
+// its maximum and steps of 2^-17 of it below. m, l and O are fp32.
+//
+// Work split: units of 32 keys of one (request, KV head, row tile), laid end to
+// end over all requests and cut into equal shares, one CTA of 8 warps per SM. Each
+// warp takes every eighth unit of the CTA's share with a private ring of TMA
+// stages (3 x 8 KB in flight per warp: 192 KB per SM, against ~45 KB that the
+// latency asks for), so no warp waits for another inside a share. At the end of a
+// (request, head) the eight states join in shared memory; what spans several
+// CTAs is joined by a second, small launch in a fixed order.
+#include "qz_internal.cuh"
+#include "qz_paged.cuh"
+#include "qz_tc.cuh"
+
+#include <algorithm>
+
+namespace qz {
+
+namespace {
+
+__device__ unsigned int g_attn_decode_err;
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kKeys = 32;                         // keys of a unit
+constexpr int kStages = 3;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kPShift = 8.0f;                   // p = 2^(t - m + 8)
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two values as E4M3 parts: hi = E4M3(x), lo = E4M3(x - hi); 16 bits each. The
+// f16 step in between keeps 11 bits (the values lie in [-256, 256]).
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    uint32_t h, back;
+    uint16_t e, f;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(h));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(e));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(back));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(f) : "r"(h));
+    hi = e;
+    lo = f;
+}
+
+// Four values -> one register of each part (value i in byte i).
+__device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
+    uint32_t ha, la, hb, lb;
+    split2(x0, x1, ha, la);
+    split2(x2, x3, hb, lb);
+    hi = ha | hb << 16;
+    lo = la | lb << 16;
+}
+
+// 4 x 4 byte transpose: out[i] holds byte i of a, b, c, d in that order.
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&out)[4]) {
+    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+    out[0] = __byte_perm(ab0, cd0, 0x5410);
+    out[1] = __byte_perm(ab0, cd0, 0x7632);
+    out[2] = __byte_perm(ab1, cd1, 0x5410);
+    out[3] = __byte_perm(ab1, cd1, 0x7632);
+}
+
+// 3-D TMA load of a box (channels, rows, page).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+struct DecodeParams {
+    CUtensorMap tm_k, tm_v;                       // codes as (head_dim, heads * page_size, num_pages)
+    AttnArgs a;
+    int shift;                                    // log2 page_size
+    int max_rows;                                 // requests with more rows per KV head are not taken
+    int* head;                                    // [CTAs][4]: what the CTA left for the joining launch
+    float* part;                                  // [CTAs][2] partial states
+};
+
+// A request's part of the work: rows (queries x heads of the group), keys, units.
+struct Req {
+    int q0, n, L, tiles, subs;                    // first token, tokens, keys, row tiles, units per (head, tile)
+};
+
+template <int R>
+__device__ __forceinline__ Req load_req(const DecodeParams& P, int b, int G) {
+    Req r;
+    r.q0 = __ldg(P.a.cu_q + b);
+    r.n = min(__ldg(P.a.cu_q + b + 1) - r.q0, P.a.max_q);
+    r.n = (int)min((int64_t)r.n, P.a.tokens - r.q0);
+    if (r.n < 0 || r.q0 < 0) r.n = 0;
+    r.L = (int)min((int64_t)max(__ldg(P.a.kv_lens + b), 0), (int64_t)P.a.max_blocks << P.shift);
+    const int64_t rows = (int64_t)r.n * G;
+    r.tiles = rows > P.max_rows ? 0 : (int)((rows + R - 1) / R);
+    r.subs = max((r.L + kKeys - 1) / kKeys, 1);   // a request without keys still writes its rows
+    return r;
+}
+
+// The walk over the items (request, head, row tile) of a CTA's share.
+template <int R>
+struct Cursor {
+    int b, h, tile;
+    Req r;
+    __device__ void next(const DecodeParams& P, int G) {
+        if (++tile < r.tiles) return;
+        tile = 0;
+        if (++h < P.a.kv.heads) return;
+        h = 0;
+        do {
+            if (++b >= P.a.B) return;
+            r = load_req<R>(P, b, G);
+        } while (r.tiles == 0);
+    }
+};
+
+template <int D, int R>
+struct DecodeLayout {
+    static constexpr int HALF = kKeys * D;                          // bytes of K (or V) of a unit
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int RING = kWarps * kStages * STAGE;
+    static constexpr int JOIN_F = (kWarps / 2) * R * D;             // floats
+    static constexpr int META = RING + JOIN_F * 4;
+    static constexpr int SMEM = META + 1792 + 1024;                 // barriers, states, page rings; alignment
+    static constexpr int PART = R * D + 2 * R;                      // floats of a partial state
+};
+
+// One value per (row, channel) of the state, unnormalised, with m and l, goes to
+// the output; used by the main kernel and by the joining one.
+__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int hq, int D, int d0, const float* o, int n,
+                                          float m, float l) {
+    const float r = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+    uint16_t* out = a.out + token * a.ldo + (int64_t)hq * D + d0;
+#pragma unroll
+    for (int i = 0; i < n; i += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[i + 2 * j] * r, o[i + 2 * j + 1] * r);
+            w[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (a.lse && d0 == 0) a.lse[token * a.heads_q + hq] = l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_decode_kernel(const __grid_constant__ DecodeParams P) {
+    using Lay = DecodeLayout<D, R>;
+    constexpr int KS = D / 32;                    // 32-deep steps of q k
+    constexpr int NT = D / 8;                     // 8-channel tiles of O
+    constexpr int RR = R / 8;                     // rows of a thread
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* join = reinterpret_cast<float*>(smem + Lay::RING);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::META);                   // [warp][stage]
+    float* s_m = reinterpret_cast<float*>(smem + Lay::META + 256);                    // [warp][R]
+    float* s_l = s_m + kWarps * 16;
+    int64_t* s_sum = reinterpret_cast<int64_t*>(s_l + kWarps * 16);                   // [warp]
+    int* s_start = reinterpret_cast<int*>(s_sum + kWarps + 1);                        // request, unit inside it
+    int* s_page = s_start + 8;                                                        // [warp][4][3] two pages and the head of units to come
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int G = P.a.heads_q / P.a.kv.heads;
+    if (lane == 0) {
+        for (int s = 0; s < kStages; s++) mbar_init(smem_u32(bars + warp * kStages + s), 1);
+        fence_barrier_init();
+        if (warp == 0) {
+            prefetch_tmap(&P.tm_k);
+            prefetch_tmap(&P.tm_v);
+        }
+    }
+    pdl_wait();
+    pdl_trigger();                                // the joining launch may come up; it waits for this one's end
+
+    // ---- the CTA's share: all units counted, then the request that holds its first one
+    auto units_of = [&](int b) -> int64_t {
+        if (b >= P.a.B) return 0;
+        const Req r = load_req<R>(P, b, G);
+        return (int64_t)P.a.kv.heads * r.tiles * r.subs;
+    };
+    int64_t sum = 0;
+    for (int b = threadIdx.x; b < P.a.B; b += kThreads) sum += units_of(b);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kWarps; w++) total += s_sum[w];
+    const int64_t per = max((int64_t)kWarps, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
+    int* header = P.head + blockIdx.x * 4;
+    if (u0 >= u1) {
+        if (threadIdx.x == 0) header[0] = header[1] = header[2] = -1;
+        return;
+    }
+    int64_t before = 0;
+    for (int b0 = 0; b0 < P.a.B; b0 += kThreads) {
+        int64_t v = units_of(b0 + threadIdx.x);
+        const int64_t own = v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        __syncthreads();
+        if (lane == 31) s_sum[warp] = v;
+        __syncthreads();
+        int64_t all = 0, base = before;
+        for (int w = 0; w < kWarps; w++) {
+            if (w < warp) base += s_sum[w];
+            all += s_sum[w];
+        }
+        const int64_t first = base + v - own;
+        if (u0 >= first && u0 < first + own) {
+            s_start[0] = b0 + threadIdx.x;
+            *reinterpret_cast<int64_t*>(s_start + 2) = u0 - first;
+        }
+        before += all;
+        if (before > u0) break;                   // uniform
+    }
+    __syncthreads();
+
+    // ---- two walks over the share: `ahead` looks up pages and issues copies, `cur` computes
+    Cursor<R> cur;
+    cur.b = s_start[0];
+    cur.r = load_req<R>(P, cur.b, G);
+    const int64_t inside = *reinterpret_cast<int64_t*>(s_start + 2);
+    const int item0 = (int)(inside / cur.r.subs);
+    cur.h = item0 / cur.r.tiles;
+    cur.tile = item0 % cur.r.tiles;
+    const int sub0 = (int)(inside % cur.r.subs);
+    const int share = (int)(u1 - u0);             // units of the CTA (a share of 2^31 units would be 2^36 keys)
+    Cursor<R> ahead = cur;
+    int ahead_base = -sub0;                       // unit of the share at which ahead's item begins
+    int looked = warp, issued = warp;             // next units of this warp to look up and to issue (share index)
+
+    int* pages = s_page + warp * 12;              // ring of 4 units
+    const uint32_t ring = smem_u32(smem) + warp * kStages * Lay::STAGE;
+    const uint32_t bar0 = smem_u32(bars + warp * kStages);
+    const int page_keys = 1 << P.shift;
+    bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
+    int dead_at = -1;
+
+    // Pages of the warp's next unit: from the table into the ring (one unit ahead of its issue).
+    struct Look { int p0, p1, h, key; };
+    Look look;                                    // looked up, not yet issued
+    auto look_up = [&]() {                        // uniform over the warp
+        look.p0 = look.p1 = -1;
+        if (looked < share) {
+            while (looked >= ahead_base + ahead.r.subs) {
+                ahead_base += ahead.r.subs;
+                ahead.next(P, G);
+            }
+            look.key = (looked - ahead_base) * kKeys;
+            look.h = ahead.h;
+            const int32_t* row = P.a.block_table + (int64_t)ahead.b * P.a.ld_table + (look.key >> P.shift);
+            if (look.key < ahead.r.L) look.p0 = __ldg(row);
+            if (P.shift == 4 && look.key + 16 < ahead.r.L) look.p1 = __ldg(row + 1);
+        }
+    };
+    auto issue = [&]() {                          // the unit that `look` holds, into its stage
+        if (issued < share) {
+            const int k = (issued - warp) / kWarps, st = k % kStages;
+            const int p0 = look.p0 >= 0 && look.p0 < P.a.kv.num_pages ? look.p0 : -1;
+            const int p1 = P.shift == 4 ? (look.p1 >= 0 && look.p1 < P.a.kv.num_pages ? look.p1 : -1) : p0;
+            if (lane == 0) {
+                pages[(k & 3) * 3] = p0;
+                pages[(k & 3) * 3 + 1] = p1;
+                pages[(k & 3) * 3 + 2] = look.h;
+                if (!dead) {
+                    const uint32_t dst = ring + st * Lay::STAGE, bar = bar0 + st * 8;
+                    const int y = (look.h << P.shift) + (look.key & (page_keys - 1));
+                    if (P.shift == 4) {
+                        mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * Lay::HALF);
+                        if (p0 >= 0) {
+                            tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
+                            tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
+                        }
+                        if (p1 >= 0) {
+                            tma_load_3d(dst + Lay::HALF / 2, &P.tm_k, 0, y, p1, bar);
+                            tma_load_3d(dst + Lay::HALF + Lay::HALF / 2, &P.tm_v, 0, y, p1, bar);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(bar, (p0 >= 0) * Lay::STAGE);
+                        if (p0 >= 0) {
+                            tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
+                            tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        issued += kWarps;
+    };
+    look_up();
+#pragma unroll 1
+    for (int s = 0; s < kStages; s++) {
+        issue();
+        looked += kWarps;
+        look_up();
+    }
+
+    const float c0 = fabsf(P.a.sm_scale) * kLog2e;
+    int unit = 0;                                 // of the share, at the item's first unit here
+    int kdone = 0;                                // units that this warp has computed
+    int sub = sub0;
+    if (threadIdx.x == 0) {
+        header[0] = -1;
+        header[1] = 0;
+        header[2] = -1;
+    }
+    // pages and scales of the warp's next unit, one unit ahead
+    int p0 = -1, p1 = -1;
+    float ks0 = 0.0f, ks1 = 0.0f, vs0 = 1.0f, vs1 = 1.0f;
+    auto load_scales = [&]() {
+        if (warp + kdone * kWarps >= share) return;
+        const int* e = pages + (kdone & 3) * 3;
+        p0 = e[0];
+        p1 = e[1];
+        if (p0 >= 0) {
+            const int64_t i = (int64_t)p0 * P.a.kv.heads + e[2];
+            ks0 = __ldg(P.a.kv.k_scale + i);
+            vs0 = __ldg(P.a.kv.v_scale + i);
+        }
+        if (P.shift == 4 && p1 >= 0) {
+            const int64_t i = (int64_t)p1 * P.a.kv.heads + e[2];
+            ks1 = __ldg(P.a.kv.k_scale + i);
+            vs1 = __ldg(P.a.kv.v_scale + i);
+        }
+    };
+    load_scales();
+
+    while (unit < share) {
+        const int here = min(cur.r.subs - sub, share - unit);          // units of this item in this share
+        // ---- q of this item: rows g (and g + 8), two parts each, in the order the keys are read
+        uint32_t qf[RR][KS][4];                   // R = 8: hi b0, lo b0, hi b1, lo b1; R = 16: per row hi b0, hi b1, lo b0, lo b1
+        float crow[RR];
+        int seen[RR];                             // keys that the row sees
+#pragma unroll
+        for (int rr = 0; rr < RR; rr++) {
+            const int row = cur.tile * R + rr * 8 + g, i = row / G, a = row - i * G;
+            const bool there = i < cur.r.n;
+            const uint16_t* src = P.a.q + (int64_t)(cur.r.q0 + i) * P.a.ldq + (int64_t)(cur.h * G + a) * D + t * 16;
+            float v[D / 4];
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 32; j++) {    // 16 bytes: channels t*16 + (j & 1)*8 of the 64-channel half j >> 1
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (there) w = __ldg(reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + (j & 1) * 8));
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    v[j * 8 + 2 * e] = __uint_as_float(x[e] << 16);
+                    v[j * 8 + 2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < D / 4; e++) m = fmaxf(m, fabsf(v[e]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // 2^(7 - floor(log2 amax)): from the exponent field, within the normal range
+            const int ex = (int)(__float_as_uint(m) >> 23) & 255;
+            const int se = min(max(134 + 127 - ex, 1), 240);
+            const float up = m > 0.0f ? __uint_as_float((uint32_t)se << 23) : 1.0f;
+            const float down = m > 0.0f ? __uint_as_float((uint32_t)max(254 - se, 1) << 23) : 1.0f;
+            crow[rr] = c0 * down;
+            const float sgn = P.a.sm_scale < 0.0f ? -up : up;
+            seen[rr] = !there ? 0 : P.a.causal ? min(max(cur.r.L - cur.r.n + i + 1, 0), cur.r.L) : cur.r.L;
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                uint32_t h0, l0, h1, l1;
+                split4(v[8 * s] * sgn, v[8 * s + 1] * sgn, v[8 * s + 2] * sgn, v[8 * s + 3] * sgn, h0, l0);
+                split4(v[8 * s + 4] * sgn, v[8 * s + 5] * sgn, v[8 * s + 6] * sgn, v[8 * s + 7] * sgn, h1, l1);
+                if (RR == 1) {
+                    qf[rr][s][0] = h0; qf[rr][s][1] = l0; qf[rr][s][2] = h1; qf[rr][s][3] = l1;
+                } else {
+                    qf[rr][s][0] = h0; qf[rr][s][1] = h1; qf[rr][s][2] = l0; qf[rr][s][3] = l1;
+                }
+            }
+        }
+        float o[NT][4];
+        float m[RR], l[RR];
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[j][e] = 0.0f;
+#pragma unroll
+        for (int rr = 0; rr < RR; rr++) {
+            m[rr] = -INFINITY;
+            l[rr] = 0.0f;
+        }
+
+        // ---- this warp's units of the item: share indices = warp mod 8
+        int first = unit + ((warp - unit) & (kWarps - 1));
+#pragma unroll 1
+        for (int u = first; u < unit + here; u += kWarps) {
+            const int st = kdone % kStages, key0 = (sub + (u - unit)) * kKeys;
+            const float k0 = ks0, k1 = P.shift == 4 ? ks1 : ks0;
+            const float v0 = fmaxf(vs0, 1.2e-38f), v1 = P.shift == 4 ? fmaxf(vs1, 1.2e-38f) : v0;
+            if (!dead && !mbar_wait<false>(bar0 + st * 8, (kdone / kStages) & 1, &g_attn_decode_err)) dead = true;
+            if (__any_sync(0xffffffffu, dead) && dead_at < 0) dead = true, dead_at = kdone;
+            const uint8_t* kt = smem + (warp * kStages + st) * Lay::STAGE;
+            const uint8_t* vt = kt + Lay::HALF;
+
+            // S = q K^T: 4 tiles of 8 keys
+            float s[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[j][e] = 0.0f;
+                uint32_t w[D / 16];
+                const int r = j * 8 + g;
+#pragma unroll
+                for (int c = 0; c < D / 64; c++) {
+                    const int ch = D == 128 ? ((t + 4 * c) ^ g) : (t ^ ((r >> 1) & 3));
+                    const uint4 x = *reinterpret_cast<const uint4*>(kt + r * D + ch * 16);
+                    w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
+                }
+#pragma unroll
+                for (int k = 0; k < KS; k++) {
+                    if (RR == 1) {
+                        mma_e4m3(s[j], qf[0][k][0], qf[0][k][1], qf[0][k][2], qf[0][k][3], w[2 * k], w[2 * k + 1]);
+                    } else {
+                        mma_e4m3(s[j], qf[0][k][0], qf[RR - 1][k][0], qf[0][k][1], qf[RR - 1][k][1], w[2 * k], w[2 * k + 1]);
+                        mma_e4m3(s[j], qf[0][k][2], qf[RR - 1][k][2], qf[0][k][3], qf[RR - 1][k][3], w[2 * k], w[2 * k + 1]);
+                    }
+                }
+            }
+            // scores of the row(s): x[rr][2 j + e] = key 8 j + 2 t + e
+            float x[RR][8];
+            const float lv0 = __log2f(v0), lv1 = __log2f(v1);
+#pragma unroll
+            for (int rr = 0; rr < RR; rr++) {
+                const float a0 = crow[rr] * k0, a1 = crow[rr] * k1;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float raw = RR == 1 ? s[j][e] + s[j][2 + e] : s[j][2 * rr + e];
+                        x[rr][2 * j + e] = fmaf(raw, j < 2 ? a0 : a1, j < 2 ? lv0 : lv1);
+                    }
+            }
+            const int live = cur.r.L - key0;      // keys of the unit that exist
+            const bool edge = live < kKeys || p0 < 0 || p1 < 0 || (P.a.causal && key0 + kKeys > cur.r.L - cur.r.n + 1);
+            if (edge) {
+#pragma unroll
+                for (int rr = 0; rr < RR; rr++) {
+                    const int lim = seen[rr] - key0;
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+                            if (8 * j + 2 * t + e >= lim || (j < 2 ? p0 : p1) < 0) x[rr][2 * j + e] = -INFINITY;
+                }
+            }
+            uint32_t ph[RR][2], pl[RR][2];
+            const float iv0 = __frcp_rn(v0), iv1 = __frcp_rn(v1);
+            float f[RR];
+            bool moved = false;
+#pragma unroll
+            for (int rr = 0; rr < RR; rr++) {
+                float mx = x[rr][0];
+#pragma unroll
+                for (int e = 1; e < 8; e++) mx = fmaxf(mx, x[rr][e]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m2 = fmaxf(m[rr], mx);
+                moved |= m2 != m[rr];
+                f[rr] = m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - m2);
+                m[rr] = m2;
+                const float off = m2 == -INFINITY ? 0.0f : kPShift - m2;        // nothing seen yet: every p is 0
+                float p[8];
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    p[e] = ex2(x[rr][e] + off);
+                    p[4 + e] = ex2(x[rr][4 + e] + off);
+                    s0 += p[e];
+                    s1 += p[4 + e];
+                }
+                l[rr] = fmaf(s1, iv1, fmaf(s0, iv0, l[rr] * f[rr]));
+                split4(p[0], p[1], p[2], p[3], ph[rr][0], pl[rr][0]);
+                split4(p[4], p[5], p[6], p[7], ph[rr][1], pl[rr][1]);
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+                // the rows of o: RR = 1: c0, c1 (hi part) and c2, c3 (lo part) are both row g
+#pragma unroll
+                for (int j = 0; j < NT; j++) {
+                    o[j][0] *= f[0]; o[j][1] *= f[0];
+                    o[j][2] *= f[RR - 1]; o[j][3] *= f[RR - 1];
+                }
+            }
+            // O += P V: slot k = 4t + i of the first half is key {2t, 2t+1, 8+2t, 9+2t}[i], of the second + 16
+#pragma unroll
+            for (int w = 0; w < D / 64; w++) {    // 8 bytes of the thread's D / 8 channels at a time
+                uint2 vv[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {     // i = 2 jj + e: key 8 jj + 2 t + e
+                    const int r = (i >> 1) * 8 + 2 * t + (i & 1);
+                    const int ch = D == 128 ? (g ^ (r & 7)) : ((g >> 1) ^ ((r >> 1) & 3));
+                    vv[i] = *reinterpret_cast<const uint2*>(vt + r * D + ch * 16 + (D == 128 ? 8 * w : 8 * (g & 1)));
+                }
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) { // never-written bytes may be NaN codes: 0 * NaN is no 0
+                        const int r = (i >> 1) * 8 + 2 * t + (i & 1);
+                        if (r >= live || (i < 4 ? p0 : p1) < 0) vv[i] = make_uint2(0u, 0u);
+                    }
+                }
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    uint32_t b0[4], b1[4];
+                    transpose4(half ? vv[0].y : vv[0].x, half ? vv[1].y : vv[1].x, half ? vv[2].y : vv[2].x, half ? vv[3].y : vv[3].x, b0);
+                    transpose4(half ? vv[4].y : vv[4].x, half ? vv[5].y : vv[5].x, half ? vv[6].y : vv[6].x, half ? vv[7].y : vv[7].x, b1);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int j = w * 8 + half * 4 + e;
+                        if (RR == 1) {
+                            mma_e4m3(o[j], ph[0][0], pl[0][0], ph[0][1], pl[0][1], b0[e], b1[e]);
+                        } else {
+                            mma_e4m3(o[j], ph[0][0], ph[RR - 1][0], ph[0][1], ph[RR - 1][1], b0[e], b1[e]);
+                            mma_e4m3(o[j], pl[0][0], pl[RR - 1][0], pl[0][1], pl[RR - 1][1], b0[e], b1[e]);
+                        }
+                    }
+                }
+            }
+            kdone++;
+            __syncwarp();                         // the stage has been read
+            load_scales();                        // of the next unit, whose pages are in the ring
+            issue();
+            looked += kWarps;
+            look_up();
+        }
+
+        // ---- the item's end in this share: join the warps
+#pragma unroll
+        for (int rr = 0; rr < RR; rr++) {
+            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
+            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
+            if (t == 0) {
+                s_m[warp * 16 + rr * 8 + g] = m[rr];
+                s_l[warp * 16 + rr * 8 + g] = l[rr];
+            }
+        }
+        __syncthreads();
+        float mt[RR], lt[RR], fw[RR];
+#pragma unroll
+        for (int rr = 0; rr < RR; rr++) {
+            mt[rr] = -INFINITY;
+            lt[rr] = 0.0f;
+            for (int w = 0; w < kWarps; w++) mt[rr] = fmaxf(mt[rr], s_m[w * 16 + rr * 8 + g]);
+            for (int w = 0; w < kWarps; w++) {
+                const float mw = s_m[w * 16 + rr * 8 + g];
+                const float lw = s_l[w * 16 + rr * 8 + g];
+                lt[rr] += mw == -INFINITY && lw == 0.0f ? 0.0f : lw * ex2(mw - mt[rr]);
+            }
+            fw[rr] = m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - mt[rr]);
+        }
+        // channel c D/8 + j of O is column c of tile j
+        float v[RR][2][NT];                       // [row][column 2t + e][j]
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                if (RR == 1) {
+                    v[0][e][j] = (o[j][e] + o[j][2 + e]) * fw[0];
+                } else {
+                    v[0][e][j] = o[j][e] * fw[0];
+                    v[RR - 1][e][j] = o[j][2 + e] * fw[RR - 1];
+                }
+            }
+#pragma unroll 1
+        for (int half = kWarps / 2; half > 0; half >>= 1) {
+            // a thread's values one float4 apart from its neighbours': no bank conflicts
+            if (warp >= half && warp < 2 * half) {
+                float4* dst = reinterpret_cast<float4*>(join + (warp - half) * R * D);
+#pragma unroll
+                for (int rr = 0; rr < RR; rr++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int q = 0; q < NT / 4; q++)
+                            dst[((rr * 2 + e) * (NT / 4) + q) * 32 + lane] = make_float4(v[rr][e][4 * q], v[rr][e][4 * q + 1],
+                                                                                         v[rr][e][4 * q + 2], v[rr][e][4 * q + 3]);
+            }
+            __syncthreads();
+            if (warp < half) {
+                const float4* src = reinterpret_cast<const float4*>(join + warp * R * D);
+#pragma unroll
+                for (int rr = 0; rr < RR; rr++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int q = 0; q < NT / 4; q++) {
+                            const float4 x = src[((rr * 2 + e) * (NT / 4) + q) * 32 + lane];
+                            v[rr][e][4 * q] += x.x; v[rr][e][4 * q + 1] += x.y;
+                            v[rr][e][4 * q + 2] += x.z; v[rr][e][4 * q + 3] += x.w;
+                        }
+            }
+            __syncthreads();
+        }
+        if (warp == 0) {
+            const bool begins = sub == 0, ends = sub + here == cur.r.subs;
+            if (begins && ends) {
+#pragma unroll
+                for (int rr = 0; rr < RR; rr++) {
+                    const int row = cur.tile * R + rr * 8 + g, i = row / G, a = row - i * G;
+                    if (i < cur.r.n) {
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+                            write_row(P.a, cur.r.q0 + i, cur.h * G + a, D, (2 * t + e) * NT, v[rr][e], NT, mt[rr], lt[rr]);
+                    }
+                }
+            } else {
+                const int slot = begins ? 1 : 0;
+                float* dst = P.part + ((int64_t)blockIdx.x * 2 + slot) * Lay::PART;
+#pragma unroll
+                for (int rr = 0; rr < RR; rr++) {
+                    const int row = rr * 8 + g;
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int q = 0; q < NT / 4; q++)
+                            reinterpret_cast<float4*>(dst + row * D + (2 * t + e) * NT)[q] =
+                                make_float4(v[rr][e][4 * q], v[rr][e][4 * q + 1], v[rr][e][4 * q + 2], v[rr][e][4 * q + 3]);
+                    if (t == 0) {
+                        dst[R * D + row] = mt[rr];
+                        dst[R * D + R + row] = lt[rr];
+                    }
+                }
+                if (lane == 0) {
+                    if (begins) {                 // the joining launch starts here
+                        header[2] = cur.b;
+                        header[3] = cur.h * cur.r.tiles + cur.tile;
+                    } else {
+                        header[0] = cur.b;
+                        header[1] = !ends;        // goes on in the next CTA
+                    }
+                }
+            }
+        }
+        unit += here;
+        sub = 0;
+        if (unit < share) cur.next(P, G);
+    }
+    // copies still in flight (a wait that gave up): their stages must not outlive the CTA
+    if (dead)
+        for (int k = dead_at; k < dead_at + kStages && warp + k * kWarps < share; k++)
+            mbar_wait(bar0 + k % kStages * 8, (k / kStages) & 1, &g_attn_decode_err);
+}
+
+// Joins the states of an item that several CTAs share, in the order of its keys:
+// CTA c's launch-mate takes the item whose first part CTA c left.
+template <int D, int R>
+__global__ void __launch_bounds__(256)
+attn_join_kernel(const __grid_constant__ DecodeParams P, int parts) {
+    using Lay = DecodeLayout<D, R>;
+    constexpr int V = R * D / 256;                // channels of a thread: 4 (R = 8, D = 128) ...
+    pdl_trigger();
+    pdl_wait();
+    const int b = P.head[blockIdx.x * 4 + 2];
+    if (b >= 0) {
+        const int G = P.a.heads_q / P.a.kv.heads;
+        const Req r = load_req<R>(P, b, G);
+        const int item = P.head[blockIdx.x * 4 + 3], h = item / r.tiles, tile = item % r.tiles;
+        const int row = threadIdx.x * V / D, d0 = threadIdx.x * V % D;
+        const float* src = P.part + ((int64_t)blockIdx.x * 2 + 1) * Lay::PART;
+        float m = src[R * D + row], l = src[R * D + R + row], o[V];
+#pragma unroll
+        for (int i = 0; i < V; i++) o[i] = src[row * D + d0 + i];
+        bool more = true;
+        for (int c = blockIdx.x + 1; more && c < parts; c++) {
+            src = P.part + (int64_t)c * 2 * Lay::PART;
+            more = P.head[c * 4 + 1] != 0;
+            const float m2 = src[R * D + row], l2 = src[R * D + R + row], mm = fmaxf(m, m2);
+            const float f = m == -INFINITY ? (l == l ? 0.0f : l) : ex2(m - mm);
+            const float f2 = m2 == -INFINITY ? (l2 == l2 ? 0.0f : l2) : ex2(m2 - mm);
+            l = l * f + l2 * f2;
+#pragma unroll
+            for (int i = 0; i < V; i++) o[i] = o[i] * f + src[row * D + d0 + i] * f2;
+            m = mm;
+        }
+        const int rw = tile * R + row, i = rw / G, a = rw - i * G;
+        if (i < r.n) {
+            const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+            uint16_t* out = P.a.out + (int64_t)(r.q0 + i) * P.a.ldo + (int64_t)(h * G + a) * D + d0;
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+                const __nv_bfloat162 w = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+                *reinterpret_cast<__nv_bfloat162*>(out + e) = w;
+            }
+            if (P.a.lse && d0 == 0)
+                P.a.lse[(int64_t)(r.q0 + i) * P.a.heads_q + h * G + a] =
+                    l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+        }
+    }
+}
+
+template <int D, int R>
+qz_status launch_decode(DecodeParams& P, void* ws, cudaStream_t st) {
+    using Lay = DecodeLayout<D, R>;
+    const int ctas = num_sms();
+    P.head = reinterpret_cast<int*>(ws);
+    P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)ctas * 16 + 255) / 256 * 256);
+    QZ_TRY(opt_in_smem((const void*)attn_decode_kernel<D, R>, Lay::SMEM));
+    QZ_TRY(launch_pdl(attn_decode_kernel<D, R>, dim3(ctas), dim3(kThreads), Lay::SMEM, st, P));
+    return launch_pdl(attn_join_kernel<D, R>, dim3(ctas), dim3(256), 0, st, P, ctas);
+}
+
+} // namespace
+
+size_t ws_attn_decode() {
+    const size_t ctas = (size_t)num_sms();
+    return (ctas * 16 + 255) / 256 * 256 + ctas * 2 * DecodeLayout<128, 16>::PART * 4;
+}
+
+// Requests of at most max_rows rows per KV head; the others are left alone.
+qz_status attn_decode_launch(const AttnArgs& a, int max_rows, void* ws, cudaStream_t st) {
+    DecodeParams P;
+    P.a = a;
+    P.shift = a.kv.page_size == 16 ? 4 : a.kv.page_size == 32 ? 5 : a.kv.page_size == 64 ? 6 : 7;
+    P.max_rows = max_rows;
+    const uint64_t D = (uint64_t)a.kv.head_dim, rows = (uint64_t)a.kv.heads * a.kv.page_size;
+    const uint32_t box = (uint32_t)std::min(a.kv.page_size, kKeys);
+    if (!encode_tmap_3d_u8(&P.tm_k, a.kv.k_codes, D, rows, (uint64_t)a.kv.num_pages, D, (uint64_t)a.kv.page_stride,
+                           (uint32_t)D, box, (int)D) ||
+        !encode_tmap_3d_u8(&P.tm_v, a.kv.v_codes, D, rows, (uint64_t)a.kv.num_pages, D, (uint64_t)a.kv.page_stride,
+                           (uint32_t)D, box, (int)D))
+        return QZ_ERR_CUDA;
+    const int64_t most = std::min<int64_t>((int64_t)a.max_q * (a.heads_q / a.kv.heads), max_rows);
+    if (most <= 8)
+        return D == 64 ? launch_decode<64, 8>(P, ws, st) : launch_decode<128, 8>(P, ws, st);
+    return D == 64 ? launch_decode<64, 16>(P, ws, st) : launch_decode<128, 16>(P, ws, st);
+}
+
+qz_status attn_decode_error_read_and_clear() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_decode_err, sizeof(v)) != cudaSuccess) return QZ_ERR_CUDA;
+    if (v && cudaMemcpyToSymbol(g_attn_decode_err, &z, sizeof(z)) != cudaSuccess) return QZ_ERR_CUDA;
+    return v ? QZ_ERR_TIMEOUT : QZ_OK;
+}
+
+} // namespace qz

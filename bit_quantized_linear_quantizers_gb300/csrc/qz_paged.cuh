@@ -33,6 +33,10 @@ struct AttnArgs {
 };
 size_t ws_attn_paged(int64_t rows, int64_t head_dim);
 qz_status attn_paged_launch(const AttnArgs& a, void* ws, cudaStream_t st);
+// the requests of at most max_rows query rows per KV head (attn_fp8_decode.cu)
+size_t ws_attn_decode();
+qz_status attn_decode_launch(const AttnArgs& a, int max_rows, void* ws, cudaStream_t st);
+qz_status attn_decode_error_read_and_clear();
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

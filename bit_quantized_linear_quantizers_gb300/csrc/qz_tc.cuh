@@ -204,5 +204,8 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
 bool encode_tmap_2d_swz(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t outer,
                         uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, int swizzle_bytes);
+bool encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
+                       uint64_t row_bytes, uint64_t plane_bytes, uint32_t box_inner, uint32_t box_rows,
+                       int swizzle_bytes);
 
 } // namespace qz

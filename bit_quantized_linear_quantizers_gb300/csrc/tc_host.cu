@@ -83,4 +83,25 @@ bool encode_tmap_2d_swz(CUtensorMap* map, const void* base, int elem_bytes, uint
     return r == CUDA_SUCCESS;
 }
 
+// A 3-D byte tensor (pitches row_bytes and plane_bytes) read in boxes of one plane,
+// box_rows rows of the whole inner extent, with a swizzle of swizzle_bytes (as above).
+bool encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
+                       uint64_t row_bytes, uint64_t plane_bytes, uint32_t box_inner, uint32_t box_rows,
+                       int swizzle_bytes) {
+    std::call_once(g_once, load_encode);
+    if (!g_encode) return false;
+    const CUtensorMapSwizzle sw = swizzle_bytes == 32    ? CU_TENSOR_MAP_SWIZZLE_32B
+                                  : swizzle_bytes == 64  ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                         : CU_TENSOR_MAP_SWIZZLE_NONE;
+    const cuuint64_t dims[3] = {inner, rows, planes};
+    const cuuint64_t strides[2] = {row_bytes, plane_bytes};
+    const cuuint32_t box[3] = {box_inner, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 } // namespace qz
