@@ -27,8 +27,7 @@
 // (request, head) the eight states join in shared memory; what spans several
 // CTAs is joined by a second, small launch in a fixed order.
 #include "qz_internal.cuh"
-#include "qz_paged.cuh"
-#include "qz_tc.cuh"
+#include "attn_fp8.cuh"
 
 #include <algorithm>
 
@@ -41,43 +40,13 @@ __device__ unsigned int g_attn_decode_err;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 32;                         // keys of a unit
 constexpr int kStages = 3;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kPShift = 8.0f;                   // p = 2^(t - m + 8)
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Two values as E4M3 parts: hi = E4M3(x), lo = E4M3(x - hi); 16 bits each. The
-// f16 step in between keeps 11 bits (the values lie in [-256, 256]).
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-    uint32_t h, back;
-    uint16_t e, f;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(h));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(e));
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(back));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(f) : "r"(h));
-    hi = e;
-    lo = f;
-}
-
-// Four values -> one register of each part (value i in byte i).
-__device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
-    uint32_t ha, la, hb, lb;
-    split2(x0, x1, ha, la);
-    split2(x2, x3, hb, lb);
-    hi = ha | hb << 16;
-    lo = la | lb << 16;
 }
 
 // 4 x 4 byte transpose: out[i] holds byte i of a, b, c, d in that order.
@@ -88,13 +57,6 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
     out[1] = __byte_perm(ab0, cd0, 0x7632);
     out[2] = __byte_perm(ab1, cd1, 0x5410);
     out[3] = __byte_perm(ab1, cd1, 0x7632);
-}
-
-// 3-D TMA load of a box (channels, rows, page).
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4}], [%5];"
-                 ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
 struct DecodeParams {
@@ -387,11 +349,8 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             for (int e = 0; e < D / 4; e++) m = fmaxf(m, fabsf(v[e]));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // 2^(7 - floor(log2 amax)): from the exponent field, within the normal range
-            const int ex = (int)(__float_as_uint(m) >> 23) & 255;
-            const int se = min(max(134 + 127 - ex, 1), 240);
-            const float up = m > 0.0f ? __uint_as_float((uint32_t)se << 23) : 1.0f;
-            const float down = m > 0.0f ? __uint_as_float((uint32_t)max(254 - se, 1) << 23) : 1.0f;
+            float up, down;
+            row_scale(m, up, down);
             crow[rr] = c0 * down;
             const float sgn = P.a.sm_scale < 0.0f ? -up : up;
             seen[rr] = !there ? 0 : P.a.causal ? min(max(cur.r.L - cur.r.n + i + 1, 0), cur.r.L) : cur.r.L;

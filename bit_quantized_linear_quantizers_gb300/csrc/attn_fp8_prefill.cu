@@ -1,0 +1,537 @@
+// attn_fp8_prefill.cu -- attention over the paged FP8 KV cache for many query rows
+// per KV head (prompts, chunks of prompts, cross attention of prompts): bound by
+// the tensor cores, so both products run on tcgen05 with accumulators in TMEM.
+//
+// Rows: the query heads of a KV head and the tokens of a request are packed into
+// one row index (token * group + head), so a key tile is read once for the group.
+// A CTA takes 256 rows (two 128-row tiles, one warpgroup of softmax each) and
+// walks the keys in tiles of 128:
+//   S = q K^T    kind::f8f6f4. K enters as stored; bf16 q is the sum of two E4M3
+//                parts (4 + 4 significant bits, see attn_fp8_decode.cu), two MMAs at
+//                twice the bf16 rate each: the time of a bf16 product, and no
+//                widening of K.
+//   O += P V     kind::f16, P from TMEM in f16 (11 bits), V widened from E4M3 to f16 (exact)
+//                by a warpgroup of its own. Splitting P into two E4M3 parts as well would
+//                spare the widening but costs 14 issue cycles per pair of scores and
+//                scheduler against 2 (measured conversion rates: e4m3x2.f16x2 4.0 cycles
+//                per warp, f16x2.e4m3x2 2.25, f16x2.f32 2.0): more than the MMAs take.
+// The page's value scale goes into the exponent, as in the decode kernel:
+//   t = x log2(e) + log2 sv, p = 2^(t - m + 8), O = sum p c, l = sum p / sv.
+// m is raised only when a row's maximum has grown by more than 2^6 (p stays
+// below 2^15), which spares most rescalings of O.
+//
+// The two row tiles alternate on the tensor cores: while one's softmax runs, the
+// other's P V and next S do. S's TMEM columns hold P afterwards.
+#include "qz_internal.cuh"
+#include "attn_fp8.cuh"
+
+#include <algorithm>
+
+namespace qz {
+
+namespace {
+
+__device__ unsigned int g_attn_prefill_err;
+
+constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 13 MMA
+constexpr int kM = 128, kRows = 2 * kM, kN = 128; // rows of a tile, of a CTA; keys of a tile
+constexpr int kKStages = 3, kVStages = 2, kScStages = 4;
+constexpr float kPShift = 8.0f, kGrow = 6.0f;
+
+struct PrefillParams {
+    CUtensorMap tm_k, tm_v;                       // codes as (head_dim, heads * page_size, num_pages), one page's rows a box
+    AttnArgs a;
+    int shift;
+    int min_rows;                                 // requests with fewer rows per KV head are not taken
+    int tiles;                                    // upper bound of row tiles over all requests
+};
+
+template <int D>
+struct PrefillLayout {
+    static constexpr int Q = kM * D;                                // one part of one row tile
+    static constexpr int KT = kN * D;                               // a key tile (codes)
+    static constexpr int VH = kN * D * 2;                           // a value tile in f16
+    static constexpr int Q_OFF = 0;                                 // [tile][part]
+    static constexpr int K_OFF = Q_OFF + 4 * Q;
+    static constexpr int V_OFF = K_OFF + kKStages * KT;
+    static constexpr int VH_OFF = V_OFF + kVStages * KT;
+    static constexpr int SC_OFF = VH_OFF + 2 * VH;                  // [stage][8] float4: scales of 16 keys
+    static constexpr int BAR_OFF = SC_OFF + kScStages * 8 * 16;
+    static constexpr int SMEM = BAR_OFF + 512 + 1024;
+    static constexpr uint32_t S_COL = 0, O_COL = 256;               // TMEM columns: S0 S1 O0 O1
+    static constexpr uint32_t IDESC_S = idesc_dense(0u, 0u, kM, kN);                     // E4M3 x E4M3
+    static constexpr uint32_t IDESC_O = idesc_dense(0u, 0u, kM, D) | 1u << 16;           // f16 x f16, B MN-major
+};
+
+// K-major operand tile of D-byte rows under the D-byte swizzle (8-row atoms stacked).
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_k(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)((8 * D) >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
+    return d;
+}
+
+// MN-major f16 operand: 64-channel blocks (128 bytes per key, 128-byte swizzle over 8
+// keys), the blocks kN * 128 bytes apart (leading offset), 8-key groups 1024 apart.
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((kN * 128) >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+template <int REGS> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
+    using L = PrefillLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+    // barriers: K full/empty, raw V full/empty, widened V full/empty, scales full, S full, P full, O done, q, drain
+    constexpr int KF = 0, KE = KF + kKStages, VF = KE + kKStages, VE = VF + kVStages, HF = VE + kVStages, HE = HF + 2,
+                  SC = HE + 2, SF = SC + kScStages, PF = SF + 2, OD = PF + 2, QF = OD + 2, DR = QF + 2, NBAR = DR + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
+    int* s_item = reinterpret_cast<int*>(bars + NBAR + 1);          // request, row tile
+    float4* sc = reinterpret_cast<float4*>(smem + L::SC_OFF);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = P.a.heads_q / P.a.kv.heads;
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's item: KV head and row tile, the last row tiles (the longest under the causal rule) first
+    const int h = blockIdx.x % P.a.kv.heads;
+    if (warp == 13) {
+        const int want = P.tiles - 1 - (int)(blockIdx.x / P.a.kv.heads);
+        int before = 0;
+        if (lane == 0) s_item[0] = -1;
+        __syncwarp();
+        for (int b0 = 0; b0 < P.a.B; b0 += 32) {
+            const int b = b0 + lane;
+            int own = 0;
+            if (b < P.a.B) {
+                const int n = min(__ldg(P.a.cu_q + b + 1) - __ldg(P.a.cu_q + b), P.a.max_q);
+                const int64_t rows = (int64_t)max(n, 0) * G;
+                own = rows < P.min_rows ? 0 : (int)((rows + kRows - 1) / kRows);
+            }
+            int v = own;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            const int first = before + v - own;
+            if (want >= first && want < first + own) {
+                s_item[0] = b;
+                s_item[1] = want - first;
+            }
+            before += __shfl_sync(0xffffffffu, v, 31);
+            if (before > want) break;
+        }
+        __syncwarp();
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kKStages; s++) { mbar_init(bar(KF + s), 1); mbar_init(bar(KE + s), 1); }
+        for (int s = 0; s < kVStages; s++) { mbar_init(bar(VF + s), 1); mbar_init(bar(VE + s), 4); }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(bar(HF + s), 4);
+            mbar_init(bar(HE + s), 1);
+            mbar_init(bar(SF + s), 1);
+            mbar_init(bar(PF + s), 4);
+            mbar_init(bar(OD + s), 1);
+            mbar_init(bar(QF + s), 4);
+        }
+        for (int s = 0; s < kScStages; s++) mbar_init(bar(SC + s), 1);
+        mbar_init(bar(DR), 1);
+        fence_barrier_init();
+        prefetch_tmap(&P.tm_k);
+        prefetch_tmap(&P.tm_v);
+    }
+    __syncthreads();
+    const int b = s_item[0];
+    if (b < 0) return;                            // fewer row tiles than the bound: nothing here
+    if (warp == 13) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int row0 = s_item[1] * kRows;
+    const int q0 = __ldg(P.a.cu_q + b);
+    int n = min(__ldg(P.a.cu_q + b + 1) - q0, P.a.max_q);
+    n = q0 < 0 ? 0 : (int)min((int64_t)n, P.a.tokens - q0);
+    const int Lk = (int)min((int64_t)max(__ldg(P.a.kv_lens + b), 0), (int64_t)P.a.max_blocks << P.shift);
+    // key tiles of each row tile: up to what its last row sees
+    int nk[2];
+#pragma unroll
+    for (int w = 0; w < 2; w++) {
+        const int first = row0 + w * kM, last = min(first + kM, n * G) - 1;
+        const int sees = last < first ? 0 : P.a.causal ? min(max(Lk - n + last / G + 1, 0), Lk) : Lk;
+        nk[w] = (sees + kN - 1) / kN;
+    }
+    const int nkv = max(nk[0], nk[1]);
+    const int pages_tile = kN >> P.shift;         // boxes of a key tile
+
+    if (warp < 8) {
+        // ------------------------------------------------------- softmax
+        reg_inc<192>();
+        const int w = warp >> 2, q = warp & 3;
+        const int row = row0 + w * kM + q * 32 + lane, i = row / G, a = row - i * G;
+        const bool there = i < n;
+        const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+        const uint32_t s_addr = lane_base + L::S_COL + w * kN, o_addr = lane_base + L::O_COL + w * D;
+        float crow = 0.0f;
+        bool ok = true;
+        if (nk[w] > 0) {
+            // the row's two E4M3 parts into shared memory, in the swizzled order of the K-major operand
+            const uint16_t* src = P.a.q + (int64_t)(q0 + i) * P.a.ldq + (int64_t)(h * G + a) * D;
+            uint4 raw[D / 8];
+            float m = 0.0f;
+#pragma unroll
+            for (int c = 0; c < D / 8; c++) {
+                raw[c] = there ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+                const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+            }
+            float up, down;
+            row_scale(m, up, down);
+            crow = fabsf(P.a.sm_scale) * kLog2e * down;
+            if (P.a.sm_scale < 0.0f) up = -up;
+            const int r = q * 32 + lane;
+            uint8_t* hi = smem + L::Q_OFF + (w * 2) * L::Q + r * D;
+#pragma unroll
+            for (int c = 0; c < D / 16; c++) {    // 16 channels
+                uint32_t hw[4], lw[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const uint4 x = raw[2 * c + (e >> 1)];
+                    const uint32_t y0 = e & 1 ? x.z : x.x, y1 = e & 1 ? x.w : x.y;
+                    split4(__uint_as_float(y0 << 16) * up, __uint_as_float(y0 & 0xFFFF0000u) * up,
+                           __uint_as_float(y1 << 16) * up, __uint_as_float(y1 & 0xFFFF0000u) * up, hw[e], lw[e]);
+                }
+                const int ch = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+                *reinterpret_cast<uint4*>(hi + ch * 16) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                *reinterpret_cast<uint4*>(hi + L::Q + ch * 16) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(QF + w));
+        }
+        const int seen = !there ? 0 : P.a.causal ? min(max(Lk - n + i + 1, 0), Lk) : Lk;
+        // the fewest keys that a row of this warp sees (rows past the end see none, and are not stored)
+        int least = there ? seen : 0x7fffffff;
+        for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        float m = -INFINITY, l = 0.0f;
+        for (int t = 0; t < nk[w] && ok; t++) {
+            if (!mbar_wait(bar(SC + t % kScStages), (t / kScStages) & 1, &g_attn_prefill_err)) { ok = false; break; }
+            if (!mbar_wait(bar(SF + w), t & 1, &g_attn_prefill_err)) { ok = false; break; }
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; c++) tmem_ld32(s_addr + c * 32, s[c]);
+            tmem_wait_ld();
+            const float4* con = sc + (t % kScStages) * 8;             // (k scale, log2 v scale, 1 / v scale) per 16 keys
+            const int lim = seen - t * kN;
+            const bool edge = least < (t + 1) * kN;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int gr = 0; gr < 8; gr++) {
+                const float4 cn = con[gr];
+                const float ca = crow * cn.x;
+                if (!edge) {
+                    float gm = __uint_as_float(s[gr >> 1][(gr & 1) * 16]);
+#pragma unroll
+                    for (int e = 1; e < 16; e++) gm = fmaxf(gm, __uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]));
+                    mx = fmaxf(mx, fmaf(gm, ca, cn.y));               // ca >= 0: the largest score of the group
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        if (gr * 16 + e < lim) mx = fmaxf(mx, fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]), ca, cn.y));
+                }
+            }
+            const bool raise = mx > m + kGrow || m == -INFINITY;
+            const float m2 = raise ? fmaxf(mx, m) : m;
+            const float f = m == -INFINITY ? 0.0f : ex2(m - m2);
+            if (t > 0 && __any_sync(0xffffffffu, m2 != m)) {          // O so far, under the new maximum
+#pragma unroll
+                for (int c = 0; c < D / 32; c++) {
+                    uint32_t o[32];
+                    tmem_ld32(o_addr + c * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st32(o_addr + c * 32, o);
+                }
+            }
+            l *= f;
+            m = m2;
+            const float off = m == -INFINITY ? 0.0f : kPShift - m;
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int gg = 0; gg < 4; gg++) {
+                    const int gr = half * 4 + gg;
+                    const float4 cn = con[gr];
+                    const float ca = crow * cn.x, cb = cn.y + off;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float p0 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]), ca, cb));
+                        float p1 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e + 1]), ca, cb));
+                        if (edge) {
+                            p0 = gr * 16 + e < lim ? p0 : 0.0f;
+                            p1 = gr * 16 + e + 1 < lim ? p1 : 0.0f;
+                        }
+                        sum += p0 + p1;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[gg * 8 + e / 2]) : "f"(p1), "f"(p0));
+                    }
+                    l = fmaf(sum, cn.z, l);
+                }
+                tmem_st32(s_addr + half * 32, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(PF + w));
+        }
+        // ---- output
+        if (nk[w] > 0 && ok) ok = mbar_wait(bar(OD + w), 0, &g_attn_prefill_err);
+        tc_fence_after();
+        const float r = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+        uint16_t* out = P.a.out + (int64_t)(q0 + i) * P.a.ldo + (int64_t)(h * G + a) * D;
+        if (ok) {
+#pragma unroll
+            for (int c = 0; c < D / 32; c++) {
+                uint32_t o[32];
+                if (nk[w] > 0) {
+                    tmem_ld32(o_addr + c * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e++) o[e] = 0u;
+                }
+                if (there) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            float x0 = __uint_as_float(o[e + 2 * j]) * r, x1 = __uint_as_float(o[e + 2 * j + 1]) * r;
+                            if (l == 0.0f) x0 = x1 = 0.0f;            // a row that saw nothing
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
+                            y[j] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            if (there && P.a.lse)
+                P.a.lse[(int64_t)(q0 + i) * P.a.heads_q + h * G + a] =
+                    l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+        }
+        tc_fence_before();
+    } else if (warp < 12) {
+        // ------------------------------------------------- V codes to f16
+        reg_dec<72>();
+        const int tid = threadIdx.x - 256;
+        bool ok = true;
+        for (int t = 0; t < nkv && ok; t++) {
+            const int st = t % kVStages, hb = t & 1;
+            if (!mbar_wait<false>(bar(VF + st), (t / kVStages) & 1, &g_attn_prefill_err)) { ok = false; break; }
+            if (!mbar_wait(bar(HE + hb), ((t >> 1) & 1) ^ 1, &g_attn_prefill_err)) { ok = false; break; }
+            const uint8_t* src = smem + L::V_OFF + st * L::KT;
+            uint8_t* dst = smem + L::VH_OFF + hb * L::VH;
+            const int live = Lk - t * kN;         // rows behind the last key were never written: zeros
+            constexpr int CH = D / 16;            // 16-code chunks of a row
+#pragma unroll
+            for (int k = 0; k < CH; k++) {
+                const int idx = k * 128 + tid, r = idx / CH, c = idx % CH;
+                uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
+                if (r >= live) x = make_uint4(0, 0, 0, 0);
+                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[8];
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    asm("{ .reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi; }"
+                        : "=r"(y[2 * e]), "=r"(y[2 * e + 1]) : "r"(in[e]));
+                uint8_t* row = dst + (c >> 2) * (kN * 128) + r * 128;
+                const int c0 = (c & 3) * 2, sw = r & 7, odd = c >> 2;               // the second block's halves swapped: other banks
+                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ sw) << 4)) = odd ? hi : lo;
+                *reinterpret_cast<uint4*>(row + (((c0 + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(HF + hb));
+                mbar_arrive(bar(VE + st));
+            }
+        }
+    } else {
+        reg_dec<56>();
+        if (warp == 12) {
+            // ------------------------------------------------- TMA, scales
+            const int32_t* tab = P.a.block_table + (int64_t)b * P.a.ld_table;
+            const int page_end = (Lk + (1 << P.shift) - 1) >> P.shift;
+            auto page_at = [&](int t) {           // lane's page of tile t, num_pages (out of bounds: reads as zeros) if none
+                const int j = t * pages_tile + lane;
+                int p = -1;
+                if (lane < pages_tile && j < page_end) p = __ldg(tab + j);
+                return p >= 0 && p < P.a.kv.num_pages ? p : P.a.kv.num_pages;
+            };
+            int p = nkv > 0 ? page_at(0) : 0;
+            bool ok = true;
+            int t = 0;
+            for (; t < nkv && ok; t++) {
+                const int ks = t % kKStages, vs = t % kVStages;
+                const int next = t + 1 < nkv ? page_at(t + 1) : 0;
+                float4 cn = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+                if (lane < pages_tile && p < P.a.kv.num_pages) {
+                    const int64_t i = (int64_t)p * P.a.kv.heads + h;
+                    const float kscale = __ldg(P.a.kv.k_scale + i), vscale = fmaxf(__ldg(P.a.kv.v_scale + i), 1.2e-38f);
+                    cn = make_float4(kscale, __log2f(vscale), __frcp_rn(vscale), 0.0f);
+                }
+                ok = mbar_wait(bar(KE + ks), ((t / kKStages) & 1) ^ 1, &g_attn_prefill_err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(KF + ks), L::KT);
+                __syncwarp();
+                if (lane < pages_tile)
+                    tma_load_3d(sbase + L::K_OFF + ks * L::KT + (lane << P.shift) * D, &P.tm_k, 0, h << P.shift, p, bar(KF + ks));
+                // scales per 16 keys (a page covers page_size / 16 of them)
+                const int reps = 1 << (P.shift - 4);
+                if (lane < pages_tile)
+                    for (int j = 0; j < reps; j++) sc[(t % kScStages) * 8 + lane * reps + j] = cn;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(SC + t % kScStages));
+                ok = mbar_wait(bar(VE + vs), ((t / kVStages) & 1) ^ 1, &g_attn_prefill_err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(VF + vs), L::KT);
+                __syncwarp();
+                if (lane < pages_tile)
+                    tma_load_3d(sbase + L::V_OFF + vs * L::KT + (lane << P.shift) * D, &P.tm_v, 0, h << P.shift, p, bar(VF + vs));
+                p = next;
+            }
+            // no copy outlives the CTA (at once unless a wait gave up)
+            for (int j = max(0, t - kKStages); j < t; j++) mbar_wait(bar(KF + j % kKStages), (j / kKStages) & 1, &g_attn_prefill_err);
+            for (int j = max(0, t - kVStages); j < t; j++) mbar_wait(bar(VF + j % kVStages), (j / kVStages) & 1, &g_attn_prefill_err);
+            if (!ok) mbar_wait(bar(KF + t % kKStages), (t / kKStages) & 1, &g_attn_prefill_err);
+        } else if (warp == 13) {
+            // -------------------------------------------------------- MMA
+            if (lane == 0 && nkv > 0) {
+                bool ok = true;
+                auto wait = [&](int i, uint32_t parity) { ok = ok && mbar_wait(bar(i), parity, &g_attn_prefill_err); };
+                auto score = [&](int w, int t) {  // S of row tile w and key tile t, both parts of q
+                    const uint32_t d = tmem + L::S_COL + w * kN, ka = sbase + L::K_OFF + (t % kKStages) * L::KT;
+#pragma unroll
+                    for (int part = 0; part < 2; part++)
+#pragma unroll
+                        for (int k = 0; k < D / 32; k++)
+                            mma_f8f6f4(d, sdesc_k<D>(sbase + L::Q_OFF + (w * 2 + part) * L::Q) + k * 2, sdesc_k<D>(ka) + k * 2,
+                                       L::IDESC_S, part + k > 0);
+                    tc_commit(bar(SF + w));
+                };
+                auto value = [&](int w, int t) {  // O += P V
+                    const uint32_t pa = tmem + L::S_COL + w * kN, va = sbase + L::VH_OFF + (t & 1) * L::VH;
+#pragma unroll
+                    for (int k = 0; k < kN / 16; k++)
+                        mma_f16_ts(tmem + L::O_COL + w * D, pa + k * 8, sdesc_v(va + k * 2048), L::IDESC_O, t > 0 || k > 0);
+                    if (t + 1 == nk[w]) tc_commit(bar(OD + w));
+                };
+                for (int w = 0; w < 2; w++)
+                    if (nk[w] > 0) wait(QF + w, 0);
+                wait(KF, 0);
+                tc_fence_after();
+                if (ok) {
+                    for (int w = 0; w < 2; w++)
+                        if (nk[w] > 0) score(w, 0);
+                    tc_commit(bar(KE));
+                }
+                for (int t = 0; t < nkv && ok; t++) {
+                    if (t + 1 < nkv) wait(KF + (t + 1) % kKStages, ((t + 1) / kKStages) & 1);
+                    wait(HF + (t & 1), (t >> 1) & 1);
+                    for (int w = 0; w < 2 && ok; w++) {
+                        if (t < nk[w]) {
+                            wait(PF + w, t & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            value(w, t);
+                            if (t + 1 < nk[w]) score(w, t + 1);
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit(bar(HE + (t & 1)));
+                    if (t + 1 < nkv) tc_commit(bar(KE + (t + 1) % kKStages));
+                }
+                tc_commit(bar(DR));               // no MMA outlives the CTA's tensor memory
+                mbar_wait(bar(DR), 0, &g_attn_prefill_err);
+            }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+qz_status launch_prefill(const PrefillParams& P, int64_t ctas, cudaStream_t st) {
+    using L = PrefillLayout<D>;
+    QZ_TRY(opt_in_smem((const void*)attn_prefill_kernel<D>, L::SMEM));
+    return launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), L::SMEM, st, P);
+}
+
+} // namespace
+
+// Requests of at least min_rows rows per KV head; the others are left alone.
+qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, cudaStream_t st) {
+    PrefillParams P;
+    P.a = a;
+    P.shift = a.kv.page_size == 16 ? 4 : a.kv.page_size == 32 ? 5 : a.kv.page_size == 64 ? 6 : 7;
+    P.min_rows = min_rows;
+    const uint64_t D = (uint64_t)a.kv.head_dim, rows = (uint64_t)a.kv.heads * a.kv.page_size;
+    const uint32_t box = (uint32_t)a.kv.page_size;
+    if (!encode_tmap_3d_u8(&P.tm_k, a.kv.k_codes, D, rows, (uint64_t)a.kv.num_pages, D, (uint64_t)a.kv.page_stride,
+                           (uint32_t)D, box, (int)D) ||
+        !encode_tmap_3d_u8(&P.tm_v, a.kv.v_codes, D, rows, (uint64_t)a.kv.num_pages, D, (uint64_t)a.kv.page_stride,
+                           (uint32_t)D, box, 0))
+        return QZ_ERR_CUDA;
+    // row tiles of the requests: at most one partly filled each, and a request taken has min_rows rows
+    const int64_t all = a.tokens * (a.heads_q / a.kv.heads);
+    const int64_t tiles = all / kRows + std::min<int64_t>(a.B, all / min_rows + 1);
+    if (tiles * a.kv.heads > 0x7fffffff) return QZ_ERR_SHAPE;
+    P.tiles = (int)tiles;
+    return a.kv.head_dim == 64 ? launch_prefill<64>(P, tiles * a.kv.heads, st)
+                               : launch_prefill<128>(P, tiles * a.kv.heads, st);
+}
+
+qz_status attn_prefill_error_read_and_clear() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_prefill_err, sizeof(v)) != cudaSuccess) return QZ_ERR_CUDA;
+    if (v && cudaMemcpyToSymbol(g_attn_prefill_err, &z, sizeof(z)) != cudaSuccess) return QZ_ERR_CUDA;
+    return v ? QZ_ERR_TIMEOUT : QZ_OK;
+}
+
+} // namespace qz

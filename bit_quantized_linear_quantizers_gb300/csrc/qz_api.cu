@@ -78,10 +78,10 @@ qz_status selftest_error_read_and_clear() {
 
 qz_status device_error_read_and_clear() {
     // read and clear every word, report the first error found
-    const qz_status s[7] = {w4a16_error_read_and_clear(), w4a16_tc_error_read_and_clear(),
+    const qz_status s[8] = {w4a16_error_read_and_clear(), w4a16_tc_error_read_and_clear(),
                             fp8_block_error_read_and_clear(), fp4_error_read_and_clear(),
                             int8_error_read_and_clear(), selftest_error_read_and_clear(),
-                            attn_decode_error_read_and_clear()};
+                            attn_decode_error_read_and_clear(), attn_prefill_error_read_and_clear()};
     for (qz_status v : s)
         if (v != QZ_OK) return v;
     return QZ_OK;
