@@ -37,6 +37,7 @@ constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 wid
 constexpr int kM = 128, kRows = 2 * kM, kN = 128; // rows of a tile, of a CTA; keys of a tile
 constexpr int kKStages = 3, kVStages = 2, kScStages = 4;
 constexpr float kPShift = 8.0f, kGrow = 6.0f;
+constexpr float kTiny = 1e-30f;                   // least factor of a raw score: -inf stays -inf under it
 
 struct PrefillParams {
     CUtensorMap tm_k, tm_v;                       // codes as (head_dim, heads * page_size, num_pages), one page's rows a box
@@ -85,6 +86,12 @@ __device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
+}
+
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
 }
 
 template <int REGS> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
@@ -188,7 +195,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax
-        reg_inc<192>();
+        reg_inc<208>();
         const int w = warp >> 2, q = warp & 3;
         const int row = row0 + w * kM + q * 32 + lane, i = row / G, a = row - i * G;
         const bool there = i < n;
@@ -248,22 +255,25 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             tmem_wait_ld();
             const float4* con = sc + (t % kScStages) * 8;             // (k scale, log2 v scale, 1 / v scale) per 16 keys
             const int lim = seen - t * kN;
-            const bool edge = least < (t + 1) * kN;
+            if (least < (t + 1) * kN) {           // some row of the warp does not see the whole tile
+#pragma unroll
+                for (int e = 0; e < kN; e++)
+                    if (e >= lim) s[e >> 5][e & 31] = 0xFF800000u;    // -inf: its score is -inf, its p 0
+            }
+            // largest score of the row: the scale of 16 keys is positive, so their raw maximum gives it
             float mx = -INFINITY;
 #pragma unroll
             for (int gr = 0; gr < 8; gr++) {
                 const float4 cn = con[gr];
-                const float ca = crow * cn.x;
-                if (!edge) {
-                    float gm = __uint_as_float(s[gr >> 1][(gr & 1) * 16]);
+                const uint32_t* x = s[gr >> 1] + (gr & 1) * 16;
+                float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
 #pragma unroll
-                    for (int e = 1; e < 16; e++) gm = fmaxf(gm, __uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]));
-                    mx = fmaxf(mx, fmaf(gm, ca, cn.y));               // ca >= 0: the largest score of the group
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        if (gr * 16 + e < lim) mx = fmaxf(mx, fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]), ca, cn.y));
+                for (int e = 6; e < 14; e += 4) {
+                    g0 = max3(__float_as_uint(g0), x[e], x[e + 1]);
+                    g1 = max3(__float_as_uint(g1), x[e + 2], x[e + 3]);
                 }
+                g0 = max3(__float_as_uint(g0), x[14], x[15]);
+                mx = fmaxf(mx, fmaf(fmaxf(g0, g1), fmaxf(crow * cn.x, kTiny), cn.y));
             }
             const bool raise = mx > m + kGrow || m == -INFINITY;
             const float m2 = raise ? fmaxf(mx, m) : m;
@@ -289,20 +299,17 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                 for (int gg = 0; gg < 4; gg++) {
                     const int gr = half * 4 + gg;
                     const float4 cn = con[gr];
-                    const float ca = crow * cn.x, cb = cn.y + off;
-                    float sum = 0.0f;
+                    const float ca = fmaxf(crow * cn.x, kTiny), cb = cn.y + off;
+                    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        float p0 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]), ca, cb));
-                        float p1 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e + 1]), ca, cb));
-                        if (edge) {
-                            p0 = gr * 16 + e < lim ? p0 : 0.0f;
-                            p1 = gr * 16 + e + 1 < lim ? p1 : 0.0f;
-                        }
-                        sum += p0 + p1;
+                        const float p0 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]), ca, cb));
+                        const float p1 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e + 1]), ca, cb));
+                        s0 += p0;
+                        s1 += p1;
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[gg * 8 + e / 2]) : "f"(p1), "f"(p0));
                     }
-                    l = fmaf(sum, cn.z, l);
+                    l = fmaf(s0 + s1, cn.z, l);
                 }
                 tmem_st32(s_addr + half * 32, pk);
             }
@@ -349,7 +356,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
         tc_fence_before();
     } else if (warp < 12) {
         // ------------------------------------------------- V codes to f16
-        reg_dec<72>();
+        reg_dec<48>();
         const int tid = threadIdx.x - 256;
         bool ok = true;
         for (int t = 0; t < nkv && ok; t++) {
@@ -360,7 +367,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             uint8_t* dst = smem + L::VH_OFF + hb * L::VH;
             const int live = Lk - t * kN;         // rows behind the last key were never written: zeros
             constexpr int CH = D / 16;            // 16-code chunks of a row
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < CH; k++) {
                 const int idx = k * 128 + tid, r = idx / CH, c = idx % CH;
                 uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
@@ -386,7 +393,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             }
         }
     } else {
-        reg_dec<56>();
+        reg_dec<48>();
         if (warp == 12) {
             // ------------------------------------------------- TMA, scales
             const int32_t* tab = P.a.block_table + (int64_t)b * P.a.ld_table;
