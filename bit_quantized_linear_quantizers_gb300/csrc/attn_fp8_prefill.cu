@@ -33,7 +33,7 @@ namespace {
 
 __device__ unsigned int g_attn_prefill_err;
 
-constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 13 MMA
+constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 14 and 15 MMA
 constexpr int kM = 128, kRows = 2 * kM, kN = 128; // rows of a tile, of a CTA; keys of a tile
 constexpr int kKStages = 3, kVStages = 2, kScStages = 4;
 constexpr float kPShift = 8.0f, kGrow = 6.0f;
@@ -64,38 +64,53 @@ struct PrefillLayout {
     static constexpr uint32_t IDESC_O = idesc_dense(0u, 0u, kM, D) | 1u << 16;           // f16 x f16, B MN-major
 };
 
-// K-major operand tile of D-byte rows under the D-byte swizzle (8-row atoms stacked).
+// Shared-memory descriptors as two words, so that the issuing thread adds an offset
+// to the low one only: the low word holds the address (in 16-byte units) and the
+// leading offset, the high word is a constant of the layout. One thread issues 32
+// MMAs of 64 cycles per pair of row tiles: with descriptors built per MMA the issue
+// took 156 cycles each, more than twice the MMAs themselves.
+// K-major operand of D-byte rows under the D-byte swizzle (8-row atoms stacked).
 template <int D>
-__device__ __forceinline__ uint64_t sdesc_k(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)1 << 16;
-    d |= (uint64_t)((8 * D) >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
-    return d;
-}
-
+__device__ __forceinline__ uint32_t sdesc_k_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
+template <int D>
+__device__ constexpr uint32_t sdesc_k_hi() { return (uint32_t)(8 * D) >> 4 | 1u << 14 | (D == 128 ? 2u : 4u) << 29; }
 // MN-major f16 operand: 64-channel blocks (128 bytes per key, 128-byte swizzle over 8
 // keys), the blocks kN * 128 bytes apart (leading offset), 8-key groups 1024 apart.
-__device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((kN * 128) >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+__device__ __forceinline__ uint32_t sdesc_v_lo(uint32_t saddr) {
+    return (saddr & 0x3FFFFu) >> 4 | (uint32_t)((kN * 128) >> 4) << 16;
 }
+constexpr uint32_t kDescVHi = 1024u >> 4 | 1u << 14 | 2u << 29;
 
+__device__ __forceinline__ void mma_s(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
+    asm volatile("{ .reg .pred p; .reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p; }"
+                 ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+__device__ __forceinline__ void mma_o(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool acc) {
+    asm volatile("{ .reg .pred p; .reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }"
+                 ::"r"(d), "r"(a), "r"(b_lo), "r"(kDescVHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
 __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
     return r;
 }
 
-template <int REGS> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
-template <int REGS> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
+// The bounded wait of this kernel: few polls with a long suspend hint.
+constexpr uint32_t kHintNs = 1000, kPolls = 1u<<21;
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kPolls; i++) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(bar), "r"(parity), "r"(kHintNs) : "memory");
+        if (ok) return true;
+    }
+    atomicExch(&g_attn_prefill_err, (unsigned int)QZ_ERR_TIMEOUT);
+    return false;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -108,7 +123,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
     auto bar = [&](int i) { return smem_u32(bars + i); };
     // barriers: K full/empty, raw V full/empty, widened V full/empty, scales full, S full, P full, O done, q, drain
     constexpr int KF = 0, KE = KF + kKStages, VF = KE + kKStages, VE = VF + kVStages, HF = VE + kVStages, HE = HF + 2,
-                  SC = HE + 2, SF = SC + kScStages, PF = SF + 2, OD = PF + 2, QF = OD + 2, DR = QF + 2, NBAR = DR + 1;
+                  SC = HE + 2, SF = SC + kScStages, PF = SF + 2, OD = PF + 2, QF = OD + 2, DR = QF + 2, TN = DR + 2, NBAR = TN + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
     int* s_item = reinterpret_cast<int*>(bars + NBAR + 1);          // request, row tile
     float4* sc = reinterpret_cast<float4*>(smem + L::SC_OFF);
@@ -149,18 +164,19 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
         __syncwarp();
     }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kKStages; s++) { mbar_init(bar(KF + s), 1); mbar_init(bar(KE + s), 1); }
+        for (int s = 0; s < kKStages; s++) { mbar_init(bar(KF + s), 1); mbar_init(bar(KE + s), 2); }
         for (int s = 0; s < kVStages; s++) { mbar_init(bar(VF + s), 1); mbar_init(bar(VE + s), 4); }
         for (int s = 0; s < 2; s++) {
             mbar_init(bar(HF + s), 4);
-            mbar_init(bar(HE + s), 1);
+            mbar_init(bar(HE + s), 2);
+            mbar_init(bar(DR + s), 1);
+            mbar_init(bar(TN + s), 1);
             mbar_init(bar(SF + s), 1);
             mbar_init(bar(PF + s), 4);
             mbar_init(bar(OD + s), 1);
             mbar_init(bar(QF + s), 4);
         }
         for (int s = 0; s < kScStages; s++) mbar_init(bar(SC + s), 1);
-        mbar_init(bar(DR), 1);
         fence_barrier_init();
         prefetch_tmap(&P.tm_k);
         prefetch_tmap(&P.tm_v);
@@ -195,7 +211,6 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax
-        reg_inc<208>();
         const int w = warp >> 2, q = warp & 3;
         const int row = row0 + w * kM + q * 32 + lane, i = row / G, a = row - i * G;
         const bool there = i < n;
@@ -246,40 +261,51 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
         for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
         float m = -INFINITY, l = 0.0f;
         for (int t = 0; t < nk[w] && ok; t++) {
-            if (!mbar_wait(bar(SC + t % kScStages), (t / kScStages) & 1, &g_attn_prefill_err)) { ok = false; break; }
-            if (!mbar_wait(bar(SF + w), t & 1, &g_attn_prefill_err)) { ok = false; break; }
+            if (!warp_wait(bar(SC + t % kScStages), (t / kScStages) & 1)) { ok = false; break; }
+            if (!warp_wait(bar(SF + w), t & 1)) { ok = false; break; }
             tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; c++) tmem_ld32(s_addr + c * 32, s[c]);
-            tmem_wait_ld();
             const float4* con = sc + (t % kScStages) * 8;             // (k scale, log2 v scale, 1 / v scale) per 16 keys
             const int lim = seen - t * kN;
-            if (least < (t + 1) * kN) {           // some row of the warp does not see the whole tile
-#pragma unroll
-                for (int e = 0; e < kN; e++)
-                    if (e >= lim) s[e >> 5][e & 31] = 0xFF800000u;    // -inf: its score is -inf, its p 0
-            }
-            // largest score of the row: the scale of 16 keys is positive, so their raw maximum gives it
+            const bool edge = least < (t + 1) * kN;                   // some row of the warp does not see the whole tile
+            // S is read from TMEM twice, 64 keys at a time in rolled loops, instead of once into 128
+            // registers: unrolled over the tile, the code of the roles together outgrew the
+            // instruction cache, and the MMA warps' fetches held up the tensor cores.
+            // Largest score of the row: the scale of 16 keys is positive, so their raw maximum gives it.
             float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 2; c++) {
+                uint32_t s[2][32];
+                tmem_ld32(s_addr + c * 64, s[0]);
+                tmem_ld32(s_addr + c * 64 + 32, s[1]);
+                tmem_wait_ld();
+                if (edge) {
+                    const int lm = lim - c * 64;
 #pragma unroll
-            for (int gr = 0; gr < 8; gr++) {
-                const float4 cn = con[gr];
-                const uint32_t* x = s[gr >> 1] + (gr & 1) * 16;
-                float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
-#pragma unroll
-                for (int e = 6; e < 14; e += 4) {
-                    g0 = max3(__float_as_uint(g0), x[e], x[e + 1]);
-                    g1 = max3(__float_as_uint(g1), x[e + 2], x[e + 3]);
+                    for (int e = 0; e < 64; e++)
+                        if (e >= lm) s[e >> 5][e & 31] = 0xFF800000u;               // -inf: its score is -inf, its p 0
+                    tmem_st32(s_addr + c * 64, s[0]);
+                    tmem_st32(s_addr + c * 64 + 32, s[1]);
                 }
-                g0 = max3(__float_as_uint(g0), x[14], x[15]);
-                mx = fmaxf(mx, fmaf(fmaxf(g0, g1), fmaxf(crow * cn.x, kTiny), cn.y));
+#pragma unroll
+                for (int gr = 0; gr < 4; gr++) {
+                    const float4 cn = con[c * 4 + gr];
+                    const uint32_t* x = s[gr >> 1] + (gr & 1) * 16;
+                    float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
+#pragma unroll
+                    for (int e = 6; e < 14; e += 4) {
+                        g0 = max3(__float_as_uint(g0), x[e], x[e + 1]);
+                        g1 = max3(__float_as_uint(g1), x[e + 2], x[e + 3]);
+                    }
+                    g0 = max3(__float_as_uint(g0), x[14], x[15]);
+                    mx = fmaxf(mx, fmaf(fmaxf(g0, g1), fmaxf(crow * cn.x, kTiny), cn.y));
+                }
             }
+            if (edge) tmem_wait_st();
             const bool raise = mx > m + kGrow || m == -INFINITY;
             const float m2 = raise ? fmaxf(mx, m) : m;
             const float f = m == -INFINITY ? 0.0f : ex2(m - m2);
             if (t > 0 && __any_sync(0xffffffffu, m2 != m)) {          // O so far, under the new maximum
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 32; c++) {
                     uint32_t o[32];
                     tmem_ld32(o_addr + c * 32, o);
@@ -292,13 +318,15 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             l *= f;
             m = m2;
             const float off = m == -INFINITY ? 0.0f : kPShift - m;
+#pragma unroll 1
+            for (int c = 0; c < 2; c++) {         // 64 keys: 32 columns of P, over S columns that are read by now
+                uint32_t s[2][32], pk[32];
+                tmem_ld32(s_addr + c * 64, s[0]);
+                tmem_ld32(s_addr + c * 64 + 32, s[1]);
+                tmem_wait_ld();
 #pragma unroll
-            for (int half = 0; half < 2; half++) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int gg = 0; gg < 4; gg++) {
-                    const int gr = half * 4 + gg;
-                    const float4 cn = con[gr];
+                for (int gr = 0; gr < 4; gr++) {
+                    const float4 cn = con[c * 4 + gr];
                     const float ca = fmaxf(crow * cn.x, kTiny), cb = cn.y + off;
                     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
@@ -307,11 +335,11 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                         const float p1 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e + 1]), ca, cb));
                         s0 += p0;
                         s1 += p1;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[gg * 8 + e / 2]) : "f"(p1), "f"(p0));
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[gr * 8 + e / 2]) : "f"(p1), "f"(p0));
                     }
                     l = fmaf(s0 + s1, cn.z, l);
                 }
-                tmem_st32(s_addr + half * 32, pk);
+                tmem_st32(s_addr + c * 32, pk);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -319,7 +347,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             if (lane == 0) mbar_arrive(bar(PF + w));
         }
         // ---- output
-        if (nk[w] > 0 && ok) ok = mbar_wait(bar(OD + w), 0, &g_attn_prefill_err);
+        if (nk[w] > 0 && ok) ok = warp_wait(bar(OD + w), 0);
         tc_fence_after();
         const float r = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
         uint16_t* out = P.a.out + (int64_t)(q0 + i) * P.a.ldo + (int64_t)(h * G + a) * D;
@@ -356,13 +384,12 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
         tc_fence_before();
     } else if (warp < 12) {
         // ------------------------------------------------- V codes to f16
-        reg_dec<48>();
         const int tid = threadIdx.x - 256;
         bool ok = true;
         for (int t = 0; t < nkv && ok; t++) {
             const int st = t % kVStages, hb = t & 1;
-            if (!mbar_wait<false>(bar(VF + st), (t / kVStages) & 1, &g_attn_prefill_err)) { ok = false; break; }
-            if (!mbar_wait(bar(HE + hb), ((t >> 1) & 1) ^ 1, &g_attn_prefill_err)) { ok = false; break; }
+            if (!warp_wait(bar(VF + st), (t / kVStages) & 1)) { ok = false; break; }
+            if (!warp_wait(bar(HE + hb), ((t >> 1) & 1) ^ 1)) { ok = false; break; }
             const uint8_t* src = smem + L::V_OFF + st * L::KT;
             uint8_t* dst = smem + L::VH_OFF + hb * L::VH;
             const int live = Lk - t * kN;         // rows behind the last key were never written: zeros
@@ -393,7 +420,6 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             }
         }
     } else {
-        reg_dec<48>();
         if (warp == 12) {
             // ------------------------------------------------- TMA, scales
             const int32_t* tab = P.a.block_table + (int64_t)b * P.a.ld_table;
@@ -416,7 +442,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                     const float kscale = __ldg(P.a.kv.k_scale + i), vscale = fmaxf(__ldg(P.a.kv.v_scale + i), 1.2e-38f);
                     cn = make_float4(kscale, __log2f(vscale), __frcp_rn(vscale), 0.0f);
                 }
-                ok = mbar_wait(bar(KE + ks), ((t / kKStages) & 1) ^ 1, &g_attn_prefill_err);
+                ok = warp_wait(bar(KE + ks), ((t / kKStages) & 1) ^ 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(bar(KF + ks), L::KT);
@@ -429,7 +455,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                     for (int j = 0; j < reps; j++) sc[(t % kScStages) * 8 + lane * reps + j] = cn;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(SC + t % kScStages));
-                ok = mbar_wait(bar(VE + vs), ((t / kVStages) & 1) ^ 1, &g_attn_prefill_err);
+                ok = warp_wait(bar(VE + vs), ((t / kVStages) & 1) ^ 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(bar(VF + vs), L::KT);
@@ -442,55 +468,57 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             for (int j = max(0, t - kKStages); j < t; j++) mbar_wait(bar(KF + j % kKStages), (j / kKStages) & 1, &g_attn_prefill_err);
             for (int j = max(0, t - kVStages); j < t; j++) mbar_wait(bar(VF + j % kVStages), (j / kVStages) & 1, &g_attn_prefill_err);
             if (!ok) mbar_wait(bar(KF + t % kKStages), (t / kKStages) & 1, &g_attn_prefill_err);
-        } else if (warp == 13) {
-            // -------------------------------------------------------- MMA
+        } else if (warp >= 14) {
+            // ----------------------------- MMA of row tile w: one warp each
+            const int w = warp - 14, nkw = nk[w];
             if (lane == 0 && nkv > 0) {
+                const uint32_t sd = tmem + L::S_COL + w * kN, od = tmem + L::O_COL + w * D;
+                const uint32_t qa = sdesc_k_lo<D>(sbase + L::Q_OFF + w * 2 * L::Q), k_lo = sdesc_k_lo<D>(sbase + L::K_OFF),
+                               v_lo = sdesc_v_lo(sbase + L::VH_OFF);
                 bool ok = true;
-                auto wait = [&](int i, uint32_t parity) { ok = ok && mbar_wait(bar(i), parity, &g_attn_prefill_err); };
-                auto score = [&](int w, int t) {  // S of row tile w and key tile t, both parts of q
-                    const uint32_t d = tmem + L::S_COL + w * kN, ka = sbase + L::K_OFF + (t % kKStages) * L::KT;
+                auto wait = [&](int i, uint32_t parity) { ok = ok && warp_wait(bar(i), parity); };
+                auto score = [&](uint32_t ka) {   // S, both parts of q
 #pragma unroll
-                    for (int part = 0; part < 2; part++)
+                    for (int k = 0; k < D / 32; k++) mma_s(sd, qa + k * 2, ka + k * 2, sdesc_k_hi<D>(), L::IDESC_S, k > 0);
 #pragma unroll
-                        for (int k = 0; k < D / 32; k++)
-                            mma_f8f6f4(d, sdesc_k<D>(sbase + L::Q_OFF + (w * 2 + part) * L::Q) + k * 2, sdesc_k<D>(ka) + k * 2,
-                                       L::IDESC_S, part + k > 0);
+                    for (int k = 0; k < D / 32; k++) mma_s(sd, qa + (L::Q >> 4) + k * 2, ka + k * 2, sdesc_k_hi<D>(), L::IDESC_S, true);
                     tc_commit(bar(SF + w));
                 };
-                auto value = [&](int w, int t) {  // O += P V
-                    const uint32_t pa = tmem + L::S_COL + w * kN, va = sbase + L::VH_OFF + (t & 1) * L::VH;
-#pragma unroll
-                    for (int k = 0; k < kN / 16; k++)
-                        mma_f16_ts(tmem + L::O_COL + w * D, pa + k * 8, sdesc_v(va + k * 2048), L::IDESC_O, t > 0 || k > 0);
-                    if (t + 1 == nk[w]) tc_commit(bar(OD + w));
-                };
-                for (int w = 0; w < 2; w++)
-                    if (nk[w] > 0) wait(QF + w, 0);
+                // A row tile that sees fewer key tiles than its partner still releases every stage, and
+                // only after it was filled: an arrival ahead of its phase would count for an earlier one.
                 wait(KF, 0);
-                tc_fence_after();
-                if (ok) {
-                    for (int w = 0; w < 2; w++)
-                        if (nk[w] > 0) score(w, 0);
-                    tc_commit(bar(KE));
+                if (w == 1) wait(TN + 1, 0);
+                if (nkw > 0) {
+                    wait(QF + w, 0);
+                    tc_fence_after();
+                    if (ok) score(k_lo);
                 }
+                mbar_arrive(bar(TN + 1 - w));
+                tc_commit(bar(KE));
+                int ks = 0;                       // stage and phase of the next key tile
+                uint32_t kph = 0;
                 for (int t = 0; t < nkv && ok; t++) {
-                    if (t + 1 < nkv) wait(KF + (t + 1) % kKStages, ((t + 1) / kKStages) & 1);
+                    if (++ks == kKStages) { ks = 0; kph ^= 1; }
                     wait(HF + (t & 1), (t >> 1) & 1);
-                    for (int w = 0; w < 2 && ok; w++) {
-                        if (t < nk[w]) {
-                            wait(PF + w, t & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            value(w, t);
-                            if (t + 1 < nk[w]) score(w, t + 1);
-                        }
+                    if (t + 1 < nkv) wait(KF + ks, kph);
+                    wait(TN + w, (t + w) & 1);    // w = 0: after the partner's batch t, w = 1: t + 1
+                    if (t < nkw) {
+                        wait(PF + w, t & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t va = v_lo + (t & 1) * (L::VH >> 4);
+                        mma_o(od, sd, va, L::IDESC_O, t > 0);                        // O += P V
+#pragma unroll
+                        for (int k = 1; k < kN / 16; k++) mma_o(od, sd + k * 8, va + k * (2048 >> 4), L::IDESC_O, true);
+                        if (t + 1 < nkw) score(k_lo + ks * (L::KT >> 4));
+                        else tc_commit(bar(OD + w));
                     }
-                    if (!ok) break;
+                    mbar_arrive(bar(TN + 1 - w));
                     tc_commit(bar(HE + (t & 1)));
-                    if (t + 1 < nkv) tc_commit(bar(KE + (t + 1) % kKStages));
+                    if (t + 1 < nkv) tc_commit(bar(KE + ks));
                 }
-                tc_commit(bar(DR));               // no MMA outlives the CTA's tensor memory
-                mbar_wait(bar(DR), 0, &g_attn_prefill_err);
+                tc_commit(bar(DR + w));           // no MMA outlives the CTA's tensor memory
+                mbar_wait(bar(DR + w), 0, &g_attn_prefill_err);
             }
             __syncwarp();
         }
