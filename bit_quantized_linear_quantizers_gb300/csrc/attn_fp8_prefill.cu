@@ -17,8 +17,8 @@
 //                per warp, f16x2.e4m3x2 2.25, f16x2.f32 2.0): more than the MMAs take.
 // The page's value scale goes into the exponent, as in the decode kernel:
 //   t = x log2(e) + log2 sv, p = 2^(t - m + 8), O = sum p c, l = sum p / sv.
-// m is raised only when a row's maximum has grown by more than 2^6 (p stays
-// below 2^15), which spares most rescalings of O.
+// m is raised only when p outgrows f16 (sums of 16 above 2^15), which spares the
+// maximum of most tiles and most rescalings of O.
 //
 // The two row tiles alternate on the tensor cores: while one's softmax runs, the
 // other's P V and next S do. S's TMEM columns hold P afterwards.
@@ -36,7 +36,8 @@ __device__ unsigned int g_attn_prefill_err;
 constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 14 and 15 MMA
 constexpr int kM = 128, kRows = 2 * kM, kN = 128; // rows of a tile, of a CTA; keys of a tile
 constexpr int kKStages = 3, kVStages = 2, kScStages = 4;
-constexpr float kPShift = 8.0f, kGrow = 6.0f;
+constexpr float kPShift = 8.0f;
+constexpr float kMost = 32768.0f;                  // a sum of 16 p up to which each fits f16 (largest 65504)
 constexpr float kTiny = 1e-30f;                   // least factor of a raw score: -inf stays -inf under it
 
 struct PrefillParams {
@@ -93,11 +94,20 @@ __device__ __forceinline__ void mma_o(uint32_t d, uint32_t a, uint32_t b_lo, uin
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }"
                  ::"r"(d), "r"(a), "r"(b_lo), "r"(kDescVHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
-__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
-    return r;
+// (a, b) * s + c and (a, b) += (x, y) on the paired fp32 instructions.
+__device__ __forceinline__ void fma2(float a, float b, float s, float c, float& x, float& y) {
+    asm("{ .reg .b64 v, m, k, r;\n\tmov.b64 v, {%2, %3}; mov.b64 m, {%4, %4}; mov.b64 k, {%5, %5};\n\t"
+        "fma.rn.f32x2 r, v, m, k;\n\tmov.b64 {%0, %1}, r; }"
+        : "=f"(x), "=f"(y) : "f"(a), "f"(b), "f"(s), "f"(c));
 }
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+    asm("{ .reg .b64 v, r;\n\tmov.b64 v, {%0, %1}; mov.b64 r, {%2, %3};\n\t"
+        "add.rn.f32x2 v, v, r;\n\tmov.b64 {%0, %1}, v; }"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+
+template <int REGS> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 
 // The bounded wait of this kernel: few polls with a long suspend hint.
 constexpr uint32_t kHintNs = 1000, kPolls = 1u<<21;
@@ -211,6 +221,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax
+        reg_inc<184>();                           // 8 x 184 + 8 x 72 = 16 x 128 registers a lane
         const int w = warp >> 2, q = warp & 3;
         const int row = row0 + w * kM + q * 32 + lane, i = row / G, a = row - i * G;
         const bool there = i < n;
@@ -267,80 +278,87 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             const float4* con = sc + (t % kScStages) * 8;             // (k scale, log2 v scale, 1 / v scale) per 16 keys
             const int lim = seen - t * kN;
             const bool edge = least < (t + 1) * kN;                   // some row of the warp does not see the whole tile
-            // S is read from TMEM twice, 64 keys at a time in rolled loops, instead of once into 128
-            // registers: unrolled over the tile, the code of the roles together outgrew the
-            // instruction cache, and the MMA warps' fetches held up the tensor cores.
-            // Largest score of the row: the scale of 16 keys is positive, so their raw maximum gives it.
-            float mx = -INFINITY;
+            // One pass without a maximum: p under the m so far. Only where a sum shows that p may have
+            // grown past f16's range (or no m is known yet) is the tile's maximum taken, m raised,
+            // O scaled and the pass made again. P stays in registers until all of S is read and
+            // found in range, since it takes S's columns.
+            uint32_t pk[64];
+            float sum;
+            bool raise = m == -INFINITY && lim > 0;
+            while (true) {
+                if (__any_sync(0xffffffffu, raise)) {
+                    float mx = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < 2; c++) {
+                    for (int c = 0; c < 4; c++) {
+                        uint32_t x[32];
+                        tmem_ld32(s_addr + c * 32, x);
+                        const float4 c0 = con[c * 2], c1 = con[c * 2 + 1];
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e++) {
+                            const float4& cn = e < 16 ? c0 : c1;
+                            const float v = fmaf(__uint_as_float(x[e]), fmaxf(crow * cn.x, kTiny), cn.y);
+                            if (c * 32 + e < lim) mx = fmaxf(mx, v);
+                        }
+                    }
+                    const float m2 = raise ? fmaxf(m, mx) : m;
+                    const float f = m == -INFINITY ? 0.0f : ex2(m - m2);
+                    if (t > 0) {                  // O so far, under the new maximum
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; c++) {
+                            uint32_t o[32];
+                            tmem_ld32(o_addr + c * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(o_addr + c * 32, o);
+                        }
+                    }
+                    l *= f;
+                    m = m2;
+                }
+                const float off = m == -INFINITY ? 0.0f : kPShift - m;
+                float top = 0.0f;
                 uint32_t s[2][32];
-                tmem_ld32(s_addr + c * 64, s[0]);
-                tmem_ld32(s_addr + c * 64 + 32, s[1]);
-                tmem_wait_ld();
-                if (edge) {
-                    const int lm = lim - c * 64;
+                sum = 0.0f;
+                tmem_ld32(s_addr, s[0]);
 #pragma unroll
-                    for (int e = 0; e < 64; e++)
-                        if (e >= lm) s[e >> 5][e & 31] = 0xFF800000u;               // -inf: its score is -inf, its p 0
-                    tmem_st32(s_addr + c * 64, s[0]);
-                    tmem_st32(s_addr + c * 64 + 32, s[1]);
-                }
-#pragma unroll
-                for (int gr = 0; gr < 4; gr++) {
-                    const float4 cn = con[c * 4 + gr];
-                    const uint32_t* x = s[gr >> 1] + (gr & 1) * 16;
-                    float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
-#pragma unroll
-                    for (int e = 6; e < 14; e += 4) {
-                        g0 = max3(__float_as_uint(g0), x[e], x[e + 1]);
-                        g1 = max3(__float_as_uint(g1), x[e + 2], x[e + 3]);
-                    }
-                    g0 = max3(__float_as_uint(g0), x[14], x[15]);
-                    mx = fmaxf(mx, fmaf(fmaxf(g0, g1), fmaxf(crow * cn.x, kTiny), cn.y));
-                }
-            }
-            if (edge) tmem_wait_st();
-            const bool raise = mx > m + kGrow || m == -INFINITY;
-            const float m2 = raise ? fmaxf(mx, m) : m;
-            const float f = m == -INFINITY ? 0.0f : ex2(m - m2);
-            if (t > 0 && __any_sync(0xffffffffu, m2 != m)) {          // O so far, under the new maximum
-#pragma unroll 1
-                for (int c = 0; c < D / 32; c++) {
-                    uint32_t o[32];
-                    tmem_ld32(o_addr + c * 32, o);
+                for (int c = 0; c < 4; c++) {
+                    uint32_t* x = s[c & 1];
                     tmem_wait_ld();
+                    if (c < 3) tmem_ld32(s_addr + (c + 1) * 32, s[(c + 1) & 1]);    // in flight during this chunk
+                    if (edge) {
 #pragma unroll
-                    for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st32(o_addr + c * 32, o);
-                }
-            }
-            l *= f;
-            m = m2;
-            const float off = m == -INFINITY ? 0.0f : kPShift - m;
-#pragma unroll 1
-            for (int c = 0; c < 2; c++) {         // 64 keys: 32 columns of P, over S columns that are read by now
-                uint32_t s[2][32], pk[32];
-                tmem_ld32(s_addr + c * 64, s[0]);
-                tmem_ld32(s_addr + c * 64 + 32, s[1]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int gr = 0; gr < 4; gr++) {
-                    const float4 cn = con[c * 4 + gr];
-                    const float ca = fmaxf(crow * cn.x, kTiny), cb = cn.y + off;
-                    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float p0 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e]), ca, cb));
-                        const float p1 = ex2(fmaf(__uint_as_float(s[gr >> 1][(gr & 1) * 16 + e + 1]), ca, cb));
-                        s0 += p0;
-                        s1 += p1;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[gr * 8 + e / 2]) : "f"(p1), "f"(p0));
+                        for (int e = 0; e < 32; e++)
+                            if (c * 32 + e >= lim) x[e] = 0xFF800000u;              // -inf: its score is -inf, its p 0
                     }
-                    l = fmaf(s0 + s1, cn.z, l);
+#pragma unroll
+                    for (int gr = 0; gr < 2; gr++) {
+                        const float4 cn = con[c * 2 + gr];
+                        const uint32_t* y = x + gr * 16;
+                        const float ca = fmaxf(crow * cn.x, kTiny), cb = cn.y + off;
+                        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float p0, p1;
+                            fma2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]), ca, cb, p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            add2(s0, s1, p0, p1);
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[c * 16 + gr * 8 + e / 2]) : "f"(p1), "f"(p0));
+                        }
+                        const float both = s0 + s1;
+                        top = fmaxf(top, both);
+                        sum = fmaf(both, cn.z, sum);
+                    }
                 }
-                tmem_st32(s_addr + c * 32, pk);
+                // a p of the next pass is at most 2^8: no third one
+                raise = top > kMost && there;
+                if (!__any_sync(0xffffffffu, raise)) break;
             }
+            l += sum;
+            tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+            tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -384,6 +402,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
         tc_fence_before();
     } else if (warp < 12) {
         // ------------------------------------------------- V codes to f16
+        reg_dec<72>();
         const int tid = threadIdx.x - 256;
         bool ok = true;
         for (int t = 0; t < nkv && ok; t++) {
@@ -420,6 +439,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             }
         }
     } else {
+        reg_dec<72>();
         if (warp == 12) {
             // ------------------------------------------------- TMA, scales
             const int32_t* tab = P.a.block_table + (int64_t)b * P.a.ld_table;
