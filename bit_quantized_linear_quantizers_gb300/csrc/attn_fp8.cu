@@ -5,6 +5,8 @@
 #include "qz_internal.cuh"
 #include "qz_paged.cuh"
 
+#include <algorithm>
+
 namespace qz {
 
 namespace {
@@ -14,13 +16,16 @@ namespace {
 constexpr int kDecodeRows = 64;
 } // namespace
 
-size_t ws_attn_paged(int64_t, int64_t) { return ws_attn_decode(); }
+// The two kernels of a call run one after the other and share the workspace.
+size_t ws_attn_paged(int64_t rows, int64_t) {
+    return rows <= kDecodeRows ? ws_attn_decode() : std::max(ws_attn_decode(), ws_attn_prefill());
+}
 
 qz_status attn_paged_launch(const AttnArgs& a, void* ws, cudaStream_t st) {
     const int64_t rows = (int64_t)a.max_q * (a.heads_q / a.kv.heads);
     if (rows <= kDecodeRows) return attn_decode_launch(a, kDecodeRows, ws, st);
-    if (a.B == 1) return attn_prefill_launch(a, 1, st);          // one request: no second launch for what it is not
-    QZ_TRY(attn_prefill_launch(a, kDecodeRows + 1, st));
+    if (a.B == 1) return attn_prefill_launch(a, 1, ws, st);          // one request: no second launch for what it is not
+    QZ_TRY(attn_prefill_launch(a, kDecodeRows + 1, ws, st));
     return attn_decode_launch(a, kDecodeRows, ws, st);
 }
 

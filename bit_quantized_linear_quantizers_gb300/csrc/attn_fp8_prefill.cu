@@ -22,6 +22,12 @@
 //
 // The two row tiles alternate on the tensor cores: while one's softmax runs, the
 // other's P V and next S do. S's TMEM columns hold P afterwards.
+//
+// One CTA per SM stays for the launch: a scheduler warp takes the items (row tile,
+// KV head, part of the keys) of CTAs not yet launched (cluster launch control), the
+// longest first, one item ahead of the roles, so copies and q of the next item run
+// under the end of the last one. A launch of few row tiles splits their keys into
+// parts, whose states a second launch joins in order.
 #include "qz_internal.cuh"
 #include "attn_fp8.cuh"
 
@@ -33,9 +39,10 @@ namespace {
 
 __device__ unsigned int g_attn_prefill_err;
 
-constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 14 and 15 MMA
+constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 13 items, 14-15 MMA
 constexpr int kM = 128, kRows = 2 * kM, kN = 128; // rows of a tile, of a CTA; keys of a tile
 constexpr int kKStages = 3, kVStages = 2, kScStages = 4;
+constexpr int kSplitKeys = 512;
 constexpr float kPShift = 8.0f;
 constexpr float kMost = 32768.0f;                  // a sum of 16 p up to which each fits f16 (largest 65504)
 constexpr float kTiny = 1e-30f;                   // least factor of a raw score: -inf stays -inf under it
@@ -46,6 +53,14 @@ struct PrefillParams {
     int shift;
     int min_rows;                                 // requests with fewer rows per KV head are not taken
     int tiles;                                    // upper bound of row tiles over all requests
+    int splits;                                   // parts of an item's keys; with more than one:
+    int* head;                                    //   [tiles * heads][2] request (-1: none) and first row
+    float* part;                                  //   [tiles * heads][splits] states: O [256][D], m [256], l [256]
+};
+
+// What a role reads about an item.
+struct Item {
+    int b, row0, h, q0, n, L, t0, nk[2], part;    // t0: first key tile; nk: key tiles of each row tile; part: -1 or its state
 };
 
 template <int D>
@@ -60,6 +75,7 @@ struct PrefillLayout {
     static constexpr int SC_OFF = VH_OFF + 2 * VH;                  // [stage][8] float4: scales of 16 keys
     static constexpr int BAR_OFF = SC_OFF + kScStages * 8 * 16;
     static constexpr int SMEM = BAR_OFF + 512 + 1024;
+    static constexpr int PART = kRows * D + 2 * kRows;              // floats of a part's state
     static constexpr uint32_t S_COL = 0, O_COL = 256;               // TMEM columns: S0 S1 O0 O1
     static constexpr uint32_t IDESC_S = idesc_dense(0u, 0u, kM, kN);                     // E4M3 x E4M3
     static constexpr uint32_t IDESC_O = idesc_dense(0u, 0u, kM, D) | 1u << 16;           // f16 x f16, B MN-major
@@ -122,6 +138,23 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return false;
 }
 
+// Cluster launch control: asks for the item of a CTA that has not been launched.
+__device__ __forceinline__ void try_cancel(uint32_t result, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(result), "r"(bar) : "memory");
+}
+// Its blockIdx.x, or -1 where there is none left.
+__device__ __forceinline__ int canceled_cta(uint32_t result) {
+    uint32_t ok, x = 0;
+    asm volatile("{ .reg .pred p; .reg .b128 r;\n\t"
+                 "ld.shared.b128 r, [%2];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r; }"
+                 : "=r"(ok), "=r"(x) : "r"(result) : "memory");
+    return ok ? (int)x : -1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
@@ -131,69 +164,41 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
     const uint32_t sbase = smem_u32(smem);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     auto bar = [&](int i) { return smem_u32(bars + i); };
-    // barriers: K full/empty, raw V full/empty, widened V full/empty, scales full, S full, P full, O done, q, drain
+    // barriers: K full/empty, raw V full/empty, widened V full/empty, scales full, S full, P full, O done, q, drain,
+    // turn, item full/empty, scheduler
     constexpr int KF = 0, KE = KF + kKStages, VF = KE + kKStages, VE = VF + kVStages, HF = VE + kVStages, HE = HF + 2,
-                  SC = HE + 2, SF = SC + kScStages, PF = SF + 2, OD = PF + 2, QF = OD + 2, DR = QF + 2, TN = DR + 2, NBAR = TN + 2;
+                  SC = HE + 2, SF = SC + kScStages, PF = SF + 2, OD = PF + 2, QF = OD + 2, DR = QF + 2, TN = DR + 2,
+                  IF = TN + 2, IE = IF + 2, CB = IE + 2, NBAR = CB + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
-    int* s_item = reinterpret_cast<int*>(bars + NBAR + 1);          // request, row tile
+    uint8_t* canceled = smem + L::BAR_OFF + 384;                    // 16 bytes
+    Item* items = reinterpret_cast<Item*>(smem + L::BAR_OFF + 400); // two: a role's current one stays here, not in registers
     float4* sc = reinterpret_cast<float4*>(smem + L::SC_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = P.a.heads_q / P.a.kv.heads;
-    pdl_wait();
-    pdl_trigger();
-
-    // ---- this CTA's item: KV head and row tile, the last row tiles (the longest under the causal rule) first
-    const int h = blockIdx.x % P.a.kv.heads;
-    if (warp == 13) {
-        const int want = P.tiles - 1 - (int)(blockIdx.x / P.a.kv.heads);
-        int before = 0;
-        if (lane == 0) s_item[0] = -1;
-        __syncwarp();
-        for (int b0 = 0; b0 < P.a.B; b0 += 32) {
-            const int b = b0 + lane;
-            int own = 0;
-            if (b < P.a.B) {
-                const int n = min(__ldg(P.a.cu_q + b + 1) - __ldg(P.a.cu_q + b), P.a.max_q);
-                const int64_t rows = (int64_t)max(n, 0) * G;
-                own = rows < P.min_rows ? 0 : (int)((rows + kRows - 1) / kRows);
-            }
-            int v = own;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            const int first = before + v - own;
-            if (want >= first && want < first + own) {
-                s_item[0] = b;
-                s_item[1] = want - first;
-            }
-            before += __shfl_sync(0xffffffffu, v, 31);
-            if (before > want) break;
-        }
-        __syncwarp();
-    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kKStages; s++) { mbar_init(bar(KF + s), 1); mbar_init(bar(KE + s), 2); }
         for (int s = 0; s < kVStages; s++) { mbar_init(bar(VF + s), 1); mbar_init(bar(VE + s), 4); }
         for (int s = 0; s < 2; s++) {
             mbar_init(bar(HF + s), 4);
             mbar_init(bar(HE + s), 2);
-            mbar_init(bar(DR + s), 1);
-            mbar_init(bar(TN + s), 1);
             mbar_init(bar(SF + s), 1);
             mbar_init(bar(PF + s), 4);
             mbar_init(bar(OD + s), 1);
             mbar_init(bar(QF + s), 4);
+            mbar_init(bar(DR + s), 1);
+            mbar_init(bar(TN + s), 1);
         }
         for (int s = 0; s < kScStages; s++) mbar_init(bar(SC + s), 1);
+        for (int s = 0; s < 2; s++) {
+            mbar_init(bar(IF + s), 1);
+            mbar_init(bar(IE + s), 15);           // 8 softmax, 4 widening, 1 TMA and 2 MMA warps
+        }
+        mbar_init(bar(CB), 1);
         fence_barrier_init();
         prefetch_tmap(&P.tm_k);
         prefetch_tmap(&P.tm_v);
     }
-    __syncthreads();
-    const int b = s_item[0];
-    if (b < 0) return;                            // fewer row tiles than the bound: nothing here
     if (warp == 13) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -202,343 +207,510 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-
-    const int row0 = s_item[1] * kRows;
-    const int q0 = __ldg(P.a.cu_q + b);
-    int n = min(__ldg(P.a.cu_q + b + 1) - q0, P.a.max_q);
-    n = q0 < 0 ? 0 : (int)min((int64_t)n, P.a.tokens - q0);
-    const int Lk = (int)min((int64_t)max(__ldg(P.a.kv_lens + b), 0), (int64_t)P.a.max_blocks << P.shift);
-    // key tiles of each row tile: up to what its last row sees
-    int nk[2];
-#pragma unroll
-    for (int w = 0; w < 2; w++) {
-        const int first = row0 + w * kM, last = min(first + kM, n * G) - 1;
-        const int sees = last < first ? 0 : P.a.causal ? min(max(Lk - n + last / G + 1, 0), Lk) : Lk;
-        nk[w] = (sees + kN - 1) / kN;
-    }
-    const int nkv = max(nk[0], nk[1]);
+    pdl_wait();
+    pdl_trigger();
     const int pages_tile = kN >> P.shift;         // boxes of a key tile
+
+    // The k-th item of this CTA: is there one (its b >= 0), and the role's leave of it.
+    auto has_item = [&](int k) { return warp_wait(bar(IF + (k & 1)), (k >> 1) & 1) && items[k & 1].b >= 0; };
+    auto done_item = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(IE + (k & 1)));
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax
         reg_inc<184>();                           // 8 x 184 + 8 x 72 = 16 x 128 registers a lane
         const int w = warp >> 2, q = warp & 3;
-        const int row = row0 + w * kM + q * 32 + lane, i = row / G, a = row - i * G;
-        const bool there = i < n;
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t s_addr = lane_base + L::S_COL + w * kN, o_addr = lane_base + L::O_COL + w * D;
-        float crow = 0.0f;
+        const int r = q * 32 + lane;              // row of the tile
+        auto q_row = [&](const Item& x, int i) {  // this thread's row of q: token i
+            return P.a.q + (int64_t)(x.q0 + i) * P.a.ldq + (int64_t)(x.h * G + x.row0 + w * kM + r - i * G) * D;
+        };
+        bool more = has_item(0);
+        uint32_t od = 0;                          // phase of the row tile's O
+        int tw = 0;                               // key tiles that this row tile has taken, over all items
+        int tc = 0;                               // key tiles of the CTA before this item
         bool ok = true;
-        if (nk[w] > 0) {
-            // the row's two E4M3 parts into shared memory, in the swizzled order of the K-major operand
-            const uint16_t* src = P.a.q + (int64_t)(q0 + i) * P.a.ldq + (int64_t)(h * G + a) * D;
-            uint4 raw[D / 8];
-            float m = 0.0f;
+        for (int k = 0; more; k++) {
+            const Item& it = items[k & 1];
+            const int nk = it.nk[w];
+            const int i = (it.row0 + w * kM + r) / G;
+            const bool there = i < it.n;
+            float crow = 0.0f;
+            if (nk > 0) {
+                uint4 raw[D / 8];                 // this thread's row of q, zeros where there is none
+                const uint16_t* src = q_row(it, i);
 #pragma unroll
-            for (int c = 0; c < D / 8; c++) {
-                raw[c] = there ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-                const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                for (int c = 0; c < D / 8; c++)
+                    raw[c] = there ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+                // the row's two E4M3 parts into shared memory, in the swizzled order of the K-major operand
+                // (the last S of the item before is complete: this warp has waited for it)
+                float m = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-            }
-            float up, down;
-            row_scale(m, up, down);
-            crow = fabsf(P.a.sm_scale) * kLog2e * down;
-            if (P.a.sm_scale < 0.0f) up = -up;
-            const int r = q * 32 + lane;
-            uint8_t* hi = smem + L::Q_OFF + (w * 2) * L::Q + r * D;
+                for (int c = 0; c < D / 8; c++) {
+                    const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-            for (int c = 0; c < D / 16; c++) {    // 16 channels
-                uint32_t hw[4], lw[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const uint4 x = raw[2 * c + (e >> 1)];
-                    const uint32_t y0 = e & 1 ? x.z : x.x, y1 = e & 1 ? x.w : x.y;
-                    split4(__uint_as_float(y0 << 16) * up, __uint_as_float(y0 & 0xFFFF0000u) * up,
-                           __uint_as_float(y1 << 16) * up, __uint_as_float(y1 & 0xFFFF0000u) * up, hw[e], lw[e]);
+                    for (int e = 0; e < 4; e++)
+                        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
                 }
-                const int ch = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-                *reinterpret_cast<uint4*>(hi + ch * 16) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                *reinterpret_cast<uint4*>(hi + L::Q + ch * 16) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(QF + w));
-        }
-        const int seen = !there ? 0 : P.a.causal ? min(max(Lk - n + i + 1, 0), Lk) : Lk;
-        // the fewest keys that a row of this warp sees (rows past the end see none, and are not stored)
-        int least = there ? seen : 0x7fffffff;
-        for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-        float m = -INFINITY, l = 0.0f;
-        for (int t = 0; t < nk[w] && ok; t++) {
-            if (!warp_wait(bar(SC + t % kScStages), (t / kScStages) & 1)) { ok = false; break; }
-            if (!warp_wait(bar(SF + w), t & 1)) { ok = false; break; }
-            tc_fence_after();
-            const float4* con = sc + (t % kScStages) * 8;             // (k scale, log2 v scale, 1 / v scale) per 16 keys
-            const int lim = seen - t * kN;
-            const bool edge = least < (t + 1) * kN;                   // some row of the warp does not see the whole tile
-            // One pass without a maximum: p under the m so far. Only where a sum shows that p may have
-            // grown past f16's range (or no m is known yet) is the tile's maximum taken, m raised,
-            // O scaled and the pass made again. P stays in registers until all of S is read and
-            // found in range, since it takes S's columns.
-            uint32_t pk[64];
-            float sum;
-            bool raise = m == -INFINITY && lim > 0;
-            while (true) {
-                if (__any_sync(0xffffffffu, raise)) {
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; c++) {
-                        uint32_t x[32];
-                        tmem_ld32(s_addr + c * 32, x);
-                        const float4 c0 = con[c * 2], c1 = con[c * 2 + 1];
-                        tmem_wait_ld();
+                float up, down;
+                row_scale(m, up, down);
+                crow = fabsf(P.a.sm_scale) * kLog2e * down;
+                if (P.a.sm_scale < 0.0f) up = -up;
+                uint8_t* hi = smem + L::Q_OFF + (w * 2) * L::Q + r * D;
 #pragma unroll
-                        for (int e = 0; e < 32; e++) {
-                            const float4& cn = e < 16 ? c0 : c1;
-                            const float v = fmaf(__uint_as_float(x[e]), fmaxf(crow * cn.x, kTiny), cn.y);
-                            if (c * 32 + e < lim) mx = fmaxf(mx, v);
-                        }
+                for (int c = 0; c < D / 16; c++) {                    // 16 channels
+                    uint32_t hw[4], lw[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const uint4 x = raw[2 * c + (e >> 1)];
+                        const uint32_t y0 = e & 1 ? x.z : x.x, y1 = e & 1 ? x.w : x.y;
+                        split4(__uint_as_float(y0 << 16) * up, __uint_as_float(y0 & 0xFFFF0000u) * up,
+                               __uint_as_float(y1 << 16) * up, __uint_as_float(y1 & 0xFFFF0000u) * up, hw[e], lw[e]);
                     }
-                    const float m2 = raise ? fmaxf(m, mx) : m;
-                    const float f = m == -INFINITY ? 0.0f : ex2(m - m2);
-                    if (t > 0) {                  // O so far, under the new maximum
+                    const int ch = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+                    *reinterpret_cast<uint4*>(hi + ch * 16) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                    *reinterpret_cast<uint4*>(hi + L::Q + ch * 16) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(QF + w));
+            }
+            // keys that the row sees, counted from the item's first key tile
+            const int seen = (!there ? 0 : P.a.causal ? min(max(it.L - it.n + i + 1, 0), it.L) : it.L) - it.t0 * kN;
+            // the fewest that a row of this warp sees (rows past the end see none, and are not stored)
+            int least = there ? seen : 0x7fffffff;
+            for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+            float m = -INFINITY, l = 0.0f;
+            for (int t = 0; t < nk; t++, tw++) {
+                const int ts = tc + t;
+                if (!warp_wait(bar(SC + ts % kScStages), (ts / kScStages) & 1)) { ok = false; break; }
+                if (!warp_wait(bar(SF + w), tw & 1)) { ok = false; break; }
+                tc_fence_after();
+                const float4* con = sc + (ts % kScStages) * 8;        // (k scale, log2 v scale, 1 / v scale) per 16 keys
+                const int lim = seen - t * kN;
+                const bool edge = least < (t + 1) * kN;                   // some row of the warp does not see the whole tile
+                // One pass without a maximum: p under the m so far. Only where a sum shows that p may have
+                // grown past f16's range (or no m is known yet) is the tile's maximum taken, m raised,
+                // O scaled and the pass made again. P stays in registers until all of S is read and
+                // found in range, since it takes S's columns.
+                uint32_t pk[64];
+                float sum;
+                bool raise = m == -INFINITY && lim > 0;
+                while (true) {
+                    if (__any_sync(0xffffffffu, raise)) {
+                        float mx = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; c++) {
-                            uint32_t o[32];
-                            tmem_ld32(o_addr + c * 32, o);
+                        for (int c = 0; c < 4; c++) {
+                            uint32_t x[32];
+                            tmem_ld32(s_addr + c * 32, x);
+                            const float4 c0 = con[c * 2], c1 = con[c * 2 + 1];
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(o_addr + c * 32, o);
+                            for (int e = 0; e < 32; e++) {
+                                const float4& cn = e < 16 ? c0 : c1;
+                                const float v = fmaf(__uint_as_float(x[e]), fmaxf(crow * cn.x, kTiny), cn.y);
+                                if (c * 32 + e < lim) mx = fmaxf(mx, v);
+                            }
+                        }
+                        const float m2 = raise ? fmaxf(m, mx) : m;
+                        const float f = m == -INFINITY ? 0.0f : ex2(m - m2);
+                        if (t > 0) {                  // O so far, under the new maximum
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; c++) {
+                                uint32_t o[32];
+                                tmem_ld32(o_addr + c * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(o_addr + c * 32, o);
+                            }
+                        }
+                        l *= f;
+                        m = m2;
+                    }
+                    const float off = m == -INFINITY ? 0.0f : kPShift - m;
+                    float top = 0.0f;
+                    uint32_t s[2][32];
+                    sum = 0.0f;
+                    tmem_ld32(s_addr, s[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        uint32_t* x = s[c & 1];
+                        tmem_wait_ld();
+                        if (c < 3) tmem_ld32(s_addr + (c + 1) * 32, s[(c + 1) & 1]);    // in flight during this chunk
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 32; e++)
+                                if (c * 32 + e >= lim) x[e] = 0xFF800000u;              // -inf: its score is -inf, its p 0
+                        }
+#pragma unroll
+                        for (int gr = 0; gr < 2; gr++) {
+                            const float4 cn = con[c * 2 + gr];
+                            const uint32_t* y = x + gr * 16;
+                            const float ca = fmaxf(crow * cn.x, kTiny), cb = cn.y + off;
+                            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                float p0, p1;
+                                fma2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]), ca, cb, p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                add2(s0, s1, p0, p1);
+                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[c * 16 + gr * 8 + e / 2]) : "f"(p1), "f"(p0));
+                            }
+                            const float both = s0 + s1;
+                            top = fmaxf(top, both);
+                            sum = fmaf(both, cn.z, sum);
                         }
                     }
-                    l *= f;
-                    m = m2;
+                    // a p of the next pass is at most 2^8: no third one
+                    raise = top > kMost && there;
+                    if (!__any_sync(0xffffffffu, raise)) break;
                 }
-                const float off = m == -INFINITY ? 0.0f : kPShift - m;
-                float top = 0.0f;
-                uint32_t s[2][32];
-                sum = 0.0f;
-                tmem_ld32(s_addr, s[0]);
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t* x = s[c & 1];
-                    tmem_wait_ld();
-                    if (c < 3) tmem_ld32(s_addr + (c + 1) * 32, s[(c + 1) & 1]);    // in flight during this chunk
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 32; e++)
-                            if (c * 32 + e >= lim) x[e] = 0xFF800000u;              // -inf: its score is -inf, its p 0
-                    }
-#pragma unroll
-                    for (int gr = 0; gr < 2; gr++) {
-                        const float4 cn = con[c * 2 + gr];
-                        const uint32_t* y = x + gr * 16;
-                        const float ca = fmaxf(crow * cn.x, kTiny), cb = cn.y + off;
-                        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float p0, p1;
-                            fma2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]), ca, cb, p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            add2(s0, s1, p0, p1);
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[c * 16 + gr * 8 + e / 2]) : "f"(p1), "f"(p0));
-                        }
-                        const float both = s0 + s1;
-                        top = fmaxf(top, both);
-                        sum = fmaf(both, cn.z, sum);
-                    }
-                }
-                // a p of the next pass is at most 2^8: no third one
-                raise = top > kMost && there;
-                if (!__any_sync(0xffffffffu, raise)) break;
+                l += sum;
+                tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(PF + w));
             }
-            l += sum;
-            tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-            tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-            tmem_wait_st();
+            if (!ok) break;
+            // ---- the next item's q is on its way to the caches while this one's output leaves
+            tc += max(it.nk[0], it.nk[1]);
+            more = has_item(k + 1);
+            if (more) {
+                const Item& next = items[(k + 1) & 1];
+                const int i2 = (next.row0 + w * kM + r) / G;
+                if (i2 < next.n) {
+                    const uint16_t* src = q_row(next, i2);
+#pragma unroll
+                    for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(src + c));
+                }
+            }
+            if (nk > 0 && !warp_wait(bar(OD + w), od)) break;
+            od ^= nk > 0;
+            const int a = it.row0 + w * kM + r - i * G;
+            tc_fence_after();
+            if (it.part >= 0) {                  // a part of the keys: the state as it is
+                float* dst = P.part + (int64_t)it.part * L::PART;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; c++) {
+                    uint32_t o[32];
+                    if (nk > 0) {
+                        tmem_ld32(o_addr + c * 32, o);
+                        tmem_wait_ld();
+                    }
+                    float4* d4 = reinterpret_cast<float4*>(dst + (w * kM + r) * D + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        d4[e] = nk > 0 ? make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]))
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                dst[kRows * D + w * kM + r] = m;
+                dst[kRows * D + kRows + w * kM + r] = l;
+            } else {
+                const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+                uint16_t* out = P.a.out + (int64_t)(it.q0 + i) * P.a.ldo + (int64_t)(it.h * G + a) * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; c++) {
+                    uint32_t o[32];
+                    if (nk > 0) {
+                        tmem_ld32(o_addr + c * 32, o);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e++) o[e] = 0u;
+                    }
+                    if (there) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                float x0 = __uint_as_float(o[e + 2 * j]) * inv, x1 = __uint_as_float(o[e + 2 * j + 1]) * inv;
+                                if (l == 0.0f) x0 = x1 = 0.0f;        // a row that saw nothing
+                                const __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
+                                y[j] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                            *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                }
+                if (there && P.a.lse)
+                    P.a.lse[(int64_t)(it.q0 + i) * P.a.heads_q + it.h * G + a] =
+                        l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+            }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(PF + w));
+            done_item(k);
         }
-        // ---- output
-        if (nk[w] > 0 && ok) ok = warp_wait(bar(OD + w), 0);
-        tc_fence_after();
-        const float r = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-        uint16_t* out = P.a.out + (int64_t)(q0 + i) * P.a.ldo + (int64_t)(h * G + a) * D;
-        if (ok) {
-#pragma unroll
-            for (int c = 0; c < D / 32; c++) {
-                uint32_t o[32];
-                if (nk[w] > 0) {
-                    tmem_ld32(o_addr + c * 32, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e++) o[e] = 0u;
-                }
-                if (there) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            float x0 = __uint_as_float(o[e + 2 * j]) * r, x1 = __uint_as_float(o[e + 2 * j + 1]) * r;
-                            if (l == 0.0f) x0 = x1 = 0.0f;            // a row that saw nothing
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
-                            y[j] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
-                        *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                }
-            }
-            if (there && P.a.lse)
-                P.a.lse[(int64_t)(q0 + i) * P.a.heads_q + h * G + a] =
-                    l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
-        }
-        tc_fence_before();
     } else if (warp < 12) {
         // ------------------------------------------------- V codes to f16
         reg_dec<72>();
         const int tid = threadIdx.x - 256;
+        constexpr int CH = D / 16, STEP = 128 / CH;                   // 16-code chunks of a row; rows per step
+        // rows STEP apart keep the swizzle (a multiple of 8), so a step only adds to the addresses
+        const int r0 = tid / CH, c = tid % CH, sw = r0 & 7, odd = c >> 2, c0 = (c & 3) * 2;
+        const uint8_t* src0 = smem + L::V_OFF + r0 * D + c * 16;
+        uint8_t* dst0 = smem + L::VH_OFF + odd * (kN * 128) + r0 * 128;
+        const int o1 = ((c0 + odd) ^ sw) << 4, o2 = ((c0 + 1 - odd) ^ sw) << 4;     // the second block's halves swapped: other banks
         bool ok = true;
-        for (int t = 0; t < nkv && ok; t++) {
-            const int st = t % kVStages, hb = t & 1;
-            if (!warp_wait(bar(VF + st), (t / kVStages) & 1)) { ok = false; break; }
-            if (!warp_wait(bar(HE + hb), ((t >> 1) & 1) ^ 1)) { ok = false; break; }
-            const uint8_t* src = smem + L::V_OFF + st * L::KT;
-            uint8_t* dst = smem + L::VH_OFF + hb * L::VH;
-            const int live = Lk - t * kN;         // rows behind the last key were never written: zeros
-            constexpr int CH = D / 16;            // 16-code chunks of a row
-#pragma unroll 2
-            for (int k = 0; k < CH; k++) {
-                const int idx = k * 128 + tid, r = idx / CH, c = idx % CH;
-                uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
-                if (r >= live) x = make_uint4(0, 0, 0, 0);
-                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                uint32_t y[8];
+        int kt = 0;                               // key tiles of the CTA so far
+        for (int k = 0; ok && has_item(k); k++) {
+            const Item& it = items[k & 1];
+            const int nkv = max(it.nk[0], it.nk[1]);
+            for (int t = 0; t < nkv; t++, kt++) {
+                const int st = kt & 1;
+                if (!warp_wait(bar(VF + st), (kt >> 1) & 1)) { ok = false; break; }
+                if (!warp_wait(bar(HE + st), ((kt >> 1) & 1) ^ 1)) { ok = false; break; }
+                const uint8_t* src = src0 + st * L::KT;
+                uint8_t* dst = dst0 + st * L::VH;
+                const int live = it.L - (it.t0 + t) * kN;             // rows behind the last key were never written: zeros
+                // rolled: in bursts, this traffic holds up the S products, which alone read 128 bytes of
+                // shared memory a cycle (unrolled 8 times 365 us, twice 309, rolled 292 on 4864 x 4096)
+#pragma unroll 1
+                for (int j = 0; j < CH; j++) {
+                    uint4 x = *reinterpret_cast<const uint4*>(src + j * STEP * D);
+                    if (r0 + j * STEP >= live) x = make_uint4(0, 0, 0, 0);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t y[8];
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    asm("{ .reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi; }"
-                        : "=r"(y[2 * e]), "=r"(y[2 * e + 1]) : "r"(in[e]));
-                uint8_t* row = dst + (c >> 2) * (kN * 128) + r * 128;
-                const int c0 = (c & 3) * 2, sw = r & 7, odd = c >> 2;               // the second block's halves swapped: other banks
-                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ sw) << 4)) = odd ? hi : lo;
-                *reinterpret_cast<uint4*>(row + (((c0 + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+                    for (int e = 0; e < 4; e++)
+                        asm("{ .reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi; }"
+                            : "=r"(y[2 * e]), "=r"(y[2 * e + 1]) : "r"(in[e]));
+                    const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                    *reinterpret_cast<uint4*>(dst + j * STEP * 128 + o1) = odd ? hi : lo;
+                    *reinterpret_cast<uint4*>(dst + j * STEP * 128 + o2) = odd ? lo : hi;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(HF + st));
+                    mbar_arrive(bar(VE + st));
+                }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(HF + hb));
-                mbar_arrive(bar(VE + st));
-            }
+            done_item(k);
         }
     } else {
         reg_dec<72>();
         if (warp == 12) {
             // ------------------------------------------------- TMA, scales
-            const int32_t* tab = P.a.block_table + (int64_t)b * P.a.ld_table;
-            const int page_end = (Lk + (1 << P.shift) - 1) >> P.shift;
-            auto page_at = [&](int t) {           // lane's page of tile t, num_pages (out of bounds: reads as zeros) if none
-                const int j = t * pages_tile + lane;
-                int p = -1;
-                if (lane < pages_tile && j < page_end) p = __ldg(tab + j);
-                return p >= 0 && p < P.a.kv.num_pages ? p : P.a.kv.num_pages;
-            };
-            int p = nkv > 0 ? page_at(0) : 0;
             bool ok = true;
-            int t = 0;
-            for (; t < nkv && ok; t++) {
-                const int ks = t % kKStages, vs = t % kVStages;
-                const int next = t + 1 < nkv ? page_at(t + 1) : 0;
-                float4 cn = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
-                if (lane < pages_tile && p < P.a.kv.num_pages) {
-                    const int64_t i = (int64_t)p * P.a.kv.heads + h;
-                    const float kscale = __ldg(P.a.kv.k_scale + i), vscale = fmaxf(__ldg(P.a.kv.v_scale + i), 1.2e-38f);
-                    cn = make_float4(kscale, __log2f(vscale), __frcp_rn(vscale), 0.0f);
-                }
-                ok = warp_wait(bar(KE + ks), ((t / kKStages) & 1) ^ 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(KF + ks), L::KT);
-                __syncwarp();
-                if (lane < pages_tile)
-                    tma_load_3d(sbase + L::K_OFF + ks * L::KT + (lane << P.shift) * D, &P.tm_k, 0, h << P.shift, p, bar(KF + ks));
-                // scales per 16 keys (a page covers page_size / 16 of them)
-                const int reps = 1 << (P.shift - 4);
-                if (lane < pages_tile)
-                    for (int j = 0; j < reps; j++) sc[(t % kScStages) * 8 + lane * reps + j] = cn;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(SC + t % kScStages));
-                ok = warp_wait(bar(VE + vs), ((t / kVStages) & 1) ^ 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(VF + vs), L::KT);
-                __syncwarp();
-                if (lane < pages_tile)
-                    tma_load_3d(sbase + L::V_OFF + vs * L::KT + (lane << P.shift) * D, &P.tm_v, 0, h << P.shift, p, bar(VF + vs));
-                p = next;
-            }
-            // no copy outlives the CTA (at once unless a wait gave up)
-            for (int j = max(0, t - kKStages); j < t; j++) mbar_wait(bar(KF + j % kKStages), (j / kKStages) & 1, &g_attn_prefill_err);
-            for (int j = max(0, t - kVStages); j < t; j++) mbar_wait(bar(VF + j % kVStages), (j / kVStages) & 1, &g_attn_prefill_err);
-            if (!ok) mbar_wait(bar(KF + t % kKStages), (t / kKStages) & 1, &g_attn_prefill_err);
-        } else if (warp >= 14) {
-            // ----------------------------- MMA of row tile w: one warp each
-            const int w = warp - 14, nkw = nk[w];
-            if (lane == 0 && nkv > 0) {
-                const uint32_t sd = tmem + L::S_COL + w * kN, od = tmem + L::O_COL + w * D;
-                const uint32_t qa = sdesc_k_lo<D>(sbase + L::Q_OFF + w * 2 * L::Q), k_lo = sdesc_k_lo<D>(sbase + L::K_OFF),
-                               v_lo = sdesc_v_lo(sbase + L::VH_OFF);
-                bool ok = true;
-                auto wait = [&](int i, uint32_t parity) { ok = ok && warp_wait(bar(i), parity); };
-                auto score = [&](uint32_t ka) {   // S, both parts of q
-#pragma unroll
-                    for (int k = 0; k < D / 32; k++) mma_s(sd, qa + k * 2, ka + k * 2, sdesc_k_hi<D>(), L::IDESC_S, k > 0);
-#pragma unroll
-                    for (int k = 0; k < D / 32; k++) mma_s(sd, qa + (L::Q >> 4) + k * 2, ka + k * 2, sdesc_k_hi<D>(), L::IDESC_S, true);
-                    tc_commit(bar(SF + w));
+            int kt = 0, ks = 0;
+            uint32_t kph = 1;          // K stage and the parity its release is waited for with
+            for (int k = 0; ok && has_item(k); k++) {
+                const Item& it = items[k & 1];
+                const int nkv = max(it.nk[0], it.nk[1]), h = it.h;
+                const int32_t* tab = P.a.block_table + (int64_t)it.b * P.a.ld_table;
+                const int page_end = (it.L + (1 << P.shift) - 1) >> P.shift;
+                auto page_at = [&](int t) {       // lane's page of tile t, num_pages (out of bounds: reads as zeros) if none
+                    const int j = (it.t0 + t) * pages_tile + lane;
+                    int p = -1;
+                    if (lane < pages_tile && j < page_end) p = __ldg(tab + j);
+                    return p >= 0 && p < P.a.kv.num_pages ? p : P.a.kv.num_pages;
                 };
-                // A row tile that sees fewer key tiles than its partner still releases every stage, and
-                // only after it was filled: an arrival ahead of its phase would count for an earlier one.
-                wait(KF, 0);
-                if (w == 1) wait(TN + 1, 0);
-                if (nkw > 0) {
-                    wait(QF + w, 0);
-                    tc_fence_after();
-                    if (ok) score(k_lo);
-                }
-                mbar_arrive(bar(TN + 1 - w));
-                tc_commit(bar(KE));
-                int ks = 0;                       // stage and phase of the next key tile
-                uint32_t kph = 0;
-                for (int t = 0; t < nkv && ok; t++) {
-                    if (++ks == kKStages) { ks = 0; kph ^= 1; }
-                    wait(HF + (t & 1), (t >> 1) & 1);
-                    if (t + 1 < nkv) wait(KF + ks, kph);
-                    wait(TN + w, (t + w) & 1);    // w = 0: after the partner's batch t, w = 1: t + 1
-                    if (t < nkw) {
-                        wait(PF + w, t & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t va = v_lo + (t & 1) * (L::VH >> 4);
-                        mma_o(od, sd, va, L::IDESC_O, t > 0);                        // O += P V
-#pragma unroll
-                        for (int k = 1; k < kN / 16; k++) mma_o(od, sd + k * 8, va + k * (2048 >> 4), L::IDESC_O, true);
-                        if (t + 1 < nkw) score(k_lo + ks * (L::KT >> 4));
-                        else tc_commit(bar(OD + w));
+                auto scales_of = [&](int p) {
+                    float4 cn = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+                    if (lane < pages_tile && p < P.a.kv.num_pages) {
+                        const int64_t i = (int64_t)p * P.a.kv.heads + h;
+                        cn.x = __ldg(P.a.kv.k_scale + i);
+                        cn.z = __ldg(P.a.kv.v_scale + i);
                     }
-                    mbar_arrive(bar(TN + 1 - w));
-                    tc_commit(bar(HE + (t & 1)));
-                    if (t + 1 < nkv) tc_commit(bar(KE + ks));
+                    return cn;
+                };
+                // pages two tiles ahead of their copies, scales one
+                int p = nkv > 0 ? page_at(0) : 0, p1 = nkv > 1 ? page_at(1) : 0;
+                float4 cn = scales_of(nkv > 0 ? p : P.a.kv.num_pages);
+                for (int t = 0; t < nkv; t++, kt++) {
+                    const int vs = kt & 1;
+                    const int p2 = t + 2 < nkv ? page_at(t + 2) : 0;
+                    const float4 cn1 = scales_of(t + 1 < nkv ? p1 : P.a.kv.num_pages);
+                    ok = warp_wait(bar(KE + ks), kph);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(KF + ks), L::KT);
+                    __syncwarp();
+                    if (lane < pages_tile)
+                        tma_load_3d(sbase + L::K_OFF + ks * L::KT + (lane << P.shift) * D, &P.tm_k, 0, h << P.shift, p, bar(KF + ks));
+                    // scales per 16 keys (a page covers page_size / 16 of them)
+                    const int reps = 1 << (P.shift - 4);
+                    if (p < P.a.kv.num_pages) {
+                        const float v = fmaxf(cn.z, 1.2e-38f);
+                        cn.y = __log2f(v);
+                        cn.z = __frcp_rn(v);
+                    }
+                    if (lane < pages_tile)
+                        for (int j = 0; j < reps; j++) sc[(kt % kScStages) * 8 + lane * reps + j] = cn;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(SC + kt % kScStages));
+                    if (++ks == kKStages) { ks = 0; kph ^= 1; }
+                    ok = warp_wait(bar(VE + vs), ((kt >> 1) & 1) ^ 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(VF + vs), L::KT);
+                    __syncwarp();
+                    if (lane < pages_tile)
+                        tma_load_3d(sbase + L::V_OFF + vs * L::KT + (lane << P.shift) * D, &P.tm_v, 0, h << P.shift, p, bar(VF + vs));
+                    p = p1;
+                    p1 = p2;
+                    cn = cn1;
                 }
+                done_item(k);
+            }
+            // no copy outlives the CTA (at once unless a wait gave up: the roles have read every tile)
+            if (!ok) {
+                for (int j = max(0, kt - kKStages); j <= kt; j++) warp_wait(bar(KF + j % kKStages), (j / kKStages) & 1);
+                for (int j = max(0, kt - kVStages); j < kt; j++) warp_wait(bar(VF + (j & 1)), (j >> 1) & 1);
+            }
+        } else if (warp == 13) {
+            // ------------------------------------------------------ items
+            int id = blockIdx.x, asked = 0;
+            for (int k = 0; ; ) {
+                Item it;
+                it.b = -1;
+                if (id >= 0) {                    // the last row tiles (the longest under the causal rule) first
+                    it.h = id % P.a.kv.heads;
+                    const int rest = id / P.a.kv.heads, split = rest % P.splits, want = P.tiles - 1 - rest / P.splits;
+                    int before = 0;
+                    for (int b0 = 0; b0 < P.a.B; b0 += 32) {
+                        const int b = b0 + lane;
+                        int own = 0, start = 0, n = 0;
+                        if (b < P.a.B) {
+                            start = __ldg(P.a.cu_q + b);
+                            n = min(__ldg(P.a.cu_q + b + 1) - start, P.a.max_q);
+                            const int64_t rows = (int64_t)max(n, 0) * G;
+                            own = rows < P.min_rows ? 0 : (int)((rows + kRows - 1) / kRows);
+                        }
+                        int v = own;
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int u = __shfl_up_sync(0xffffffffu, v, o);
+                            if (lane >= o) v += u;
+                        }
+                        const int first = before + v - own;
+                        const uint32_t hit = __ballot_sync(0xffffffffu, want >= first && want < first + own);
+                        if (hit) {
+                            const int l0 = __ffs(hit) - 1;
+                            it.b = b0 + l0;
+                            it.row0 = (want - __shfl_sync(0xffffffffu, first, l0)) * kRows;
+                            it.q0 = __shfl_sync(0xffffffffu, start, l0);
+                            it.n = __shfl_sync(0xffffffffu, n, l0);
+                            break;
+                        }
+                        before += __shfl_sync(0xffffffffu, v, 31);
+                        if (before > want) break;
+                    }
+                    if (P.splits > 1 && split == 0 && lane == 0) {
+                        P.head[(want * P.a.kv.heads + it.h) * 2] = it.b;
+                        P.head[(want * P.a.kv.heads + it.h) * 2 + 1] = it.row0;
+                    }
+                    if (it.b >= 0) {
+                        it.n = it.q0 < 0 ? 0 : (int)min((int64_t)it.n, P.a.tokens - it.q0);
+                        it.L = (int)min((int64_t)max(__ldg(P.a.kv_lens + it.b), 0), (int64_t)P.a.max_blocks << P.shift);
+                        // key tiles of each row tile: up to what its last row sees, cut to this part
+                        int full[2];
+#pragma unroll
+                        for (int w = 0; w < 2; w++) {
+                            const int first = it.row0 + w * kM, last = min(first + kM, it.n * G) - 1;
+                            const int sees = last < first ? 0 : P.a.causal ? min(max(it.L - it.n + last / G + 1, 0), it.L) : it.L;
+                            full[w] = (sees + kN - 1) / kN;
+                        }
+                        const int all = max(full[0], full[1]);
+                        it.t0 = (int)((int64_t)all * split / P.splits);
+                        const int t1 = (int)((int64_t)all * (split + 1) / P.splits);
+#pragma unroll
+                        for (int w = 0; w < 2; w++) it.nk[w] = max(min(full[w], t1) - it.t0, 0);
+                        it.part = P.splits > 1 ? (want * P.a.kv.heads + it.h) * P.splits + split : -1;
+                    }
+                }
+                if (it.b >= 0 || id < 0) {
+                    if (lane == 0) {
+                        items[k & 1] = it;
+                        mbar_arrive(bar(IF + (k & 1)));
+                    }
+                    if (id < 0) break;
+                    k++;                          // its place is free once every role has left the item before last
+                    if (!warp_wait(bar(IE + (k & 1)), ((k >> 1) & 1) ^ 1)) break;
+                }
+                if (lane == 0) {
+                    fence_proxy_async_smem();     // the last answer has been read
+                    mbar_arrive_expect_tx(bar(CB), 16);
+                    try_cancel(smem_u32(canceled), bar(CB));
+                }
+                __syncwarp();
+                if (!warp_wait(bar(CB), asked & 1)) break;
+                asked++;
+                id = canceled_cta(smem_u32(canceled));
+            }
+        } else {
+            // ----------------------------- MMA of row tile w: one warp each
+            const int w = warp - 14;
+            const uint32_t sd = tmem + L::S_COL + w * kN, od = tmem + L::O_COL + w * D;
+            const uint32_t qa = sdesc_k_lo<D>(sbase + L::Q_OFF + w * 2 * L::Q), k_lo = sdesc_k_lo<D>(sbase + L::K_OFF),
+                           v_lo = sdesc_v_lo(sbase + L::VH_OFF);
+            bool ok = true;
+            int kt = 0, ks = 0, tw = 0, batch = 0;                    // key tiles; K stage; own key tiles; MMA batches
+            uint32_t kph = 0, qph = 0;
+            for (int k = 0; ok && has_item(k); k++) {
+                const int nkv = max(items[k & 1].nk[0], items[k & 1].nk[1]), nkw = items[k & 1].nk[w];
+                if (lane == 0 && nkv > 0) {
+                    auto wait = [&](int i, uint32_t parity) { ok = ok && warp_wait(bar(i), parity); };
+                    auto turn = [&]() {           // w = 0: after the partner's batch before, w = 1: after its batch
+                        wait(TN + w, (batch & 1) ^ 1 ^ w);
+                        batch++;
+                    };
+                    auto score = [&](uint32_t ka) {                   // S, both parts of q
+#pragma unroll
+                        for (int j = 0; j < D / 32; j++) mma_s(sd, qa + j * 2, ka + j * 2, sdesc_k_hi<D>(), L::IDESC_S, j > 0);
+#pragma unroll
+                        for (int j = 0; j < D / 32; j++) mma_s(sd, qa + (L::Q >> 4) + j * 2, ka + j * 2, sdesc_k_hi<D>(), L::IDESC_S, true);
+                        tc_commit(bar(SF + w));
+                    };
+                    // A row tile that sees fewer key tiles than its partner still releases every stage, and
+                    // only after it was filled: an arrival ahead of its phase would count for an earlier one.
+                    wait(KF + ks, kph);
+                    if (nkw > 0) wait(QF + w, qph);
+                    turn();
+                    if (ok) {
+                        tc_fence_after();
+                        if (nkw > 0) score(k_lo + ks * (L::KT >> 4));
+                        mbar_arrive(bar(TN + 1 - w));
+                        tc_commit(bar(KE + ks));
+                    }
+                    for (int t = 0; t < nkv && ok; t++, kt++) {
+                        if (++ks == kKStages) { ks = 0; kph ^= 1; }
+                        wait(HF + (kt & 1), (kt >> 1) & 1);
+                        if (t + 1 < nkv) wait(KF + ks, kph);
+                        turn();
+                        if (t < nkw) {
+                            wait(PF + w, tw & 1);
+                            tw++;
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t va = v_lo + (kt & 1) * (L::VH >> 4);
+                            mma_o(od, sd, va, L::IDESC_O, t > 0);                    // O += P V
+#pragma unroll
+                            for (int j = 1; j < kN / 16; j++) mma_o(od, sd + j * 8, va + j * (2048 >> 4), L::IDESC_O, true);
+                            if (t + 1 < nkw) score(k_lo + ks * (L::KT >> 4));
+                            else tc_commit(bar(OD + w));
+                        }
+                        if (!ok) break;
+                        mbar_arrive(bar(TN + 1 - w));
+                        tc_commit(bar(HE + (kt & 1)));
+                        if (t + 1 < nkv) tc_commit(bar(KE + ks));
+                    }
+                    qph ^= nkw > 0;
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                done_item(k);
+            }
+            if (lane == 0) {
                 tc_commit(bar(DR + w));           // no MMA outlives the CTA's tensor memory
-                mbar_wait(bar(DR + w), 0, &g_attn_prefill_err);
+                warp_wait(bar(DR + w), 0);
             }
             __syncwarp();
         }
@@ -551,17 +723,67 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
     }
 }
 
+// Joins the states of an item's key parts in order: 8 rows of one item per CTA.
 template <int D>
-qz_status launch_prefill(const PrefillParams& P, int64_t ctas, cudaStream_t st) {
+__global__ void __launch_bounds__(2 * D)
+attn_prefill_join_kernel(const __grid_constant__ PrefillParams P) {
     using L = PrefillLayout<D>;
+    pdl_trigger();
+    pdl_wait();
+    const int idx = blockIdx.y, b = P.head[idx * 2];
+    if (b < 0) return;
+    const int G = P.a.heads_q / P.a.kv.heads, h = idx % P.a.kv.heads;
+    const int r = blockIdx.x * 8 + threadIdx.x / (D / 4), d0 = threadIdx.x % (D / 4) * 4;
+    const int q0 = __ldg(P.a.cu_q + b);
+    int n = min(__ldg(P.a.cu_q + b + 1) - q0, P.a.max_q);
+    n = q0 < 0 ? 0 : (int)min((int64_t)n, P.a.tokens - q0);
+    const int row = P.head[idx * 2 + 1] + r, i = row / G, a = row - i * G;
+    if (i >= n) return;
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < P.splits; s++) {
+        const float* src = P.part + ((int64_t)idx * P.splits + s) * L::PART;
+        const float m2 = src[kRows * D + r], l2 = src[kRows * D + kRows + r], mm = fmaxf(m, m2);
+        const float4 x = *reinterpret_cast<const float4*>(src + r * D + d0);
+        const float f = m == -INFINITY ? (l == l ? 0.0f : l) : ex2(m - mm);
+        const float f2 = m2 == -INFINITY ? (l2 == l2 ? 0.0f : l2) : ex2(m2 - mm);
+        l = l * f + l2 * f2;
+        o.x = o.x * f + x.x * f2;
+        o.y = o.y * f + x.y * f2;
+        o.z = o.z * f + x.z * f2;
+        o.w = o.w * f + x.w * f2;
+        m = mm;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), y1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(P.a.out + (int64_t)(q0 + i) * P.a.ldo + (int64_t)(h * G + a) * D + d0) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+    if (P.a.lse && d0 == 0)
+        P.a.lse[(int64_t)(q0 + i) * P.a.heads_q + h * G + a] =
+            l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+}
+
+template <int D>
+qz_status launch_prefill(PrefillParams& P, int64_t ctas, void* ws, cudaStream_t st) {
+    using L = PrefillLayout<D>;
+    const int items = P.tiles * P.a.kv.heads;
+    P.head = reinterpret_cast<int*>(ws);
+    P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)items * 8 + 255) / 256 * 256);
     QZ_TRY(opt_in_smem((const void*)attn_prefill_kernel<D>, L::SMEM));
-    return launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), L::SMEM, st, P);
+    QZ_TRY(launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), L::SMEM, st, P));
+    if (P.splits == 1) return QZ_OK;
+    return launch_pdl(attn_prefill_join_kernel<D>, dim3(kRows / 8, items), dim3(2 * D), 0, st, P);
 }
 
 } // namespace
 
+// States of a launch that splits its items: at most one part per SM.
+size_t ws_attn_prefill() {
+    return (size_t)num_sms() * (PrefillLayout<128>::PART * 4 + 8) + 256;
+}
+
 // Requests of at least min_rows rows per KV head; the others are left alone.
-qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, cudaStream_t st) {
+qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, void* ws, cudaStream_t st) {
     PrefillParams P;
     P.a = a;
     P.shift = a.kv.page_size == 16 ? 4 : a.kv.page_size == 32 ? 5 : a.kv.page_size == 64 ? 6 : 7;
@@ -576,10 +798,15 @@ qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, cudaStream_t st) 
     // row tiles of the requests: at most one partly filled each, and a request taken has min_rows rows
     const int64_t all = a.tokens * (a.heads_q / a.kv.heads);
     const int64_t tiles = all / kRows + std::min<int64_t>(a.B, all / min_rows + 1);
-    if (tiles * a.kv.heads > 0x7fffffff) return QZ_ERR_SHAPE;
+    // Parts of the keys: as many as fill the SMs where the row tiles fill less than half of them, each of
+    // kSplitKeys keys or more (by the table's width; the lengths are on the device).
+    const int64_t keys = (int64_t)a.max_blocks * a.kv.page_size;
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(num_sms() / (tiles * a.kv.heads), keys / kSplitKeys));
+    if (tiles * a.kv.heads * splits > 0x7fffffff) return QZ_ERR_SHAPE;
     P.tiles = (int)tiles;
-    return a.kv.head_dim == 64 ? launch_prefill<64>(P, tiles * a.kv.heads, st)
-                               : launch_prefill<128>(P, tiles * a.kv.heads, st);
+    P.splits = (int)splits;
+    const int64_t ctas = tiles * a.kv.heads * splits;
+    return a.kv.head_dim == 64 ? launch_prefill<64>(P, ctas, ws, st) : launch_prefill<128>(P, ctas, ws, st);
 }
 
 qz_status attn_prefill_error_read_and_clear() {

@@ -38,7 +38,8 @@ size_t ws_attn_decode();
 qz_status attn_decode_launch(const AttnArgs& a, int max_rows, void* ws, cudaStream_t st);
 qz_status attn_decode_error_read_and_clear();
 // the requests of at least min_rows query rows per KV head (attn_fp8_prefill.cu)
-qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, cudaStream_t st);
+size_t ws_attn_prefill();
+qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, void* ws, cudaStream_t st);
 qz_status attn_prefill_error_read_and_clear();
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
