@@ -19,8 +19,11 @@
 // (0, 256] and its two parts step by 2^-9 at the finest, so p keeps 8 bits down to 2^-9 of
 // its maximum and steps of 2^-17 of it below. m, l and O are fp32.
 //
-// Work split: units of 32 keys of one (request, KV head, row tile), laid end to
-// end over all requests and cut into equal shares, one CTA of 8 warps per SM. Each
+// Work split: the units (32 keys) of every item (request, KV head, row tile), each
+// item with a charge of kItemCost units for its q, its joining and its output in front,
+// laid end to end over all requests and cut into equal shares, one CTA of 8 warps per
+// SM (without the charge, a CTA with 70 items of a unit each ran six times as long as the
+// others). Each
 // warp takes every eighth unit of the CTA's share with a private ring of TMA
 // stages (3 x 8 KB in flight per warp: 192 KB per SM, against ~45 KB that the
 // latency asks for), so no warp waits for another inside a share. At the end of a
@@ -40,6 +43,7 @@ __device__ unsigned int g_attn_decode_err;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 32;                         // keys of a unit
 constexpr int kStages = 3;
+constexpr int kItemCost = 12;                     // units that an item's q, joining and output take (2 us against 1.4 for 8 units)
 constexpr float kPShift = 8.0f;                   // p = 2^(t - m + 8)
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -64,7 +68,9 @@ struct DecodeParams {
     AttnArgs a;
     int shift;                                    // log2 page_size
     int max_rows;                                 // requests with more rows per KV head are not taken
-    int* head;                                    // [CTAs][4]: what the CTA left for the joining launch
+    int* head;                                    // [CTAs][8]: what the CTA left for the joining launch: 0: the part of an
+                                                  // item begun before (0 or -1), 1: it goes on, 2: an item that goes on
+                                                  // begins here (0 or -1), 3 .. 6: its first token, tokens, first row, KV head
     float* part;                                  // [CTAs][2] partial states
 };
 
@@ -83,24 +89,34 @@ __device__ __forceinline__ Req load_req(const DecodeParams& P, int b, int G) {
     r.L = (int)min((int64_t)max(__ldg(P.a.kv_lens + b), 0), (int64_t)P.a.max_blocks << P.shift);
     const int64_t rows = (int64_t)r.n * G;
     r.tiles = rows > P.max_rows ? 0 : (int)((rows + R - 1) / R);
-    r.subs = max((r.L + kKeys - 1) / kKeys, 1);   // a request without keys still writes its rows
+    r.subs = (r.L + kKeys - 1) / kKeys;
     return r;
 }
 
-// The walk over the items (request, head, row tile) of a CTA's share.
+// The walk over the items that a CTA's share touches. An item lies at a .. a + kItemCost
+// + subs of the line, counted from the share's begin; its units follow its charge.
 template <int R>
-struct Cursor {
-    int b, h, tile;
+struct Walk {
+    int b, h, tile, a, share;
     Req r;
+    __device__ bool valid() const { return a < share && b < 0x7fffffff; }
+    __device__ int lo() const { return min(max(-a - kItemCost, 0), r.subs); }
+    __device__ int hi() const { return min(max(share - a - kItemCost, 0), r.subs); }
+    // some of its units are in the share; an item without keys belongs to the share that it begins in
+    __device__ bool mine() const { return r.subs ? lo() < hi() : a >= 0; }
     __device__ void next(const DecodeParams& P, int G) {
+        a += kItemCost + r.subs;
         if (++tile < r.tiles) return;
         tile = 0;
         if (++h < P.a.kv.heads) return;
         h = 0;
         do {
-            if (++b >= P.a.B) return;
+            if (++b >= P.a.B) { b = 0x7fffffff; return; }
             r = load_req<R>(P, b, G);
         } while (r.tiles == 0);
+    }
+    __device__ void next_mine(const DecodeParams& P, int G) {
+        do next(P, G); while (valid() && !mine());
     }
 };
 
@@ -168,25 +184,24 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     auto units_of = [&](int b) -> int64_t {
         if (b >= P.a.B) return 0;
         const Req r = load_req<R>(P, b, G);
-        return (int64_t)P.a.kv.heads * r.tiles * r.subs;
+        return (int64_t)P.a.kv.heads * r.tiles * (r.subs + kItemCost);
     };
-    int64_t sum = 0;
-    for (int b = threadIdx.x; b < P.a.B; b += kThreads) sum += units_of(b);
+    const int64_t mine0 = units_of(threadIdx.x);
+    int64_t sum = mine0;
+    for (int b = threadIdx.x + kThreads; b < P.a.B; b += kThreads) sum += units_of(b);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[warp] = sum;
     __syncthreads();
     int64_t total = 0;
     for (int w = 0; w < kWarps; w++) total += s_sum[w];
-    const int64_t per = max((int64_t)kWarps, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t per = max((int64_t)(kWarps + kItemCost), (total + gridDim.x - 1) / gridDim.x);
     const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
-    int* header = P.head + blockIdx.x * 4;
-    if (u0 >= u1) {
-        if (threadIdx.x == 0) header[0] = header[1] = header[2] = -1;
-        return;
-    }
+    int* header = P.head + blockIdx.x * 8;
+    if (threadIdx.x == 0) header[0] = header[2] = -1;
+    if (u0 >= u1) return;
     int64_t before = 0;
     for (int b0 = 0; b0 < P.a.B; b0 += kThreads) {
-        int64_t v = units_of(b0 + threadIdx.x);
+        int64_t v = b0 == 0 ? mine0 : units_of(b0 + threadIdx.x);
         const int64_t own = v;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
@@ -211,18 +226,36 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     __syncthreads();
 
     // ---- two walks over the share: `ahead` looks up pages and issues copies, `cur` computes
-    Cursor<R> cur;
+    Walk<R> cur;
     cur.b = s_start[0];
     cur.r = load_req<R>(P, cur.b, G);
-    const int64_t inside = *reinterpret_cast<int64_t*>(s_start + 2);
-    const int item0 = (int)(inside / cur.r.subs);
-    cur.h = item0 / cur.r.tiles;
-    cur.tile = item0 % cur.r.tiles;
-    const int sub0 = (int)(inside % cur.r.subs);
-    const int share = (int)(u1 - u0);             // units of the CTA (a share of 2^31 units would be 2^36 keys)
-    Cursor<R> ahead = cur;
-    int ahead_base = -sub0;                       // unit of the share at which ahead's item begins
-    int looked = warp, issued = warp;             // next units of this warp to look up and to issue (share index)
+    cur.share = (int)(u1 - u0);                   // (a share of 2^31 units would be 2^36 keys)
+    {
+        const int64_t inside = *reinterpret_cast<int64_t*>(s_start + 2), len = cur.r.subs + kItemCost;
+        const int item0 = (int)(inside / len);
+        cur.h = item0 / cur.r.tiles;
+        cur.tile = item0 % cur.r.tiles;
+        cur.a = -(int)(inside % len);
+    }
+    if (!cur.mine()) cur.next_mine(P, G);
+    Walk<R> ahead = cur;
+    int ahead_base = 0;                           // units of the share before ahead's item
+    int looked = warp, issued = 0;                // next unit of this warp to look up (of the share's); units issued
+
+    // q of an item: rows g (and g + 8), channels t*16 .. of each 64-channel half, as it lies in memory
+    uint4 raw[RR][D / 32];
+    auto load_q = [&](const Walk<R>& it) {
+#pragma unroll
+        for (int rr = 0; rr < RR; rr++) {
+            const int row = it.tile * R + rr * 8 + g, i = row / G, a = row - i * G;
+            const bool there = it.valid() && i < it.r.n;
+            const uint16_t* src = P.a.q + (int64_t)(it.r.q0 + i) * P.a.ldq + (int64_t)(it.h * G + a) * D + t * 16;
+#pragma unroll
+            for (int j = 0; j < D / 32; j++)
+                raw[rr][j] = there ? __ldg(reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + (j & 1) * 8)) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load_q(cur);
 
     int* pages = s_page + warp * 12;              // ring of 4 units
     const uint32_t ring = smem_u32(smem) + warp * kStages * Lay::STAGE;
@@ -231,81 +264,75 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
     int dead_at = -1;
 
-    // Pages of the warp's next unit: from the table into the ring (one unit ahead of its issue).
+    // Pages of the warp's next unit, from the table (one unit ahead of its issue); h < 0: there is none.
     struct Look { int p0, p1, h, key; };
-    Look look;                                    // looked up, not yet issued
     auto look_up = [&]() {                        // uniform over the warp
-        look.p0 = look.p1 = -1;
-        if (looked < share) {
-            while (looked >= ahead_base + ahead.r.subs) {
-                ahead_base += ahead.r.subs;
-                ahead.next(P, G);
-            }
-            look.key = (looked - ahead_base) * kKeys;
-            look.h = ahead.h;
-            const int32_t* row = P.a.block_table + (int64_t)ahead.b * P.a.ld_table + (look.key >> P.shift);
-            if (look.key < ahead.r.L) look.p0 = __ldg(row);
-            if (P.shift == 4 && look.key + 16 < ahead.r.L) look.p1 = __ldg(row + 1);
+        Look k = {-1, -1, -1, 0};
+        while (ahead.valid() && looked >= ahead_base + ahead.hi() - ahead.lo()) {
+            ahead_base += ahead.hi() - ahead.lo();
+            ahead.next(P, G);
         }
+        if (ahead.valid()) {
+            k.key = (ahead.lo() + looked - ahead_base) * kKeys;
+            k.h = ahead.h;
+            const int32_t* row = P.a.block_table + (int64_t)ahead.b * P.a.ld_table + (k.key >> P.shift);
+            k.p0 = __ldg(row);
+            if (P.shift == 4 && k.key + 16 < ahead.r.L) k.p1 = __ldg(row + 1);
+        }
+        looked += kWarps;
+        return k;
     };
-    auto issue = [&]() {                          // the unit that `look` holds, into its stage
-        if (issued < share) {
-            const int k = (issued - warp) / kWarps, st = k % kStages;
-            const int p0 = look.p0 >= 0 && look.p0 < P.a.kv.num_pages ? look.p0 : -1;
-            const int p1 = P.shift == 4 ? (look.p1 >= 0 && look.p1 < P.a.kv.num_pages ? look.p1 : -1) : p0;
-            if (lane == 0) {
-                pages[(k & 3) * 3] = p0;
-                pages[(k & 3) * 3 + 1] = p1;
-                pages[(k & 3) * 3 + 2] = look.h;
-                if (!dead) {
-                    const uint32_t dst = ring + st * Lay::STAGE, bar = bar0 + st * 8;
-                    const int y = (look.h << P.shift) + (look.key & (page_keys - 1));
-                    if (P.shift == 4) {
-                        mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * Lay::HALF);
-                        if (p0 >= 0) {
-                            tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
-                            tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
-                        }
-                        if (p1 >= 0) {
-                            tma_load_3d(dst + Lay::HALF / 2, &P.tm_k, 0, y, p1, bar);
-                            tma_load_3d(dst + Lay::HALF + Lay::HALF / 2, &P.tm_v, 0, y, p1, bar);
-                        }
-                    } else {
-                        mbar_arrive_expect_tx(bar, (p0 >= 0) * Lay::STAGE);
-                        if (p0 >= 0) {
-                            tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
-                            tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
-                        }
+    auto issue = [&](const Look& look) {          // its copies, into the warp's next stage
+        const int k = issued++, st = k % kStages;
+        const int p0 = look.p0 >= 0 && look.p0 < P.a.kv.num_pages ? look.p0 : -1;
+        const int p1 = P.shift == 4 ? (look.p1 >= 0 && look.p1 < P.a.kv.num_pages ? look.p1 : -1) : p0;
+        if (lane == 0) {
+            pages[(k & 3) * 3] = p0;
+            pages[(k & 3) * 3 + 1] = p1;
+            pages[(k & 3) * 3 + 2] = look.h;
+            if (!dead && look.h >= 0) {
+                const uint32_t dst = ring + st * Lay::STAGE, bar = bar0 + st * 8;
+                const int y = (look.h << P.shift) + (look.key & (page_keys - 1));
+                if (P.shift == 4) {
+                    mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * Lay::HALF);
+                    if (p0 >= 0) {
+                        tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
+                        tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
+                    }
+                    if (p1 >= 0) {
+                        tma_load_3d(dst + Lay::HALF / 2, &P.tm_k, 0, y, p1, bar);
+                        tma_load_3d(dst + Lay::HALF + Lay::HALF / 2, &P.tm_v, 0, y, p1, bar);
+                    }
+                } else {
+                    mbar_arrive_expect_tx(bar, (p0 >= 0) * Lay::STAGE);
+                    if (p0 >= 0) {
+                        tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
+                        tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
                     }
                 }
             }
-            __syncwarp();
         }
-        issued += kWarps;
+        __syncwarp();
     };
-    look_up();
-#pragma unroll 1
-    for (int s = 0; s < kStages; s++) {
-        issue();
-        looked += kWarps;
-        look_up();
+    Look look;                                    // looked up, not yet issued
+    {
+        Look first[kStages];                      // the first lookups in flight together
+#pragma unroll
+        for (int s = 0; s < kStages; s++) first[s] = look_up();
+        look = look_up();
+#pragma unroll
+        for (int s = 0; s < kStages; s++) issue(first[s]);
     }
 
     const float c0 = fabsf(P.a.sm_scale) * kLog2e;
-    int unit = 0;                                 // of the share, at the item's first unit here
+    int unit = 0;                                 // units of the share before the item
     int kdone = 0;                                // units that this warp has computed
-    int sub = sub0;
-    if (threadIdx.x == 0) {
-        header[0] = -1;
-        header[1] = 0;
-        header[2] = -1;
-    }
     // pages and scales of the warp's next unit, one unit ahead
     int p0 = -1, p1 = -1;
     float ks0 = 0.0f, ks1 = 0.0f, vs0 = 1.0f, vs1 = 1.0f;
     auto load_scales = [&]() {
-        if (warp + kdone * kWarps >= share) return;
         const int* e = pages + (kdone & 3) * 3;
+        if (e[2] < 0) return;                     // no more units
         p0 = e[0];
         p1 = e[1];
         if (p0 >= 0) {
@@ -321,24 +348,34 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     };
     load_scales();
 
-    while (unit < share) {
-        const int here = min(cur.r.subs - sub, share - unit);          // units of this item in this share
+    while (cur.valid()) {
+        if (cur.r.subs == 0) {                    // no keys: zeros
+            for (int c = threadIdx.x; c < R * D / 8; c += kThreads) {
+                const int row = cur.tile * R + c / (D / 8), i = row / G, a = row - i * G;
+                if (i >= cur.r.n) break;
+                const int64_t token = cur.r.q0 + i;
+                *reinterpret_cast<uint4*>(P.a.out + token * P.a.ldo + (int64_t)(cur.h * G + a) * D + c % (D / 8) * 8) =
+                    make_uint4(0, 0, 0, 0);
+                if (P.a.lse && c % (D / 8) == 0) P.a.lse[token * P.a.heads_q + cur.h * G + a] = -INFINITY;
+            }
+            cur.next_mine(P, G);
+            load_q(cur);
+            continue;
+        }
+        const int sub = cur.lo(), here = cur.hi() - sub;               // units of this item in this share
         // ---- q of this item: rows g (and g + 8), two parts each, in the order the keys are read
         uint32_t qf[RR][KS][4];                   // R = 8: hi b0, lo b0, hi b1, lo b1; R = 16: per row hi b0, hi b1, lo b0, lo b1
         float crow[RR];
         int seen[RR];                             // keys that the row sees
 #pragma unroll
         for (int rr = 0; rr < RR; rr++) {
-            const int row = cur.tile * R + rr * 8 + g, i = row / G, a = row - i * G;
+            const int i = (cur.tile * R + rr * 8 + g) / G;
             const bool there = i < cur.r.n;
-            const uint16_t* src = P.a.q + (int64_t)(cur.r.q0 + i) * P.a.ldq + (int64_t)(cur.h * G + a) * D + t * 16;
             float v[D / 4];
             float m = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 32; j++) {    // 16 bytes: channels t*16 + (j & 1)*8 of the 64-channel half j >> 1
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (there) w = __ldg(reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + (j & 1) * 8));
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t x[4] = {raw[rr][j].x, raw[rr][j].y, raw[rr][j].z, raw[rr][j].w};
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     v[j * 8 + 2 * e] = __uint_as_float(x[e] << 16);
@@ -515,12 +552,14 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             kdone++;
             __syncwarp();                         // the stage has been read
             load_scales();                        // of the next unit, whose pages are in the ring
-            issue();
-            looked += kWarps;
-            look_up();
+            issue(look);
+            look = look_up();
         }
 
-        // ---- the item's end in this share: join the warps
+        // ---- the item's end in this share: join the warps, the next item's q on its way
+        Walk<R> nxt = cur;
+        nxt.next_mine(P, G);
+        load_q(nxt);
 #pragma unroll
         for (int rr = 0; rr < RR; rr++) {
             l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
@@ -618,22 +657,24 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                 }
                 if (lane == 0) {
                     if (begins) {                 // the joining launch starts here
-                        header[2] = cur.b;
-                        header[3] = cur.h * cur.r.tiles + cur.tile;
+                        header[2] = 0;
+                        header[3] = cur.r.q0;
+                        header[4] = cur.r.n;
+                        header[5] = cur.tile * R;
+                        header[6] = cur.h;
                     } else {
-                        header[0] = cur.b;
+                        header[0] = 0;
                         header[1] = !ends;        // goes on in the next CTA
                     }
                 }
             }
         }
         unit += here;
-        sub = 0;
-        if (unit < share) cur.next(P, G);
+        cur = nxt;
     }
     // copies still in flight (a wait that gave up): their stages must not outlive the CTA
     if (dead)
-        for (int k = dead_at; k < dead_at + kStages && warp + k * kWarps < share; k++)
+        for (int k = dead_at; k < dead_at + kStages && pages[(k & 3) * 3 + 2] >= 0; k++)
             mbar_wait(bar0 + k % kStages * 8, (k / kStages) & 1, &g_attn_decode_err);
 }
 
@@ -646,11 +687,10 @@ attn_join_kernel(const __grid_constant__ DecodeParams P, int parts) {
     constexpr int V = R * D / 256;                // channels of a thread: 4 (R = 8, D = 128) ...
     pdl_trigger();
     pdl_wait();
-    const int b = P.head[blockIdx.x * 4 + 2];
-    if (b >= 0) {
+    const int* own = P.head + blockIdx.x * 8;
+    if (own[2] >= 0) {
         const int G = P.a.heads_q / P.a.kv.heads;
-        const Req r = load_req<R>(P, b, G);
-        const int item = P.head[blockIdx.x * 4 + 3], h = item / r.tiles, tile = item % r.tiles;
+        const int q0 = own[3], n = own[4], row0 = own[5], h = own[6];
         const int row = threadIdx.x * V / D, d0 = threadIdx.x * V % D;
         const float* src = P.part + ((int64_t)blockIdx.x * 2 + 1) * Lay::PART;
         float m = src[R * D + row], l = src[R * D + R + row], o[V];
@@ -659,7 +699,7 @@ attn_join_kernel(const __grid_constant__ DecodeParams P, int parts) {
         bool more = true;
         for (int c = blockIdx.x + 1; more && c < parts; c++) {
             src = P.part + (int64_t)c * 2 * Lay::PART;
-            more = P.head[c * 4 + 1] != 0;
+            more = P.head[c * 8 + 1] != 0;
             const float m2 = src[R * D + row], l2 = src[R * D + R + row], mm = fmaxf(m, m2);
             const float f = m == -INFINITY ? (l == l ? 0.0f : l) : ex2(m - mm);
             const float f2 = m2 == -INFINITY ? (l2 == l2 ? 0.0f : l2) : ex2(m2 - mm);
@@ -668,17 +708,17 @@ attn_join_kernel(const __grid_constant__ DecodeParams P, int parts) {
             for (int i = 0; i < V; i++) o[i] = o[i] * f + src[row * D + d0 + i] * f2;
             m = mm;
         }
-        const int rw = tile * R + row, i = rw / G, a = rw - i * G;
-        if (i < r.n) {
+        const int rw = row0 + row, i = rw / G, a = rw - i * G;
+        if (i < n) {
             const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-            uint16_t* out = P.a.out + (int64_t)(r.q0 + i) * P.a.ldo + (int64_t)(h * G + a) * D + d0;
+            uint16_t* out = P.a.out + (int64_t)(q0 + i) * P.a.ldo + (int64_t)(h * G + a) * D + d0;
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
                 const __nv_bfloat162 w = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
                 *reinterpret_cast<__nv_bfloat162*>(out + e) = w;
             }
             if (P.a.lse && d0 == 0)
-                P.a.lse[(int64_t)(r.q0 + i) * P.a.heads_q + h * G + a] =
+                P.a.lse[(int64_t)(q0 + i) * P.a.heads_q + h * G + a] =
                     l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
         }
     }
@@ -689,7 +729,7 @@ qz_status launch_decode(DecodeParams& P, void* ws, cudaStream_t st) {
     using Lay = DecodeLayout<D, R>;
     const int ctas = num_sms();
     P.head = reinterpret_cast<int*>(ws);
-    P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)ctas * 16 + 255) / 256 * 256);
+    P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)ctas * 32 + 255) / 256 * 256);
     QZ_TRY(opt_in_smem((const void*)attn_decode_kernel<D, R>, Lay::SMEM));
     QZ_TRY(launch_pdl(attn_decode_kernel<D, R>, dim3(ctas), dim3(kThreads), Lay::SMEM, st, P));
     return launch_pdl(attn_join_kernel<D, R>, dim3(ctas), dim3(256), 0, st, P, ctas);
@@ -699,7 +739,7 @@ qz_status launch_decode(DecodeParams& P, void* ws, cudaStream_t st) {
 
 size_t ws_attn_decode() {
     const size_t ctas = (size_t)num_sms();
-    return (ctas * 16 + 255) / 256 * 256 + ctas * 2 * DecodeLayout<128, 16>::PART * 4;
+    return (ctas * 32 + 255) / 256 * 256 + ctas * 2 * DecodeLayout<128, 16>::PART * 4;
 }
 
 // Requests of at most max_rows rows per KV head; the others are left alone.
