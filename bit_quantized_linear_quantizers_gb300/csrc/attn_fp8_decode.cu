@@ -13,20 +13,26 @@
 // bf16 form at half the depth).
 //
 // The value scale of a page goes into the exponent instead of into V:
-//   t_j = x_j log2(e) + log2 sv_j,  m = max t,  p_j = 2^(t_j - m + 8)
+//   t_j = x_j log2(e) + log2 sv_j,  p_j = 2^(t_j - m + 7)
 //   O = sum_j p_j c_j,  l = sum_j p_j / sv_j,  result O / l,
-// since p_j = 2^(x_j log2 e) sv_j up to a factor common to O and l. p lies in
-// (0, 256] and its two parts step by 2^-9 at the finest, so p keeps 8 bits down to 2^-9 of
-// its maximum and steps of 2^-17 of it below. m, l and O are fp32.
+// since p_j = 2^(x_j log2 e) sv_j up to a factor common to O and l. m follows the
+// maximum of t, but only where it grew by more than 1.75: the largest p lies in
+// [2^7, 2^8.75], below E4M3's 448, and few units rescale O. p's two parts step by 2^-9 at
+// the finest, so p keeps 8 bits down to 2^-9 of its maximum and steps of 2^-17 of it below.
+// m, l and O are fp32.
 //
 // Work split: the units (32 keys) of every item (request, KV head, row tile), each
 // item with a charge of kItemCost units for its q, its joining and its output in front,
 // laid end to end over all requests and cut into equal shares, one CTA of 8 warps per
 // SM (without the charge, a CTA with 70 items of a unit each ran six times as long as the
 // others). Each
-// warp takes every eighth unit of the CTA's share with a private ring of TMA
-// stages (3 x 8 KB in flight per warp: 192 KB per SM, against ~45 KB that the
-// latency asks for), so no warp waits for another inside a share. At the end of a
+// warp takes every eighth unit of the CTA's share from a ring of its own (3 stages of
+// 8 KB: 192 KB in flight per SM, against ~45 KB that the latency asks for), so no warp
+// waits for another inside a share. The pages and scales of its next 32 units are looked
+// up together, a lane for each, and passed on by shuffles: looked up unit by unit they were
+// a third of the instructions; by a ninth warp for all rings, that warp's copies were
+// the bound (112 us for 64 x <= 8192 keys with no arithmetic at all). V's fragments come
+// transposed from shared memory by ldmatrix on bytes. At the end of a
 // (request, head) the eight states join in shared memory; what spans several
 // CTAs is joined by a second, small launch in a fixed order.
 #include "qz_internal.cuh"
@@ -44,7 +50,7 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 32;                         // keys of a unit
 constexpr int kStages = 3;
 constexpr int kItemCost = 12;                     // units that an item's q, joining and output take (2 us against 1.4 for 8 units)
-constexpr float kPShift = 8.0f;                   // p = 2^(t - m + 8)
+constexpr float kPShift = 7.0f, kGrow = 1.75f;     // p = 2^(t - m + 7); growth of the maximum that m lets pass
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -53,16 +59,13 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 4 x 4 byte transpose: out[i] holds byte i of a, b, c, d in that order.
-__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&out)[4]) {
-    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
-    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
-    out[0] = __byte_perm(ab0, cd0, 0x5410);
-    out[1] = __byte_perm(ab0, cd0, 0x7632);
-    out[2] = __byte_perm(ab1, cd1, 0x5410);
-    out[3] = __byte_perm(ab1, cd1, 0x7632);
+// Two 16 x 16 byte matrices transposed: lane l gives the address of row l (16 bytes). Rows
+// are keys, columns channels: r[0] and r[2] hold keys 4t .. 4t+3 and 16 + 4t .. of channel g,
+// r[1] and r[3] of channel 8 + g, as the B operand of m16n8k32 wants them.
+__device__ __forceinline__ void ldmatrix_t8(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-
 struct DecodeParams {
     CUtensorMap tm_k, tm_v;                       // codes as (head_dim, heads * page_size, num_pages)
     AttnArgs a;
@@ -127,28 +130,9 @@ struct DecodeLayout {
     static constexpr int RING = kWarps * kStages * STAGE;
     static constexpr int JOIN_F = (kWarps / 2) * R * D;             // floats
     static constexpr int META = RING + JOIN_F * 4;
-    static constexpr int SMEM = META + 1792 + 1024;                 // barriers, states, page rings; alignment
+    static constexpr int SMEM = META + 1408 + 1024;                 // barriers, states; alignment
     static constexpr int PART = R * D + 2 * R;                      // floats of a partial state
 };
-
-// One value per (row, channel) of the state, unnormalised, with m and l, goes to
-// the output; used by the main kernel and by the joining one.
-__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int hq, int D, int d0, const float* o, int n,
-                                          float m, float l) {
-    const float r = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    uint16_t* out = a.out + token * a.ldo + (int64_t)hq * D + d0;
-#pragma unroll
-    for (int i = 0; i < n; i += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(o[i + 2 * j] * r, o[i + 2 * j + 1] * r);
-            w[j] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-        *reinterpret_cast<uint4*>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if (a.lse && d0 == 0) a.lse[token * a.heads_q + hq] = l > 0.0f ? (m - kPShift + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
-}
 
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -164,13 +148,13 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     float* s_m = reinterpret_cast<float*>(smem + Lay::META + 256);                    // [warp][R]
     float* s_l = s_m + kWarps * 16;
     int64_t* s_sum = reinterpret_cast<int64_t*>(s_l + kWarps * 16);                   // [warp]
-    int* s_start = reinterpret_cast<int*>(s_sum + kWarps + 1);                        // request, unit inside it
-    int* s_page = s_start + 8;                                                        // [warp][4][3] two pages and the head of units to come
+    int* s_start = reinterpret_cast<int*>(s_sum + kWarps);                            // request, unit inside it
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int G = P.a.heads_q / P.a.kv.heads;
+    const uint32_t bar0 = smem_u32(bars + warp * kStages), ring = smem_u32(smem) + warp * kStages * Lay::STAGE;
     if (lane == 0) {
-        for (int s = 0; s < kStages; s++) mbar_init(smem_u32(bars + warp * kStages + s), 1);
+        for (int s = 0; s < kStages; s++) mbar_init(bar0 + s * 8, 1);
         fence_barrier_init();
         if (warp == 0) {
             prefetch_tmap(&P.tm_k);
@@ -225,7 +209,6 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     }
     __syncthreads();
 
-    // ---- two walks over the share: `ahead` looks up pages and issues copies, `cur` computes
     Walk<R> cur;
     cur.b = s_start[0];
     cur.r = load_req<R>(P, cur.b, G);
@@ -238,9 +221,6 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         cur.a = -(int)(inside % len);
     }
     if (!cur.mine()) cur.next_mine(P, G);
-    Walk<R> ahead = cur;
-    int ahead_base = 0;                           // units of the share before ahead's item
-    int looked = warp, issued = 0;                // next unit of this warp to look up (of the share's); units issued
 
     // q of an item: rows g (and g + 8), channels t*16 .. of each 64-channel half, as it lies in memory
     uint4 raw[RR][D / 32];
@@ -257,96 +237,104 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     };
     load_q(cur);
 
-    int* pages = s_page + warp * 12;              // ring of 4 units
-    const uint32_t ring = smem_u32(smem) + warp * kStages * Lay::STAGE;
-    const uint32_t bar0 = smem_u32(bars + warp * kStages);
-    const int page_keys = 1 << P.shift;
-    bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
-    int dead_at = -1;
-
-    // Pages of the warp's next unit, from the table (one unit ahead of its issue); h < 0: there is none.
-    struct Look { int p0, p1, h, key; };
-    auto look_up = [&]() {                        // uniform over the warp
-        Look k = {-1, -1, -1, 0};
-        while (ahead.valid() && looked >= ahead_base + ahead.hi() - ahead.lo()) {
-            ahead_base += ahead.hi() - ahead.lo();
-            ahead.next(P, G);
+    // ---- the warp's next 32 units, one per lane: pages, rows in them, scales
+    struct Batch { int p0, p1, y; float k0, v0, k1, v1; };            // y < 0: no unit; v < 0: no page
+    Walk<R> ahead = cur;                          // at the item of the batch's first unit
+    int ahead_base = 0, looked = warp;            // units of the share before that item; the batch's first unit
+    auto look_up = [&]() {                        // leaves the walk at the next batch
+        Walk<R> w = ahead;
+        int base = ahead_base;
+        const int u = looked + lane * kWarps;
+        while (w.valid() && u >= base + w.hi() - w.lo()) {
+            base += w.hi() - w.lo();
+            w.next(P, G);
         }
-        if (ahead.valid()) {
-            k.key = (ahead.lo() + looked - ahead_base) * kKeys;
-            k.h = ahead.h;
-            const int32_t* row = P.a.block_table + (int64_t)ahead.b * P.a.ld_table + (k.key >> P.shift);
+        Batch k = {-1, -1, -1, 0.0f, -1.0f, 0.0f, -1.0f};
+        if (w.valid()) {
+            const int key = (w.lo() + u - base) * kKeys;
+            k.y = (w.h << P.shift) + (key & ((1 << P.shift) - 1));
+            const int32_t* row = P.a.block_table + (int64_t)w.b * P.a.ld_table + (key >> P.shift);
             k.p0 = __ldg(row);
-            if (P.shift == 4 && k.key + 16 < ahead.r.L) k.p1 = __ldg(row + 1);
+            if (P.shift == 4 && key + 16 < w.r.L) k.p1 = __ldg(row + 1);
         }
-        looked += kWarps;
+        ahead_base = __shfl_sync(0xffffffffu, base, 31);              // (the last lane's item, or the end)
+        ahead.b = __shfl_sync(0xffffffffu, w.b, 31);
+        ahead.h = __shfl_sync(0xffffffffu, w.h, 31);
+        ahead.tile = __shfl_sync(0xffffffffu, w.tile, 31);
+        ahead.a = __shfl_sync(0xffffffffu, w.a, 31);
+        ahead.r.q0 = __shfl_sync(0xffffffffu, w.r.q0, 31);
+        ahead.r.n = __shfl_sync(0xffffffffu, w.r.n, 31);
+        ahead.r.L = __shfl_sync(0xffffffffu, w.r.L, 31);
+        ahead.r.tiles = __shfl_sync(0xffffffffu, w.r.tiles, 31);
+        ahead.r.subs = __shfl_sync(0xffffffffu, w.r.subs, 31);
+        looked += 32 * kWarps;
         return k;
     };
-    auto issue = [&](const Look& look) {          // its copies, into the warp's next stage
-        const int k = issued++, st = k % kStages;
-        const int p0 = look.p0 >= 0 && look.p0 < P.a.kv.num_pages ? look.p0 : -1;
-        const int p1 = P.shift == 4 ? (look.p1 >= 0 && look.p1 < P.a.kv.num_pages ? look.p1 : -1) : p0;
-        if (lane == 0) {
-            pages[(k & 3) * 3] = p0;
-            pages[(k & 3) * 3 + 1] = p1;
-            pages[(k & 3) * 3 + 2] = look.h;
-            if (!dead && look.h >= 0) {
-                const uint32_t dst = ring + st * Lay::STAGE, bar = bar0 + st * 8;
-                const int y = (look.h << P.shift) + (look.key & (page_keys - 1));
-                if (P.shift == 4) {
-                    mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * Lay::HALF);
-                    if (p0 >= 0) {
-                        tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
-                        tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
-                    }
-                    if (p1 >= 0) {
-                        tma_load_3d(dst + Lay::HALF / 2, &P.tm_k, 0, y, p1, bar);
-                        tma_load_3d(dst + Lay::HALF + Lay::HALF / 2, &P.tm_v, 0, y, p1, bar);
-                    }
-                } else {
-                    mbar_arrive_expect_tx(bar, (p0 >= 0) * Lay::STAGE);
-                    if (p0 >= 0) {
-                        tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
-                        tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
-                    }
+    auto load_scales = [&](Batch& k) {
+        if (k.p0 >= P.a.kv.num_pages) k.p0 = -1;
+        if (k.p1 >= P.a.kv.num_pages) k.p1 = -1;
+        const int h = k.y >> P.shift;
+        if (k.p0 >= 0) {
+            const int64_t i = (int64_t)k.p0 * P.a.kv.heads + h;
+            k.k0 = __ldg(P.a.kv.k_scale + i);
+            k.v0 = __ldg(P.a.kv.v_scale + i);
+        }
+        if (P.shift == 4 && k.p1 >= 0) {
+            const int64_t i = (int64_t)k.p1 * P.a.kv.heads + h;
+            k.k1 = __ldg(P.a.kv.k_scale + i);
+            k.v1 = __ldg(P.a.kv.v_scale + i);
+        }
+    };
+    bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
+    int dead_at = -1;
+    int issued = 0, fill = 0;                     // units whose copies are issued; their stage
+    auto issue = [&](const Batch& b) {            // copies of the warp's next unit, in lane `issued` of its batch
+        const int from = issued & 31;
+        const int p0 = __shfl_sync(0xffffffffu, b.p0, from), p1 = __shfl_sync(0xffffffffu, b.p1, from);
+        const int y = __shfl_sync(0xffffffffu, b.y, from);
+        if (y < 0) return;
+        if (lane == 0 && !dead) {
+            const uint32_t dst = ring + fill * Lay::STAGE, bar = bar0 + fill * 8;
+            if (P.shift == 4) {                   // two pages of 16 keys
+                mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * Lay::HALF);
+                if (p0 >= 0) {
+                    tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
+                    tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
+                }
+                if (p1 >= 0) {
+                    tma_load_3d(dst + Lay::HALF / 2, &P.tm_k, 0, y, p1, bar);
+                    tma_load_3d(dst + Lay::HALF + Lay::HALF / 2, &P.tm_v, 0, y, p1, bar);
+                }
+            } else {
+                mbar_arrive_expect_tx(bar, (p0 >= 0) * Lay::STAGE);
+                if (p0 >= 0) {
+                    tma_load_3d(dst, &P.tm_k, 0, y, p0, bar);
+                    tma_load_3d(dst + Lay::HALF, &P.tm_v, 0, y, p0, bar);
                 }
             }
         }
+        issued++;
+        if (++fill == kStages) fill = 0;
         __syncwarp();
     };
-    Look look;                                    // looked up, not yet issued
-    {
-        Look first[kStages];                      // the first lookups in flight together
-#pragma unroll
-        for (int s = 0; s < kStages; s++) first[s] = look_up();
-        look = look_up();
-#pragma unroll
-        for (int s = 0; s < kStages; s++) issue(first[s]);
-    }
-
+    // Batches: copies are issued from `front`, units computed from `back`, which is the same one but for the
+    // stages in flight across a batch's end; `next` is on its way meanwhile.
+    Batch front = look_up();
+    if (front.p0 >= P.a.kv.num_pages) front.p0 = -1;
+    if (front.p1 >= P.a.kv.num_pages) front.p1 = -1;
+#pragma unroll 1
+    for (int s = 0; s < kStages; s++) issue(front);
+    load_scales(front);
+    Batch back = front, next = {-1, -1, -1, 0.0f, -1.0f, 0.0f, -1.0f};
+    int done = 0;                                 // units that this warp has computed
+    int st = 0;                                   // stage of the warp's next unit, and its phase
+    uint32_t phase = 0;
     const float c0 = fabsf(P.a.sm_scale) * kLog2e;
     int unit = 0;                                 // units of the share before the item
-    int kdone = 0;                                // units that this warp has computed
-    // pages and scales of the warp's next unit, one unit ahead
-    int p0 = -1, p1 = -1;
-    float ks0 = 0.0f, ks1 = 0.0f, vs0 = 1.0f, vs1 = 1.0f;
-    auto load_scales = [&]() {
-        const int* e = pages + (kdone & 3) * 3;
-        if (e[2] < 0) return;                     // no more units
-        p0 = e[0];
-        p1 = e[1];
-        if (p0 >= 0) {
-            const int64_t i = (int64_t)p0 * P.a.kv.heads + e[2];
-            ks0 = __ldg(P.a.kv.k_scale + i);
-            vs0 = __ldg(P.a.kv.v_scale + i);
-        }
-        if (P.shift == 4 && p1 >= 0) {
-            const int64_t i = (int64_t)p1 * P.a.kv.heads + e[2];
-            ks1 = __ldg(P.a.kv.k_scale + i);
-            vs1 = __ldg(P.a.kv.v_scale + i);
-        }
-    };
-    load_scales();
+    // row of the V matrices that this lane addresses: slots 4t + {0, 1, 2, 3} of the product are keys
+    // 2t, 2t + 1, 8 + 2t, 9 + 2t, which are the scores that the lane's quad holds
+    const int slot = lane & 15, vrow = (lane & 16) + (slot & 2 ? 8 : 0) + (slot >> 2) * 2 + (slot & 1);
+    const uint32_t voff = Lay::HALF + vrow * D + (D == 128 ? (vrow & 7) << 4 : ((vrow >> 1) & 3) << 4);
 
     while (cur.valid()) {
         if (cur.r.subs == 0) {                    // no keys: zeros
@@ -419,13 +407,21 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         int first = unit + ((warp - unit) & (kWarps - 1));
 #pragma unroll 1
         for (int u = first; u < unit + here; u += kWarps) {
-            const int st = kdone % kStages, key0 = (sub + (u - unit)) * kKeys;
-            const float k0 = ks0, k1 = P.shift == 4 ? ks1 : ks0;
-            const float v0 = fmaxf(vs0, 1.2e-38f), v1 = P.shift == 4 ? fmaxf(vs1, 1.2e-38f) : v0;
-            if (!dead && !mbar_wait<false>(bar0 + st * 8, (kdone / kStages) & 1, &g_attn_decode_err)) dead = true;
-            if (__any_sync(0xffffffffu, dead) && dead_at < 0) dead = true, dead_at = kdone;
-            const uint8_t* kt = smem + (warp * kStages + st) * Lay::STAGE;
-            const uint8_t* vt = kt + Lay::HALF;
+            const int key0 = (sub + (u - unit)) * kKeys;
+            const int from = done & 31;
+            if (from == 0) back = front;          // (the copies' batch turned over at most kStages units ago)
+            const float k0 = __shfl_sync(0xffffffffu, back.k0, from), r0 = __shfl_sync(0xffffffffu, back.v0, from);
+            float k1 = k0, r1 = r0;
+            bool p0 = __shfl_sync(0xffffffffu, back.p0, from) >= 0, p1 = p0;
+            if (P.shift == 4) {
+                k1 = __shfl_sync(0xffffffffu, back.k1, from);
+                r1 = __shfl_sync(0xffffffffu, back.v1, from);
+                p1 = __shfl_sync(0xffffffffu, back.p1, from) >= 0;
+            }
+            const float v0 = fmaxf(fabsf(r0), 1.2e-38f), v1 = fmaxf(fabsf(r1), 1.2e-38f);
+            if (!dead && !mbar_wait<false>(bar0 + st * 8, phase, &g_attn_decode_err)) dead = true;
+            if (__any_sync(0xffffffffu, dead) && dead_at < 0) dead = true, dead_at = done;
+            uint8_t* kt = smem + (warp * kStages + st) * Lay::STAGE;
 
             // S = q K^T: 4 tiles of 8 keys
             float s[4][4];
@@ -466,7 +462,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                     }
             }
             const int live = cur.r.L - key0;      // keys of the unit that exist
-            const bool edge = live < kKeys || p0 < 0 || p1 < 0 || (P.a.causal && key0 + kKeys > cur.r.L - cur.r.n + 1);
+            const bool edge = live < kKeys || !p0 || !p1 || (P.a.causal && key0 + kKeys > cur.r.L - cur.r.n + 1);
             if (edge) {
 #pragma unroll
                 for (int rr = 0; rr < RR; rr++) {
@@ -475,8 +471,15 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                     for (int j = 0; j < 4; j++)
 #pragma unroll
                         for (int e = 0; e < 2; e++)
-                            if (8 * j + 2 * t + e >= lim || (j < 2 ? p0 : p1) < 0) x[rr][2 * j + e] = -INFINITY;
+                            if (8 * j + 2 * t + e >= lim || !(j < 2 ? p0 : p1)) x[rr][2 * j + e] = -INFINITY;
                 }
+                // rows of V that were never written may hold NaN codes, and 0 * NaN is no 0
+                if (lane >= live || !(lane < 16 ? p0 : p1))
+#pragma unroll
+                    for (int c = 0; c < D / 16; c++)
+                        *reinterpret_cast<uint4*>(kt + Lay::HALF + lane * D + c * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();         // before the stage's next copy
+                __syncwarp();
             }
             uint32_t ph[RR][2], pl[RR][2];
             const float iv0 = __frcp_rn(v0), iv1 = __frcp_rn(v1);
@@ -489,11 +492,11 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                 for (int e = 1; e < 8; e++) mx = fmaxf(mx, x[rr][e]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m2 = fmaxf(m[rr], mx);
-                moved |= m2 != m[rr];
-                f[rr] = m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - m2);
-                m[rr] = m2;
-                const float off = m2 == -INFINITY ? 0.0f : kPShift - m2;        // nothing seen yet: every p is 0
+                const bool raise = mx > m[rr] + kGrow || (m[rr] == -INFINITY && mx > m[rr]);
+                f[rr] = !raise ? 1.0f : m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - mx);
+                if (raise) m[rr] = mx;
+                moved |= raise;
+                const float off = m[rr] == -INFINITY ? 0.0f : kPShift - m[rr];  // nothing seen yet: every p is 0
                 float p[8];
                 float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
@@ -515,45 +518,30 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                     o[j][2] *= f[RR - 1]; o[j][3] *= f[RR - 1];
                 }
             }
-            // O += P V: slot k = 4t + i of the first half is key {2t, 2t+1, 8+2t, 9+2t}[i], of the second + 16
+            // O += P V, 16 channels at a time
+            const uint32_t va = smem_u32(kt) + voff;
 #pragma unroll
-            for (int w = 0; w < D / 64; w++) {    // 8 bytes of the thread's D / 8 channels at a time
-                uint2 vv[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {     // i = 2 jj + e: key 8 jj + 2 t + e
-                    const int r = (i >> 1) * 8 + 2 * t + (i & 1);
-                    const int ch = D == 128 ? (g ^ (r & 7)) : ((g >> 1) ^ ((r >> 1) & 3));
-                    vv[i] = *reinterpret_cast<const uint2*>(vt + r * D + ch * 16 + (D == 128 ? 8 * w : 8 * (g & 1)));
-                }
-                if (edge) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) { // never-written bytes may be NaN codes: 0 * NaN is no 0
-                        const int r = (i >> 1) * 8 + 2 * t + (i & 1);
-                        if (r >= live || (i < 4 ? p0 : p1) < 0) vv[i] = make_uint2(0u, 0u);
-                    }
-                }
-#pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    uint32_t b0[4], b1[4];
-                    transpose4(half ? vv[0].y : vv[0].x, half ? vv[1].y : vv[1].x, half ? vv[2].y : vv[2].x, half ? vv[3].y : vv[3].x, b0);
-                    transpose4(half ? vv[4].y : vv[4].x, half ? vv[5].y : vv[5].x, half ? vv[6].y : vv[6].x, half ? vv[7].y : vv[7].x, b1);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int j = w * 8 + half * 4 + e;
-                        if (RR == 1) {
-                            mma_e4m3(o[j], ph[0][0], pl[0][0], ph[0][1], pl[0][1], b0[e], b1[e]);
-                        } else {
-                            mma_e4m3(o[j], ph[0][0], ph[RR - 1][0], ph[0][1], ph[RR - 1][1], b0[e], b1[e]);
-                            mma_e4m3(o[j], pl[0][0], pl[RR - 1][0], pl[0][1], pl[RR - 1][1], b0[e], b1[e]);
-                        }
-                    }
+            for (int j = 0; j < NT; j += 2) {
+                uint32_t b[4];
+                ldmatrix_t8(b, va ^ (uint32_t)(j * 8));               // the swizzled 16-byte chunk j / 2 of the rows
+                if (RR == 1) {
+                    mma_e4m3(o[j], ph[0][0], pl[0][0], ph[0][1], pl[0][1], b[0], b[2]);
+                    mma_e4m3(o[j + 1], ph[0][0], pl[0][0], ph[0][1], pl[0][1], b[1], b[3]);
+                } else {
+                    mma_e4m3(o[j], ph[0][0], ph[RR - 1][0], ph[0][1], ph[RR - 1][1], b[0], b[2]);
+                    mma_e4m3(o[j + 1], ph[0][0], ph[RR - 1][0], ph[0][1], ph[RR - 1][1], b[1], b[3]);
+                    mma_e4m3(o[j], pl[0][0], pl[RR - 1][0], pl[0][1], pl[RR - 1][1], b[0], b[2]);
+                    mma_e4m3(o[j + 1], pl[0][0], pl[RR - 1][0], pl[0][1], pl[RR - 1][1], b[1], b[3]);
                 }
             }
-            kdone++;
             __syncwarp();                         // the stage has been read
-            load_scales();                        // of the next unit, whose pages are in the ring
-            issue(look);
-            look = look_up();
+            if (++st == kStages) { st = 0; phase ^= 1; }
+            done++;
+            // the next batch: looked up half a batch early, its scales a quarter
+            if (from == 15) next = look_up();
+            if (from == 23) load_scales(next);
+            if ((issued & 31) == 0) front = next; // (issued runs kStages ahead of done)
+            issue(front);
         }
 
         // ---- the item's end in this share: join the warps, the next item's q on its way
@@ -583,8 +571,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             }
             fw[rr] = m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - mt[rr]);
         }
-        // channel c D/8 + j of O is column c of tile j
-        float v[RR][2][NT];                       // [row][column 2t + e][j]
+        float v[RR][2][NT];                       // [row][e][j]: channel 8 j + 2 t + e
 #pragma unroll
         for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -633,23 +620,27 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                 for (int rr = 0; rr < RR; rr++) {
                     const int row = cur.tile * R + rr * 8 + g, i = row / G, a = row - i * G;
                     if (i < cur.r.n) {
+                        const float inv = lt[rr] > 0.0f ? 1.0f / lt[rr] : (lt[rr] == lt[rr] ? 0.0f : lt[rr]);
+                        const int64_t token = cur.r.q0 + i;
+                        uint16_t* out = P.a.out + token * P.a.ldo + (int64_t)(cur.h * G + a) * D + 2 * t;
 #pragma unroll
-                        for (int e = 0; e < 2; e++)
-                            write_row(P.a, cur.r.q0 + i, cur.h * G + a, D, (2 * t + e) * NT, v[rr][e], NT, mt[rr], lt[rr]);
+                        for (int j = 0; j < NT; j++)
+                            *reinterpret_cast<__nv_bfloat162*>(out + 8 * j) =
+                                __floats2bfloat162_rn(v[rr][0][j] * inv, v[rr][1][j] * inv);
+                        if (P.a.lse && t == 0)
+                            P.a.lse[token * P.a.heads_q + cur.h * G + a] =
+                                lt[rr] > 0.0f ? (mt[rr] - kPShift + __log2f(lt[rr])) * kLn2 : (lt[rr] == lt[rr] ? -INFINITY : lt[rr]);
                     }
                 }
             } else {
-                const int slot = begins ? 1 : 0;
-                float* dst = P.part + ((int64_t)blockIdx.x * 2 + slot) * Lay::PART;
+                const int part = begins ? 1 : 0;
+                float* dst = P.part + ((int64_t)blockIdx.x * 2 + part) * Lay::PART;
 #pragma unroll
                 for (int rr = 0; rr < RR; rr++) {
                     const int row = rr * 8 + g;
 #pragma unroll
-                    for (int e = 0; e < 2; e++)
-#pragma unroll
-                        for (int q = 0; q < NT / 4; q++)
-                            reinterpret_cast<float4*>(dst + row * D + (2 * t + e) * NT)[q] =
-                                make_float4(v[rr][e][4 * q], v[rr][e][4 * q + 1], v[rr][e][4 * q + 2], v[rr][e][4 * q + 3]);
+                    for (int j = 0; j < NT; j++)
+                        *reinterpret_cast<float2*>(dst + row * D + 8 * j + 2 * t) = make_float2(v[rr][0][j], v[rr][1][j]);
                     if (t == 0) {
                         dst[R * D + row] = mt[rr];
                         dst[R * D + R + row] = lt[rr];
@@ -674,8 +665,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     }
     // copies still in flight (a wait that gave up): their stages must not outlive the CTA
     if (dead)
-        for (int k = dead_at; k < dead_at + kStages && pages[(k & 3) * 3 + 2] >= 0; k++)
-            mbar_wait(bar0 + k % kStages * 8, (k / kStages) & 1, &g_attn_decode_err);
+        for (int k = dead_at; k < issued; k++) mbar_wait(bar0 + k % kStages * 8, (k / kStages) & 1, &g_attn_decode_err);
 }
 
 // Joins the states of an item that several CTAs share, in the order of its keys:
