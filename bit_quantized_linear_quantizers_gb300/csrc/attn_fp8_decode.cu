@@ -2,24 +2,22 @@
 // per KV head (single tokens, a few tokens each): the keys and values are read
 // once, so HBM is the bound.
 //
-// The codes go into the FP8 tensor products as stored. A bf16 query is the sum of
-// two E4M3 numbers, hi = E4M3(q) and lo = E4M3(q - hi), 4 + 4 significant bits,
-// after its row is scaled by a power of two that brings the row's amax into
-// [128, 256): exact for elements above 2^-10 of the amax, off by at most 2^-17 of
-// the amax below (steps of E4M3's subnormals). The probabilities are split the
-// same way, so nothing widens the cache. With up to 8 query rows per KV head, hi
-// sits in rows 0-7 of the 16-row product and lo in rows 8-15: one
-// mma.sync.m16n8k32 does both (measured 1.26 cycles per SM, against 2.0 for the
-// bf16 form at half the depth).
+// Products: mma.sync in f16, transposed, so that the query rows are the narrow side:
+//   S^T [16 keys x 8 rows] = K q^T,  O^T [16 channels x 8 rows] += V^T P^T
+// E4M3 codes widen to f16 exactly (two per instruction). FP8 operands of mma.sync
+// are no way around that: on sm_103a they are widened inside, both of them, for every
+// instruction (measured 7.1 cycles per SM for m16n8k32 with fresh operands, against
+// 2 x 2.0 for the f16 form; 900 instructions for 32 keys instead of ~300). A bf16
+// query is exact in f16 after its row is scaled by a power of two that brings its amax
+// into [2^14, 2^15), down to 2^-29 of the amax. The scores of 8 keys x 8 rows turn
+// into the second product's operand by movmatrix.
 //
 // The value scale of a page goes into the exponent instead of into V:
-//   t_j = x_j log2(e) + log2 sv_j,  p_j = 2^(t_j - m + 7)
+//   t_j = x_j log2(e) + log2 sv_j,  p_j = 2^(t_j - m + 8)
 //   O = sum_j p_j c_j,  l = sum_j p_j / sv_j,  result O / l,
-// since p_j = 2^(x_j log2 e) sv_j up to a factor common to O and l. m follows the
-// maximum of t, but only where it grew by more than 1.75: the largest p lies in
-// [2^7, 2^8.75], below E4M3's 448, and few units rescale O. p's two parts step by 2^-9 at
-// the finest, so p keeps 8 bits down to 2^-9 of its maximum and steps of 2^-17 of it below.
-// m, l and O are fp32.
+// since p_j = 2^(x_j log2 e) sv_j up to a factor common to O and l. m is raised only
+// where a t passes m + 6 (p stays below 2^14 and keeps f16's 11 bits down to 2^-14), so
+// few units rescale O. m, l and O are fp32.
 //
 // Work split: the units (32 keys) of every item (request, KV head, row tile), each
 // item with a charge of kItemCost units for its q, its joining and its output in front,
@@ -50,18 +48,34 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 32;                         // keys of a unit
 constexpr int kStages = 3;
 constexpr int kItemCost = 12;                     // units that an item's q, joining and output take (2 us against 1.4 for 8 units)
-constexpr float kPShift = 7.0f, kGrow = 1.75f;     // p = 2^(t - m + 7); growth of the maximum that m lets pass
+constexpr float kPShift = 8.0f, kGrow = 6.0f;      // p = 2^(t - m + 8); growth of the maximum that m lets pass
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Four E4M3 codes -> f16: bytes 0, 1 and 2, 3.
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{ .reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b; }"
+        : "=r"(lo), "=r"(hi) : "r"(x));
+}
+__device__ __forceinline__ uint32_t pack_f16(float x0, float x1) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+    return h;
+}
+// 8 x 8 transpose of 16-bit values over the warp (thread (g, t) holds row g, columns 2t, 2t + 1).
+__device__ __forceinline__ uint32_t transpose_f16(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
 // Two 16 x 16 byte matrices transposed: lane l gives the address of row l (16 bytes). Rows
-// are keys, columns channels: r[0] and r[2] hold keys 4t .. 4t+3 and 16 + 4t .. of channel g,
-// r[1] and r[3] of channel 8 + g, as the B operand of m16n8k32 wants them.
+// are keys, columns channels: r[0] and r[2] hold rows 4t .. 4t+3 and 16 + 4t .. of channel g,
+// r[1] and r[3] of channel 8 + g.
 __device__ __forceinline__ void ldmatrix_t8(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -128,7 +142,7 @@ struct DecodeLayout {
     static constexpr int HALF = kKeys * D;                          // bytes of K (or V) of a unit
     static constexpr int STAGE = 2 * HALF;
     static constexpr int RING = kWarps * kStages * STAGE;
-    static constexpr int JOIN_F = (kWarps / 2) * R * D;             // floats
+    static constexpr int JOIN_F = (kWarps / 2) * R * D;             // floats (and R rows of D + 4 fit)
     static constexpr int META = RING + JOIN_F * 4;
     static constexpr int SMEM = META + 1408 + 1024;                 // barriers, states; alignment
     static constexpr int PART = R * D + 2 * R;                      // floats of a partial state
@@ -138,9 +152,9 @@ template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     using Lay = DecodeLayout<D, R>;
-    constexpr int KS = D / 32;                    // 32-deep steps of q k
-    constexpr int NT = D / 8;                     // 8-channel tiles of O
-    constexpr int RR = R / 8;                     // rows of a thread
+    constexpr int KS = D / 16;                    // 16-deep steps of K q^T
+    constexpr int MT = D / 16;                    // 16-channel tiles of O^T
+    constexpr int NR = R / 8;                     // 8-row tiles
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* join = reinterpret_cast<float*>(smem + Lay::RING);
@@ -222,11 +236,11 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     }
     if (!cur.mine()) cur.next_mine(P, G);
 
-    // q of an item: rows g (and g + 8), channels t*16 .. of each 64-channel half, as it lies in memory
-    uint4 raw[RR][D / 32];
+    // q of an item: row g of each 8, channels t*16 .. of each 64-channel half, as it lies in memory
+    uint4 raw[NR][D / 32];
     auto load_q = [&](const Walk<R>& it) {
 #pragma unroll
-        for (int rr = 0; rr < RR; rr++) {
+        for (int rr = 0; rr < NR; rr++) {
             const int row = it.tile * R + rr * 8 + g, i = row / G, a = row - i * G;
             const bool there = it.valid() && i < it.r.n;
             const uint16_t* src = P.a.q + (int64_t)(it.r.q0 + i) * P.a.ldq + (int64_t)(it.h * G + a) * D + t * 16;
@@ -331,8 +345,8 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     uint32_t phase = 0;
     const float c0 = fabsf(P.a.sm_scale) * kLog2e;
     int unit = 0;                                 // units of the share before the item
-    // row of the V matrices that this lane addresses: slots 4t + {0, 1, 2, 3} of the product are keys
-    // 2t, 2t + 1, 8 + 2t, 9 + 2t, which are the scores that the lane's quad holds
+    // Row of the V matrices that this lane addresses: rows 4t + {0, 1, 2, 3} are keys 2t, 2t + 1, 8 + 2t,
+    // 9 + 2t, the depth that P's fragment gives to lane t of a quad.
     const int slot = lane & 15, vrow = (lane & 16) + (slot & 2 ? 8 : 0) + (slot >> 2) * 2 + (slot & 1);
     const uint32_t voff = Lay::HALF + vrow * D + (D == 128 ? (vrow & 7) << 4 : ((vrow >> 1) & 3) << 4);
 
@@ -351,19 +365,18 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             continue;
         }
         const int sub = cur.lo(), here = cur.hi() - sub;               // units of this item in this share
-        // ---- q of this item: rows g (and g + 8), two parts each, in the order the keys are read
-        uint32_t qf[RR][KS][4];                   // R = 8: hi b0, lo b0, hi b1, lo b1; R = 16: per row hi b0, hi b1, lo b0, lo b1
-        float crow[RR];
-        int seen[RR];                             // keys that the row sees
+        // ---- q of this item: row g of each 8 in f16, in the order the keys are read; per thread the factor
+        // and the seen keys of rows 2t, 2t + 1 of each 8, which its scores belong to
+        uint32_t qf[NR][KS][2];
+        float crow[NR][2];
+        int seen[NR][2];
 #pragma unroll
-        for (int rr = 0; rr < RR; rr++) {
-            const int i = (cur.tile * R + rr * 8 + g) / G;
-            const bool there = i < cur.r.n;
+        for (int n = 0; n < NR; n++) {
             float v[D / 4];
             float m = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 32; j++) {    // 16 bytes: channels t*16 + (j & 1)*8 of the 64-channel half j >> 1
-                const uint32_t x[4] = {raw[rr][j].x, raw[rr][j].y, raw[rr][j].z, raw[rr][j].w};
+                const uint32_t x[4] = {raw[n][j].x, raw[n][j].y, raw[n][j].z, raw[n][j].w};
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     v[j * 8 + 2 * e] = __uint_as_float(x[e] << 16);
@@ -375,32 +388,30 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
             float up, down;
-            row_scale(m, up, down);
-            crow[rr] = c0 * down;
-            const float sgn = P.a.sm_scale < 0.0f ? -up : up;
-            seen[rr] = !there ? 0 : P.a.causal ? min(max(cur.r.L - cur.r.n + i + 1, 0), cur.r.L) : cur.r.L;
+            row_scale(m, up, down);               // to [2^7, 2^8), and on to [2^14, 2^15)
+            const float sgn = (P.a.sm_scale < 0.0f ? -up : up) * 128.0f, c = c0 * down * (1.0f / 128.0f);
 #pragma unroll
-            for (int s = 0; s < KS; s++) {
-                uint32_t h0, l0, h1, l1;
-                split4(v[8 * s] * sgn, v[8 * s + 1] * sgn, v[8 * s + 2] * sgn, v[8 * s + 3] * sgn, h0, l0);
-                split4(v[8 * s + 4] * sgn, v[8 * s + 5] * sgn, v[8 * s + 6] * sgn, v[8 * s + 7] * sgn, h1, l1);
-                if (RR == 1) {
-                    qf[rr][s][0] = h0; qf[rr][s][1] = l0; qf[rr][s][2] = h1; qf[rr][s][3] = l1;
-                } else {
-                    qf[rr][s][0] = h0; qf[rr][s][1] = h1; qf[rr][s][2] = l0; qf[rr][s][3] = l1;
-                }
+            for (int k = 0; k < KS; k++)
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    qf[n][k][e] = pack_f16(v[4 * k + 2 * e] * sgn, v[4 * k + 2 * e + 1] * sgn);
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                crow[n][e] = __shfl_sync(0xffffffffu, c, (2 * t + e) * 4);
+                const int i = (cur.tile * R + n * 8 + 2 * t + e) / G;
+                seen[n][e] = i >= cur.r.n ? 0 : P.a.causal ? min(max(cur.r.L - cur.r.n + i + 1, 0), cur.r.L) : cur.r.L;
             }
         }
-        float o[NT][4];
-        float m[RR], l[RR];
+        float o[MT][NR][4];                       // channel 16 mt + g (+ 8: [2], [3]), rows 2t, 2t + 1
+        float m[NR][2], l[NR][2];
 #pragma unroll
-        for (int j = 0; j < NT; j++)
+        for (int n = 0; n < NR; n++) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) o[j][e] = 0.0f;
+            for (int j = 0; j < MT; j++)
 #pragma unroll
-        for (int rr = 0; rr < RR; rr++) {
-            m[rr] = -INFINITY;
-            l[rr] = 0.0f;
+                for (int e = 0; e < 4; e++) o[j][n][e] = 0.0f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
         }
 
         // ---- this warp's units of the item: share indices = warp mod 8
@@ -423,56 +434,54 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             if (__any_sync(0xffffffffu, dead) && dead_at < 0) dead = true, dead_at = done;
             uint8_t* kt = smem + (warp * kStages + st) * Lay::STAGE;
 
-            // S = q K^T: 4 tiles of 8 keys
-            float s[4][4];
+            // S^T = K q^T: two tiles of 16 keys
+            float s[2][NR][4];                    // key 16 mt + g (+ 8: [2], [3]), rows 2t, 2t + 1
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
+            for (int mt = 0; mt < 2; mt++) {
 #pragma unroll
-                for (int e = 0; e < 4; e++) s[j][e] = 0.0f;
-                uint32_t w[D / 16];
-                const int r = j * 8 + g;
+                for (int n = 0; n < NR; n++)
 #pragma unroll
-                for (int c = 0; c < D / 64; c++) {
-                    const int ch = D == 128 ? ((t + 4 * c) ^ g) : (t ^ ((r >> 1) & 3));
-                    const uint4 x = *reinterpret_cast<const uint4*>(kt + r * D + ch * 16);
-                    w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
-                }
+                    for (int e = 0; e < 4; e++) s[mt][n][e] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < KS; k++) {
-                    if (RR == 1) {
-                        mma_e4m3(s[j], qf[0][k][0], qf[0][k][1], qf[0][k][2], qf[0][k][3], w[2 * k], w[2 * k + 1]);
-                    } else {
-                        mma_e4m3(s[j], qf[0][k][0], qf[RR - 1][k][0], qf[0][k][1], qf[RR - 1][k][1], w[2 * k], w[2 * k + 1]);
-                        mma_e4m3(s[j], qf[0][k][2], qf[RR - 1][k][2], qf[0][k][3], qf[RR - 1][k][3], w[2 * k], w[2 * k + 1]);
-                    }
-                }
-            }
-            // scores of the row(s): x[rr][2 j + e] = key 8 j + 2 t + e
-            float x[RR][8];
-            const float lv0 = __log2f(v0), lv1 = __log2f(v1);
-#pragma unroll
-            for (int rr = 0; rr < RR; rr++) {
-                const float a0 = crow[rr] * k0, a1 = crow[rr] * k1;
-#pragma unroll
-                for (int j = 0; j < 4; j++)
+                for (int c = 0; c < D / 64; c++) {                    // 16 channels of this thread, 4 steps
+                    uint4 x[2];
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        const float raw = RR == 1 ? s[j][e] + s[j][2 + e] : s[j][2 * rr + e];
-                        x[rr][2 * j + e] = fmaf(raw, j < 2 ? a0 : a1, j < 2 ? lv0 : lv1);
+                        const int r = mt * 16 + e * 8 + g, ch = D == 128 ? ((t + 4 * c) ^ g) : (t ^ ((r >> 1) & 3));
+                        x[e] = *reinterpret_cast<const uint4*>(kt + r * D + ch * 16);
                     }
+                    const uint32_t x0[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, x1[4] = {x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        uint32_t a0, a1, a2, a3;
+                        widen4(x0[k], a0, a2);
+                        widen4(x1[k], a1, a3);
+#pragma unroll
+                        for (int n = 0; n < NR; n++)
+                            mma_f16(s[mt][n], a0, a1, a2, a3, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
+                    }
+                }
             }
+            const float lv[2] = {__log2f(v0), __log2f(v1)}, iv[2] = {__frcp_rn(v0), __frcp_rn(v1)};
             const int live = cur.r.L - key0;      // keys of the unit that exist
             const bool edge = live < kKeys || !p0 || !p1 || (P.a.causal && key0 + kKeys > cur.r.L - cur.r.n + 1);
-            if (edge) {
+            bool raise = false;
 #pragma unroll
-                for (int rr = 0; rr < RR; rr++) {
-                    const int lim = seen[rr] - key0;
+            for (int n = 0; n < NR; n++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
+                for (int mt = 0; mt < 2; mt++) {
+                    const float a0 = crow[n][0] * (mt ? k1 : k0), a1 = crow[n][1] * (mt ? k1 : k0);
+                    s[mt][n][0] = fmaf(s[mt][n][0], a0, lv[mt]);
+                    s[mt][n][1] = fmaf(s[mt][n][1], a1, lv[mt]);
+                    s[mt][n][2] = fmaf(s[mt][n][2], a0, lv[mt]);
+                    s[mt][n][3] = fmaf(s[mt][n][3], a1, lv[mt]);
+                    if (edge) {
 #pragma unroll
-                        for (int e = 0; e < 2; e++)
-                            if (8 * j + 2 * t + e >= lim || !(j < 2 ? p0 : p1)) x[rr][2 * j + e] = -INFINITY;
+                        for (int e = 0; e < 4; e++)
+                            if (16 * mt + 8 * (e >> 1) + g >= seen[n][e & 1] - key0 || !(mt ? p1 : p0)) s[mt][n][e] = -INFINITY;
+                    }
                 }
+            if (edge) {
                 // rows of V that were never written may hold NaN codes, and 0 * NaN is no 0
                 if (lane >= live || !(lane < 16 ? p0 : p1))
 #pragma unroll
@@ -481,58 +490,65 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                 fence_proxy_async_smem();         // before the stage's next copy
                 __syncwarp();
             }
-            uint32_t ph[RR][2], pl[RR][2];
-            const float iv0 = __frcp_rn(v0), iv1 = __frcp_rn(v1);
-            float f[RR];
-            bool moved = false;
+            float mx[NR][2];                      // of this thread's keys
 #pragma unroll
-            for (int rr = 0; rr < RR; rr++) {
-                float mx = x[rr][0];
+            for (int n = 0; n < NR; n++)
 #pragma unroll
-                for (int e = 1; e < 8; e++) mx = fmaxf(mx, x[rr][e]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const bool raise = mx > m[rr] + kGrow || (m[rr] == -INFINITY && mx > m[rr]);
-                f[rr] = !raise ? 1.0f : m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - mx);
-                if (raise) m[rr] = mx;
-                moved |= raise;
-                const float off = m[rr] == -INFINITY ? 0.0f : kPShift - m[rr];  // nothing seen yet: every p is 0
-                float p[8];
-                float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    p[e] = ex2(x[rr][e] + off);
-                    p[4 + e] = ex2(x[rr][4 + e] + off);
-                    s0 += p[e];
-                    s1 += p[4 + e];
+                for (int e = 0; e < 2; e++) {
+                    mx[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+                    raise |= mx[n][e] > m[n][e] + kGrow;              // (an m of -inf: anything seen)
                 }
-                l[rr] = fmaf(s1, iv1, fmaf(s0, iv0, l[rr] * f[rr]));
-                split4(p[0], p[1], p[2], p[3], ph[rr][0], pl[rr][0]);
-                split4(p[4], p[5], p[6], p[7], ph[rr][1], pl[rr][1]);
-            }
-            if (__any_sync(0xffffffffu, moved)) {
-                // the rows of o: RR = 1: c0, c1 (hi part) and c2, c3 (lo part) are both row g
+            if (__any_sync(0xffffffffu, raise)) {
+                float f[NR][2];
 #pragma unroll
-                for (int j = 0; j < NT; j++) {
-                    o[j][0] *= f[0]; o[j][1] *= f[0];
-                    o[j][2] *= f[RR - 1]; o[j][3] *= f[RR - 1];
+                for (int n = 0; n < NR; n++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        float x = mx[n][e];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        x = fmaxf(x, m[n][e]);
+                        f[n][e] = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - x);
+                        m[n][e] = x;
+                        l[n][e] *= f[n][e];
+                    }
+#pragma unroll
+                for (int j = 0; j < MT; j++)
+#pragma unroll
+                    for (int n = 0; n < NR; n++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) o[j][n][e] *= f[n][e & 1];
+            }
+            uint32_t pf[NR][4];                   // P^T: depth steps of keys 0-15 and 16-31
+#pragma unroll
+            for (int n = 0; n < NR; n++) {
+                const float f0 = m[n][0] == -INFINITY ? 0.0f : kPShift - m[n][0];   // nothing seen yet: every p is 0
+                const float f1 = m[n][1] == -INFINITY ? 0.0f : kPShift - m[n][1];
+#pragma unroll
+                for (int mt = 0; mt < 2; mt++) {
+                    const float a = ex2(s[mt][n][0] + f0), b = ex2(s[mt][n][1] + f1);
+                    const float c = ex2(s[mt][n][2] + f0), d = ex2(s[mt][n][3] + f1);
+                    l[n][0] = fmaf(a + c, iv[mt], l[n][0]);
+                    l[n][1] = fmaf(b + d, iv[mt], l[n][1]);
+                    pf[n][2 * mt] = transpose_f16(pack_f16(a, b));
+                    pf[n][2 * mt + 1] = transpose_f16(pack_f16(c, d));
                 }
             }
-            // O += P V, 16 channels at a time
+            // O^T += V^T P^T, 16 channels at a time
             const uint32_t va = smem_u32(kt) + voff;
 #pragma unroll
-            for (int j = 0; j < NT; j += 2) {
-                uint32_t b[4];
-                ldmatrix_t8(b, va ^ (uint32_t)(j * 8));               // the swizzled 16-byte chunk j / 2 of the rows
-                if (RR == 1) {
-                    mma_e4m3(o[j], ph[0][0], pl[0][0], ph[0][1], pl[0][1], b[0], b[2]);
-                    mma_e4m3(o[j + 1], ph[0][0], pl[0][0], ph[0][1], pl[0][1], b[1], b[3]);
-                } else {
-                    mma_e4m3(o[j], ph[0][0], ph[RR - 1][0], ph[0][1], ph[RR - 1][1], b[0], b[2]);
-                    mma_e4m3(o[j + 1], ph[0][0], ph[RR - 1][0], ph[0][1], ph[RR - 1][1], b[1], b[3]);
-                    mma_e4m3(o[j], pl[0][0], pl[RR - 1][0], pl[0][1], pl[RR - 1][1], b[0], b[2]);
-                    mma_e4m3(o[j + 1], pl[0][0], pl[RR - 1][0], pl[0][1], pl[RR - 1][1], b[1], b[3]);
-                }
+            for (int j = 0; j < MT; j++) {
+                uint32_t b[4], a0, a1, a2, a3;
+                ldmatrix_t8(b, va ^ (uint32_t)(j * 16));              // the swizzled 16-byte chunk j of the rows
+                widen4(b[0], a0, a2);
+                widen4(b[1], a1, a3);
+#pragma unroll
+                for (int n = 0; n < NR; n++) mma_f16(o[j][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                widen4(b[2], a0, a2);
+                widen4(b[3], a1, a3);
+#pragma unroll
+                for (int n = 0; n < NR; n++) mma_f16(o[j][n], a0, a1, a2, a3, pf[n][2], pf[n][3]);
             }
             __syncwarp();                         // the stage has been read
             if (++st == kStages) { st = 0; phase ^= 1; }
@@ -549,114 +565,122 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         nxt.next_mine(P, G);
         load_q(nxt);
 #pragma unroll
-        for (int rr = 0; rr < RR; rr++) {
-            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
-            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
-            if (t == 0) {
-                s_m[warp * 16 + rr * 8 + g] = m[rr];
-                s_l[warp * 16 + rr * 8 + g] = l[rr];
-            }
-        }
-        __syncthreads();
-        float mt[RR], lt[RR], fw[RR];
-#pragma unroll
-        for (int rr = 0; rr < RR; rr++) {
-            mt[rr] = -INFINITY;
-            lt[rr] = 0.0f;
-            for (int w = 0; w < kWarps; w++) mt[rr] = fmaxf(mt[rr], s_m[w * 16 + rr * 8 + g]);
-            for (int w = 0; w < kWarps; w++) {
-                const float mw = s_m[w * 16 + rr * 8 + g];
-                const float lw = s_l[w * 16 + rr * 8 + g];
-                lt[rr] += mw == -INFINITY && lw == 0.0f ? 0.0f : lw * ex2(mw - mt[rr]);
-            }
-            fw[rr] = m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - mt[rr]);
-        }
-        float v[RR][2][NT];                       // [row][e][j]: channel 8 j + 2 t + e
-#pragma unroll
-        for (int j = 0; j < NT; j++)
+        for (int n = 0; n < NR; n++)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                if (RR == 1) {
-                    v[0][e][j] = (o[j][e] + o[j][2 + e]) * fw[0];
-                } else {
-                    v[0][e][j] = o[j][e] * fw[0];
-                    v[RR - 1][e][j] = o[j][2 + e] * fw[RR - 1];
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+                if (g == 0) {
+                    s_m[warp * 16 + n * 8 + 2 * t + e] = m[n][e];
+                    s_l[warp * 16 + n * 8 + 2 * t + e] = l[n][e];
+                }
+            }
+        __syncthreads();
+        float mt[NR][2], lt[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int row = n * 8 + 2 * t + e;
+                float x = -INFINITY, y = 0.0f;
+                for (int w = 0; w < kWarps; w++) x = fmaxf(x, s_m[w * 16 + row]);
+                for (int w = 0; w < kWarps; w++) {
+                    const float mw = s_m[w * 16 + row], lw = s_l[w * 16 + row];
+                    y += mw == -INFINITY && lw == 0.0f ? 0.0f : lw * ex2(mw - x);
+                }
+                mt[n][e] = x;
+                lt[n][e] = y;
+                const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - x);
+#pragma unroll
+                for (int j = 0; j < MT; j++) {
+                    o[j][n][e] *= f;
+                    o[j][n][2 + e] *= f;
                 }
             }
 #pragma unroll 1
         for (int half = kWarps / 2; half > 0; half >>= 1) {
             // a thread's values one float4 apart from its neighbours': no bank conflicts
             if (warp >= half && warp < 2 * half) {
-                float4* dst = reinterpret_cast<float4*>(join + (warp - half) * R * D);
+                float4* dst = reinterpret_cast<float4*>(join + (warp - half) * R * D) + lane;
 #pragma unroll
-                for (int rr = 0; rr < RR; rr++)
+                for (int j = 0; j < MT; j++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++)
-#pragma unroll
-                        for (int q = 0; q < NT / 4; q++)
-                            dst[((rr * 2 + e) * (NT / 4) + q) * 32 + lane] = make_float4(v[rr][e][4 * q], v[rr][e][4 * q + 1],
-                                                                                         v[rr][e][4 * q + 2], v[rr][e][4 * q + 3]);
+                    for (int n = 0; n < NR; n++)
+                        dst[(j * NR + n) * 32] = make_float4(o[j][n][0], o[j][n][1], o[j][n][2], o[j][n][3]);
             }
             __syncthreads();
             if (warp < half) {
-                const float4* src = reinterpret_cast<const float4*>(join + warp * R * D);
+                const float4* src = reinterpret_cast<const float4*>(join + warp * R * D) + lane;
 #pragma unroll
-                for (int rr = 0; rr < RR; rr++)
+                for (int j = 0; j < MT; j++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++)
-#pragma unroll
-                        for (int q = 0; q < NT / 4; q++) {
-                            const float4 x = src[((rr * 2 + e) * (NT / 4) + q) * 32 + lane];
-                            v[rr][e][4 * q] += x.x; v[rr][e][4 * q + 1] += x.y;
-                            v[rr][e][4 * q + 2] += x.z; v[rr][e][4 * q + 3] += x.w;
-                        }
+                    for (int n = 0; n < NR; n++) {
+                        const float4 x = src[(j * NR + n) * 32];
+                        o[j][n][0] += x.x;
+                        o[j][n][1] += x.y;
+                        o[j][n][2] += x.z;
+                        o[j][n][3] += x.w;
+                    }
             }
             __syncthreads();
         }
         if (warp == 0) {
             const bool begins = sub == 0, ends = sub + here == cur.r.subs;
-            if (begins && ends) {
+            // rows back to rows: [row][channel] in shared memory (4 floats of padding), then 16 bytes a lane
+            constexpr int LD = D + 4;
 #pragma unroll
-                for (int rr = 0; rr < RR; rr++) {
-                    const int row = cur.tile * R + rr * 8 + g, i = row / G, a = row - i * G;
-                    if (i < cur.r.n) {
-                        const float inv = lt[rr] > 0.0f ? 1.0f / lt[rr] : (lt[rr] == lt[rr] ? 0.0f : lt[rr]);
-                        const int64_t token = cur.r.q0 + i;
-                        uint16_t* out = P.a.out + token * P.a.ldo + (int64_t)(cur.h * G + a) * D + 2 * t;
+            for (int n = 0; n < NR; n++)
 #pragma unroll
-                        for (int j = 0; j < NT; j++)
-                            *reinterpret_cast<__nv_bfloat162*>(out + 8 * j) =
-                                __floats2bfloat162_rn(v[rr][0][j] * inv, v[rr][1][j] * inv);
-                        if (P.a.lse && t == 0)
-                            P.a.lse[token * P.a.heads_q + cur.h * G + a] =
-                                lt[rr] > 0.0f ? (mt[rr] - kPShift + __log2f(lt[rr])) * kLn2 : (lt[rr] == lt[rr] ? -INFINITY : lt[rr]);
+                for (int e = 0; e < 2; e++) {
+                    const int row = n * 8 + 2 * t + e;
+#pragma unroll
+                    for (int j = 0; j < MT; j++) {
+                        join[row * LD + j * 16 + g] = o[j][n][e];
+                        join[row * LD + j * 16 + 8 + g] = o[j][n][2 + e];
+                    }
+                    if (g == 0) {
+                        s_m[row] = mt[n][e];      // (every warp has read these)
+                        s_l[row] = lt[n][e];
                     }
                 }
-            } else {
-                const int part = begins ? 1 : 0;
-                float* dst = P.part + ((int64_t)blockIdx.x * 2 + part) * Lay::PART;
+            __syncwarp();
+            float* dst = P.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * Lay::PART;
 #pragma unroll
-                for (int rr = 0; rr < RR; rr++) {
-                    const int row = rr * 8 + g;
-#pragma unroll
-                    for (int j = 0; j < NT; j++)
-                        *reinterpret_cast<float2*>(dst + row * D + 8 * j + 2 * t) = make_float2(v[rr][0][j], v[rr][1][j]);
-                    if (t == 0) {
-                        dst[R * D + row] = mt[rr];
-                        dst[R * D + R + row] = lt[rr];
+            for (int c = lane; c < R * D / 4; c += 32) {
+                const int row = c / (D / 4), d0 = c % (D / 4) * 4;
+                const float4 x = *reinterpret_cast<const float4*>(join + row * LD + d0);
+                const float mr = s_m[row], lr = s_l[row];
+                if (!(begins && ends)) {
+                    *reinterpret_cast<float4*>(dst + row * D + d0) = x;
+                    if (d0 == 0) {
+                        dst[R * D + row] = mr;
+                        dst[R * D + R + row] = lr;
                     }
+                    continue;
                 }
-                if (lane == 0) {
-                    if (begins) {                 // the joining launch starts here
-                        header[2] = 0;
-                        header[3] = cur.r.q0;
-                        header[4] = cur.r.n;
-                        header[5] = cur.tile * R;
-                        header[6] = cur.h;
-                    } else {
-                        header[0] = 0;
-                        header[1] = !ends;        // goes on in the next CTA
-                    }
+                const int i = (cur.tile * R + row) / G, a = cur.tile * R + row - i * G;
+                if (i < cur.r.n) {
+                    const float inv = lr > 0.0f ? 1.0f / lr : (lr == lr ? 0.0f : lr);
+                    const int64_t token = cur.r.q0 + i;
+                    const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), y1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+                    *reinterpret_cast<uint2*>(P.a.out + token * P.a.ldo + (int64_t)(cur.h * G + a) * D + d0) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+                    if (P.a.lse && d0 == 0)
+                        P.a.lse[token * P.a.heads_q + cur.h * G + a] =
+                            lr > 0.0f ? (mr - kPShift + __log2f(lr)) * kLn2 : (lr == lr ? -INFINITY : lr);
+                }
+            }
+            if (!(begins && ends) && lane == 0) {
+                if (begins) {                     // the joining launch starts here
+                    header[2] = 0;
+                    header[3] = cur.r.q0;
+                    header[4] = cur.r.n;
+                    header[5] = cur.tile * R;
+                    header[6] = cur.h;
+                } else {
+                    header[0] = 0;
+                    header[1] = !ends;            // goes on in the next CTA
                 }
             }
         }

@@ -7,9 +7,10 @@
 // A CTA takes 256 rows (two 128-row tiles, one warpgroup of softmax each) and
 // walks the keys in tiles of 128:
 //   S = q K^T    kind::f8f6f4. K enters as stored; bf16 q is the sum of two E4M3
-//                parts (4 + 4 significant bits, see attn_fp8_decode.cu), two MMAs at
-//                twice the bf16 rate each: the time of a bf16 product, and no
-//                widening of K.
+//                parts (hi = E4M3(q), lo = E4M3(q - hi): 4 + 4 significant bits, after a
+//                power of two brings the row's amax into [128, 256); exact above 2^-10 of the amax,
+//                off by at most 2^-17 of it below), two MMAs at twice the bf16 rate each: the
+//                time of a bf16 product, and no widening of K.
 //   O += P V     kind::f16, P from TMEM in f16 (11 bits), V widened from E4M3 to f16 (exact)
 //                by a warpgroup of its own. Splitting P into two E4M3 parts as well would
 //                spare the widening but costs 14 issue cycles per pair of scores and
