@@ -804,6 +804,20 @@ class PagedKV:
         return cls(codes[0], codes[1], scales[0], scales[1])
 
 
+# The calls of a serving step are short, so their host time counts: the common case of each
+# check is one expression, and the helpers that name what is wrong run only where it fails.
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _i32(t, name, dev, n):
+    """Device pointer of a dense int32 tensor of n elements."""
+    if t.get_device() == dev and t.dtype is torch.int32 and t.is_contiguous() and t.numel() == n:
+        return t.data_ptr()
+    return _arg(t, name, dev, torch.int32, n)
+
+
 def _table(t, name, dev):
     if t.get_device() != dev or t.dtype is not torch.int32 or t.dim() != 2 or (t.numel() and t.stride(1) != 1):
         raise ValueError(f"{name}: expected a 2-D int32 tensor on cuda:{dev} with dense rows, got {t.dtype} "
@@ -814,13 +828,14 @@ def _table(t, name, dev):
 
 def _rows3(t, name, dev, heads, head_dim):
     """[tokens, heads, head_dim] with dense heads; returns the stride between tokens."""
-    if (t.dim() != 3 or t.get_device() != dev or (heads is not None and t.shape[1] != heads)
-            or t.shape[2] != head_dim):
+    shape = t.shape
+    if (len(shape) != 3 or t.get_device() != dev or (heads is not None and shape[1] != heads)
+            or shape[2] != head_dim):
         raise ValueError(f"{name}: expected [tokens, {heads if heads is not None else 'heads'}, {head_dim}] on "
-                         f"cuda:{dev}, got {tuple(t.shape)}")
-    n, h, d = t.shape
+                         f"cuda:{dev}, got {tuple(shape)}")
+    n, h, d = shape
     s0, s1, s2 = t.stride()
-    if t.numel() and (s2 != 1 or (h > 1 and s1 != d)):
+    if (s2 != 1 or (s1 != d and h > 1)) and t.numel():
         raise ValueError(f"{name}: the heads of a token must be dense, got strides {(s0, s1, s2)}")
     return s0 if n > 1 else h * d
 
@@ -834,17 +849,25 @@ def qz_block_tables(ctx_lens, new_lens, block_table, free_pages, free_head, page
     d = _device()
     tab, B, blocks, ld = _table(block_table, "block_table", d)
     i32, dev = torch.int32, block_table.device
-    slot_map = torch.empty((n_slots,), dtype=i32, device=dev) if slot_map is None else slot_map
-    positions = torch.empty((n_slots,), dtype=i32, device=dev) if positions is None else positions
-    cu_new = torch.empty((B + 1,), dtype=i32, device=dev) if cu_new is None else cu_new
-    kv_lens = torch.empty((B,), dtype=i32, device=dev) if kv_lens is None else kv_lens
-    free_head_out = torch.empty((1,), dtype=i32, device=dev) if free_head_out is None else free_head_out
-    _check(lib.qz_block_tables(
-        _arg(ctx_lens, "ctx_lens", d, i32, B), _arg(new_lens, "new_lens", d, i32, B), B, page_size, tab, blocks, ld,
-        _arg(free_pages, "free_pages", d, i32), free_pages.numel(), _arg(free_head, "free_head", d, i32, 1),
-        _arg(kv_lens, "kv_lens", d, i32, B), _arg(cu_new, "cu_new", d, i32, B + 1),
-        _arg(slot_map, "slot_map", d, i32, n_slots), _arg(positions, "positions", d, i32, n_slots), n_slots,
-        _arg(free_head_out, "free_head_out", d, i32, 1), _stream(stream)), "qz_block_tables")
+    if slot_map is None:
+        slot_map = torch.empty((n_slots,), dtype=i32, device=dev)
+    if positions is None:
+        positions = torch.empty((n_slots,), dtype=i32, device=dev)
+    if cu_new is None:
+        cu_new = torch.empty((B + 1,), dtype=i32, device=dev)
+    if kv_lens is None:
+        kv_lens = torch.empty((B,), dtype=i32, device=dev)
+    if free_head_out is None:
+        free_head_out = torch.empty((1,), dtype=i32, device=dev)
+    n_free = free_pages.numel()
+    st = lib.qz_block_tables(
+        _i32(ctx_lens, "ctx_lens", d, B), _i32(new_lens, "new_lens", d, B), B, page_size, tab, blocks, ld,
+        _i32(free_pages, "free_pages", d, n_free), n_free, _i32(free_head, "free_head", d, 1),
+        _i32(kv_lens, "kv_lens", d, B), _i32(cu_new, "cu_new", d, B + 1), _i32(slot_map, "slot_map", d, n_slots),
+        _i32(positions, "positions", d, n_slots), n_slots, _i32(free_head_out, "free_head_out", d, 1),
+        _raw_stream(stream, d))
+    if st:
+        raise QZError(st, "qz_block_tables")
     return slot_map, positions, cu_new, kv_lens, free_head_out
 
 
@@ -862,12 +885,13 @@ def qz_kv_append_fp8_paged(k, v, slot_map, cache: PagedKV, stream=None):
     _on_cache(cache, d)
     ldk = _rows3(k, "k", d, cache.heads, cache.head_dim)
     ldv = _rows3(v, "v", d, cache.heads, cache.head_dim)
-    if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
-        raise ValueError("k and v must have the same number of tokens and dtype")
     n = k.shape[0]
-    _check(lib.qz_kv_append_fp8_paged(k.data_ptr(), v.data_ptr(), _dtype_code(k), n, ldk, ldv,
-                                      _arg(slot_map, "slot_map", d, torch.int32, n), cache._ref, _stream(stream)),
-           "qz_kv_append_fp8_paged")
+    if v.shape[0] != n or k.dtype is not v.dtype:
+        raise ValueError("k and v must have the same number of tokens and dtype")
+    st = lib.qz_kv_append_fp8_paged(k.data_ptr(), v.data_ptr(), _dtype_code(k), n, ldk, ldv,
+                                    _i32(slot_map, "slot_map", d, n), cache._ref, _raw_stream(stream, d))
+    if st:
+        raise QZError(st, "qz_kv_append_fp8_paged")
 
 
 def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int, scale: float, causal: bool = True,
@@ -878,8 +902,9 @@ def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int,
     (out bf16 like q, lse); lse=True allocates fp32 [tokens, heads_q], None leaves it out."""
     d = _device()
     _on_cache(cache, d)
-    ldq = _rows3(q, "q", d, None, cache.head_dim)
-    tokens, hq, dim = q.shape
+    dim = cache.head_dim
+    ldq = _rows3(q, "q", d, None, dim)
+    tokens, hq, _ = q.shape
     if q.dtype is not torch.bfloat16:
         raise TypeError(f"qz_attn_fp8_paged takes bfloat16 queries, got {q.dtype}")
     tab, B, blocks, ld = _table(block_table, "block_table", d)
@@ -892,10 +917,12 @@ def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int,
             raise ValueError(f"out: expected bfloat16 {(tokens, hq, dim)}, got {out.dtype} {tuple(out.shape)}")
     if lse is True:
         lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device)
-    args = (_arg(kv_lens, "kv_lens", d, torch.int32, B), float(scale), int(bool(causal)), out.data_ptr(), ldo,
-            _opt(lse, "lse", d, torch.float32, tokens * hq))
+    p_cu, p_kv = _i32(cu_q, "cu_q", d, B + 1), _i32(kv_lens, "kv_lens", d, B)
+    p_lse = _opt(lse, "lse", d, torch.float32, tokens * hq)
     buf, nb = _ws(ws, qz_workspace_size(OP_ATTN_FP8_PAGED, max_q * (hq // cache.heads), dim), d)
-    _check(lib.qz_attn_fp8_paged(q.data_ptr(), ldq, tokens, hq, _arg(cu_q, "cu_q", d, torch.int32, B + 1), B, max_q,
-                                 cache._ref, tab, blocks, ld, *args, _ptr(buf), nb, _stream(stream)),
-           "qz_attn_fp8_paged")
+    st = lib.qz_attn_fp8_paged(q.data_ptr(), ldq, tokens, hq, p_cu, B, max_q, cache._ref, tab,
+                               blocks, ld, p_kv, scale, 1 if causal else 0, out.data_ptr(), ldo,
+                               p_lse, _ptr(buf), nb, _raw_stream(stream, d))
+    if st:
+        raise QZError(st, "qz_attn_fp8_paged")
     return out, lse
