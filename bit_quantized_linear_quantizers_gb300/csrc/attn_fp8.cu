@@ -5,8 +5,6 @@
 #include "qz_internal.cuh"
 #include "qz_paged.cuh"
 
-#include <algorithm>
-
 namespace qz {
 
 namespace {
@@ -16,17 +14,23 @@ namespace {
 constexpr int kDecodeRows = 64;
 } // namespace
 
-// The two kernels of a call run one after the other and share the workspace.
+namespace {
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+} // namespace
+
+// The two kernels of a call may overlap: a workspace each.
 size_t ws_attn_paged(int64_t rows, int64_t) {
-    return rows <= kDecodeRows ? ws_attn_decode() : std::max(ws_attn_decode(), ws_attn_prefill());
+    return rows <= kDecodeRows ? ws_attn_decode() : round256(ws_attn_decode()) + ws_attn_prefill();
 }
 
 qz_status attn_paged_launch(const AttnArgs& a, void* ws, cudaStream_t st) {
     const int64_t rows = (int64_t)a.max_q * (a.heads_q / a.kv.heads);
-    if (rows <= kDecodeRows) return attn_decode_launch(a, kDecodeRows, ws, st);
-    if (a.B == 1) return attn_prefill_launch(a, 1, ws, st);          // one request: no second launch for what it is not
-    QZ_TRY(attn_prefill_launch(a, kDecodeRows + 1, ws, st));
-    return attn_decode_launch(a, kDecodeRows, ws, st);
+    if (rows <= kDecodeRows) return attn_decode_launch(a, kDecodeRows, false, ws, st);
+    void* ws2 = static_cast<char*>(ws) + round256(ws_attn_decode());
+    bool joined = false;
+    if (a.B == 1) return attn_prefill_launch(a, 1, ws2, &joined, st);     // one request: no second launch for what it is not
+    QZ_TRY(attn_prefill_launch(a, kDecodeRows + 1, ws2, &joined, st));
+    return attn_decode_launch(a, kDecodeRows, !joined, ws, st);
 }
 
 } // namespace qz

@@ -85,6 +85,7 @@ struct DecodeParams {
     AttnArgs a;
     int shift;                                    // log2 page_size
     int max_rows;                                 // requests with more rows per KV head are not taken
+    int beside;                                   // the launch before is the prefill kernel on other requests: wait at the end
     int* head;                                    // [CTAs][8]: what the CTA left for the joining launch: 0: the part of an
                                                   // item begun before (0 or -1), 1: it goes on, 2: an item that goes on
                                                   // begins here (0 or -1), 3 .. 6: its first token, tokens, first row, KV head
@@ -175,7 +176,10 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             prefetch_tmap(&P.tm_v);
         }
     }
-    pdl_wait();
+    // The prefill kernel lets this one start when its CTAs have waited for the stream's earlier work
+    // themselves and begin to leave; the two share no memory that either writes. The wait for its end
+    // comes last, so that whatever waits for this kernel waits for both.
+    if (!P.beside) pdl_wait();
     pdl_trigger();                                // the joining launch may come up; it waits for this one's end
 
     // ---- the CTA's share: all units counted, then the request that holds its first one
@@ -196,7 +200,10 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
     int* header = P.head + blockIdx.x * 8;
     if (threadIdx.x == 0) header[0] = header[2] = -1;
-    if (u0 >= u1) return;
+    if (u0 >= u1) {
+        if (P.beside) pdl_wait();
+        return;
+    }
     int64_t before = 0;
     for (int b0 = 0; b0 < P.a.B; b0 += kThreads) {
         int64_t v = b0 == 0 ? mine0 : units_of(b0 + threadIdx.x);
@@ -690,6 +697,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     // copies still in flight (a wait that gave up): their stages must not outlive the CTA
     if (dead)
         for (int k = dead_at; k < issued; k++) mbar_wait(bar0 + k % kStages * 8, (k / kStages) & 1, &g_attn_decode_err);
+    if (P.beside) pdl_wait();
 }
 
 // Joins the states of an item that several CTAs share, in the order of its keys:
@@ -756,9 +764,11 @@ size_t ws_attn_decode() {
     return (ctas * 32 + 255) / 256 * 256 + ctas * 2 * DecodeLayout<128, 16>::PART * 4;
 }
 
-// Requests of at most max_rows rows per KV head; the others are left alone.
-qz_status attn_decode_launch(const AttnArgs& a, int max_rows, void* ws, cudaStream_t st) {
+// Requests of at most max_rows rows per KV head; the others are left alone. beside: launched directly
+// after the prefill kernel of the same call, with a workspace of its own.
+qz_status attn_decode_launch(const AttnArgs& a, int max_rows, bool beside, void* ws, cudaStream_t st) {
     DecodeParams P;
+    P.beside = beside;
     P.a = a;
     P.shift = a.kv.page_size == 16 ? 4 : a.kv.page_size == 32 ? 5 : a.kv.page_size == 64 ? 6 : 7;
     P.max_rows = max_rows;

@@ -75,7 +75,7 @@ struct PrefillLayout {
     static constexpr int VH_OFF = V_OFF + kVStages * KT;
     static constexpr int SC_OFF = VH_OFF + 2 * VH;                  // [stage][8] float4: scales of 16 keys
     static constexpr int BAR_OFF = SC_OFF + kScStages * 8 * 16;
-    static constexpr int SMEM = BAR_OFF + 512 + 1024;
+    static constexpr int SMEM = BAR_OFF + 640 + 1024;
     static constexpr int PART = kRows * D + 2 * kRows;              // floats of a part's state
     static constexpr uint32_t S_COL = 0, O_COL = 256;               // TMEM columns: S0 S1 O0 O1
     static constexpr uint32_t IDESC_S = idesc_dense(0u, 0u, kM, kN);                     // E4M3 x E4M3
@@ -173,6 +173,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
     uint8_t* canceled = smem + L::BAR_OFF + 384;                    // 16 bytes
     Item* items = reinterpret_cast<Item*>(smem + L::BAR_OFF + 400); // two: a role's current one stays here, not in registers
+    int* classes = reinterpret_cast<int*>(smem + L::BAR_OFF + 512);  // [32] row tiles of the requests of a class
     float4* sc = reinterpret_cast<float4*>(smem + L::SC_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -570,40 +571,62 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             }
         } else if (warp == 13) {
             // ------------------------------------------------------ items
+            // Requests in classes of similar length (two for each power of two of key tiles), the longest first,
+            // and a request's last row tiles first: what begins last is short.
+            auto request = [&](int b, int& start, int& n, int& cls) {               // its row tiles
+                if (b >= P.a.B) return 0;
+                start = __ldg(P.a.cu_q + b);
+                n = min(__ldg(P.a.cu_q + b + 1) - start, P.a.max_q);
+                const int64_t rows = (int64_t)max(n, 0) * G;
+                const int kt = max((__ldg(P.a.kv_lens + b) + kN - 1) / kN, 1), lg = 31 - __clz(kt);
+                cls = 31 - min(2 * lg + (lg > 0 ? kt >> (lg - 1) & 1 : 0), 31);
+                return rows < P.min_rows ? 0 : (int)((rows + kRows - 1) / kRows);
+            };
+            classes[lane] = 0;
+            __syncwarp();
+            for (int b = lane; b < P.a.B; b += 32) {
+                int start, n, cls;
+                const int own = request(b, start, n, cls);
+                if (own) atomicAdd(classes + cls, own);               // whole numbers: any order
+            }
+            __syncwarp();
+            int upto = classes[lane];             // row tiles of the classes up to this lane's
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += u;
+            }
             int id = blockIdx.x, asked = 0;
             for (int k = 0; ; ) {
                 Item it;
                 it.b = -1;
-                if (id >= 0) {                    // the last row tiles (the longest under the causal rule) first
+                if (id >= 0) {
                     it.h = id % P.a.kv.heads;
-                    const int rest = id / P.a.kv.heads, split = rest % P.splits, want = P.tiles - 1 - rest / P.splits;
-                    int before = 0;
-                    for (int b0 = 0; b0 < P.a.B; b0 += 32) {
-                        const int b = b0 + lane;
-                        int own = 0, start = 0, n = 0;
-                        if (b < P.a.B) {
-                            start = __ldg(P.a.cu_q + b);
-                            n = min(__ldg(P.a.cu_q + b + 1) - start, P.a.max_q);
-                            const int64_t rows = (int64_t)max(n, 0) * G;
-                            own = rows < P.min_rows ? 0 : (int)((rows + kRows - 1) / kRows);
+                    const int rest = id / P.a.kv.heads, split = rest % P.splits, want = rest / P.splits;
+                    const uint32_t past = __ballot_sync(0xffffffffu, upto > want);
+                    if (past) {
+                        const int cls = __ffs(past) - 1;
+                        int before = cls ? __shfl_sync(0xffffffffu, upto, cls - 1) : 0;
+                        for (int b0 = 0; b0 < P.a.B; b0 += 32) {
+                            int start = 0, n = 0, c = -1;
+                            int own = request(b0 + lane, start, n, c);
+                            if (c != cls) own = 0;
+                            int v = own;
+                            for (int o = 1; o < 32; o <<= 1) {
+                                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                                if (lane >= o) v += u;
+                            }
+                            const int first = before + v - own;
+                            const uint32_t hit = __ballot_sync(0xffffffffu, want >= first && want < first + own);
+                            if (hit) {
+                                const int l0 = __ffs(hit) - 1;
+                                it.b = b0 + l0;
+                                it.row0 = (__shfl_sync(0xffffffffu, own, l0) - 1 - (want - __shfl_sync(0xffffffffu, first, l0))) * kRows;
+                                it.q0 = __shfl_sync(0xffffffffu, start, l0);
+                                it.n = __shfl_sync(0xffffffffu, n, l0);
+                                break;
+                            }
+                            before += __shfl_sync(0xffffffffu, v, 31);
                         }
-                        int v = own;
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const int u = __shfl_up_sync(0xffffffffu, v, o);
-                            if (lane >= o) v += u;
-                        }
-                        const int first = before + v - own;
-                        const uint32_t hit = __ballot_sync(0xffffffffu, want >= first && want < first + own);
-                        if (hit) {
-                            const int l0 = __ffs(hit) - 1;
-                            it.b = b0 + l0;
-                            it.row0 = (want - __shfl_sync(0xffffffffu, first, l0)) * kRows;
-                            it.q0 = __shfl_sync(0xffffffffu, start, l0);
-                            it.n = __shfl_sync(0xffffffffu, n, l0);
-                            break;
-                        }
-                        before += __shfl_sync(0xffffffffu, v, 31);
-                        if (before > want) break;
                     }
                     if (P.splits > 1 && split == 0 && lane == 0) {
                         P.head[(want * P.a.kv.heads + it.h) * 2] = it.b;
@@ -784,7 +807,7 @@ size_t ws_attn_prefill() {
 }
 
 // Requests of at least min_rows rows per KV head; the others are left alone.
-qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, void* ws, cudaStream_t st) {
+qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, void* ws, bool* joined, cudaStream_t st) {
     PrefillParams P;
     P.a = a;
     P.shift = a.kv.page_size == 16 ? 4 : a.kv.page_size == 32 ? 5 : a.kv.page_size == 64 ? 6 : 7;
@@ -806,6 +829,7 @@ qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, void* ws, cudaStr
     if (tiles * a.kv.heads * splits > 0x7fffffff) return QZ_ERR_SHAPE;
     P.tiles = (int)tiles;
     P.splits = (int)splits;
+    *joined = splits > 1;                         // a second launch follows
     const int64_t ctas = tiles * a.kv.heads * splits;
     return a.kv.head_dim == 64 ? launch_prefill<64>(P, ctas, ws, st) : launch_prefill<128>(P, ctas, ws, st);
 }

@@ -35,11 +35,11 @@ size_t ws_attn_paged(int64_t rows, int64_t head_dim);
 qz_status attn_paged_launch(const AttnArgs& a, void* ws, cudaStream_t st);
 // the requests of at most max_rows query rows per KV head (attn_fp8_decode.cu)
 size_t ws_attn_decode();
-qz_status attn_decode_launch(const AttnArgs& a, int max_rows, void* ws, cudaStream_t st);
+qz_status attn_decode_launch(const AttnArgs& a, int max_rows, bool beside, void* ws, cudaStream_t st);
 qz_status attn_decode_error_read_and_clear();
 // the requests of at least min_rows query rows per KV head (attn_fp8_prefill.cu)
 size_t ws_attn_prefill();
-qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, void* ws, cudaStream_t st);
+qz_status attn_prefill_launch(const AttnArgs& a, int min_rows, void* ws, bool* joined, cudaStream_t st);
 qz_status attn_prefill_error_read_and_clear();
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
