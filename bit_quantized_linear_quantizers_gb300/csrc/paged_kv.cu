@@ -141,6 +141,54 @@ __device__ __forceinline__ void e4m3_codes8(const float v[8], const Recip& d, ui
     hi = e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16;
 }
 
+// Eight input values as they lie in memory (bf16: 16 bytes, fp32: 32), held so until
+// they are encoded: widened on arrival, 16 tokens of bf16 took 64 registers a lane instead
+// of 32, and half as many CTAs fitted an SM.
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> {
+    uint4 w;
+    __device__ __forceinline__ void load(const uint16_t* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float amax() const {
+        uint32_t m = 0;                           // both halves at once: the order of the bits below the sign is the values'
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) m = __vmaxu2(m, x[i] & 0x7FFF7FFFu);
+        if ((m & 0xFFFFu) > 0x7F80u || (m >> 16) > 0x7F80u) {          // a NaN: left out of the maximum, as fmaxf does
+            float v[8], f = 0.0f;
+            widen(v);
+#pragma unroll
+            for (int i = 0; i < 8; i++) f = fmaxf(f, fabsf(v[i]));
+            return f;
+        }
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ void widen(float (&v)[8]) const {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(x[i] << 16);
+            v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+        }
+    }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ float amax() const {
+        return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                     fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+    }
+    __device__ __forceinline__ void widen(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+
 // A group of W = page_size / 16 warps takes the pages whose first new token
 // lies in its window of `window` tokens, for one head of K or V (blockIdx.y).
 // Warp w of the group holds tokens 16w .. 16w+15 of the page's run in
@@ -148,7 +196,7 @@ __device__ __forceinline__ void e4m3_codes8(const float v[8], const Recip& d, ui
 // goes through shared memory. Bound by HBM for prompts and by latency for
 // single tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 4 : 2)
 kv_append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t tokens, int64_t ldk, int64_t ldv,
                  const int32_t* __restrict__ slot_map, qz_paged_kv c, int shift, int window) {
     constexpr int kWarps = kAppendThreads / 32;
@@ -188,20 +236,16 @@ kv_append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t token
             }
             const int off0 = __ldg(slot_map + t0) & (P - 1);
             const int r0 = wig * kStrip + lane / kRowLanes, d0 = (lane % kRowLanes) * 8;
-            float val[kSteps][8];
+            Raw8<T> val[kSteps];
             float m = 0.0f;
 #pragma unroll
             for (int i = 0; i < kSteps; i++) {
                 const int r = r0 + i * kRows;
-                if (r < n) Load8<T>::run(x + (t0 + r) * ld + d0, val[i]);
-                else
-#pragma unroll
-                    for (int j = 0; j < 8; j++) val[i][j] = 0.0f;
+                if (r < n) val[i].load(x + (t0 + r) * ld + d0);
+                else val[i].zero();
             }
 #pragma unroll
-            for (int i = 0; i < kSteps; i++)
-#pragma unroll
-                for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(val[i][j]));
+            for (int i = 0; i < kSteps; i++) m = fmaxf(m, val[i].amax());
             m = warp_max(m, 32);
             if (W > 1) {                          // the group's warps alone
                 if (lane == 0) red[warp] = m;
@@ -220,7 +264,9 @@ kv_append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t token
                 if (r < n) {
                     const int off = __ldg(slot_map + t0 + r) & (P - 1);
                     uint2 o;
-                    e4m3_codes8(val[i], d, o.x, o.y);
+                    float y[8];
+                    val[i].widen(y);
+                    e4m3_codes8(y, d, o.x, o.y);
                     *reinterpret_cast<uint2*>(base + off * D + d0) = o;
                 }
             }
