@@ -47,7 +47,8 @@ __device__ unsigned int g_attn_decode_err;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 32;                         // keys of a unit
 constexpr int kStages = 3;
-constexpr int kItemCost = 12;                     // units that an item's q, joining and output take (2 us against 1.4 for 8 units)
+constexpr int kItemCost = 18;                     // units that an item's q, joining and output take (6: 98 us for 64 x <= 8192 keys,
+                                                  // 12: 91.4, 24: 89.9)
 constexpr float kPShift = 8.0f, kGrow = 6.0f;      // p = 2^(t - m + 8); growth of the maximum that m lets pass
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -143,7 +144,8 @@ struct DecodeLayout {
     static constexpr int HALF = kKeys * D;                          // bytes of K (or V) of a unit
     static constexpr int STAGE = 2 * HALF;
     static constexpr int RING = kWarps * kStages * STAGE;
-    static constexpr int JOIN_F = (kWarps / 2) * R * D;             // floats (and R rows of D + 4 fit)
+    static constexpr int JOIN_W = R == 8 ? kWarps : kWarps / 2;     // states that join at once
+    static constexpr int JOIN_F = JOIN_W * R * D;                   // floats
     static constexpr int META = RING + JOIN_F * 4;
     static constexpr int SMEM = META + 1408 + 1024;                 // barriers, states; alignment
     static constexpr int PART = R * D + 2 * R;                      // floats of a partial state
@@ -584,20 +586,13 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                 }
             }
         __syncthreads();
-        float mt[NR][2], lt[NR][2];
 #pragma unroll
         for (int n = 0; n < NR; n++)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const int row = n * 8 + 2 * t + e;
-                float x = -INFINITY, y = 0.0f;
+                float x = -INFINITY;
                 for (int w = 0; w < kWarps; w++) x = fmaxf(x, s_m[w * 16 + row]);
-                for (int w = 0; w < kWarps; w++) {
-                    const float mw = s_m[w * 16 + row], lw = s_l[w * 16 + row];
-                    y += mw == -INFINITY && lw == 0.0f ? 0.0f : lw * ex2(mw - x);
-                }
-                mt[n][e] = x;
-                lt[n][e] = y;
                 const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - x);
 #pragma unroll
                 for (int j = 0; j < MT; j++) {
@@ -605,92 +600,96 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                     o[j][n][2 + e] *= f;
                 }
             }
-#pragma unroll 1
-        for (int half = kWarps / 2; half > 0; half >>= 1) {
-            // a thread's values one float4 apart from its neighbours': no bank conflicts
-            if (warp >= half && warp < 2 * half) {
-                float4* dst = reinterpret_cast<float4*>(join + (warp - half) * R * D) + lane;
-#pragma unroll
-                for (int j = 0; j < MT; j++)
-#pragma unroll
-                    for (int n = 0; n < NR; n++)
-                        dst[(j * NR + n) * 32] = make_float4(o[j][n][0], o[j][n][1], o[j][n][2], o[j][n][3]);
-            }
-            __syncthreads();
-            if (warp < half) {
-                const float4* src = reinterpret_cast<const float4*>(join + warp * R * D) + lane;
-#pragma unroll
-                for (int j = 0; j < MT; j++)
-#pragma unroll
-                    for (int n = 0; n < NR; n++) {
-                        const float4 x = src[(j * NR + n) * 32];
-                        o[j][n][0] += x.x;
-                        o[j][n][1] += x.y;
-                        o[j][n][2] += x.z;
-                        o[j][n][3] += x.w;
-                    }
-            }
-            __syncthreads();
-        }
-        if (warp == 0) {
-            const bool begins = sub == 0, ends = sub + here == cur.r.subs;
-            // rows back to rows: [row][channel] in shared memory (4 floats of padding), then 16 bytes a lane
-            constexpr int LD = D + 4;
+        // A state as [row][channel], bits 3 and 4 of the channel turned by the row's (every lane of a store
+        // in a bank of its own). The upper warps' states first where not all fit at once.
+        auto at = [&](int row, int ch) { return row * D + (ch ^ ((row >> 1 & 3) * 8)); };
+        auto put = [&](float* to) {
 #pragma unroll
             for (int n = 0; n < NR; n++)
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int row = n * 8 + 2 * t + e;
+                for (int e = 0; e < 2; e++)
 #pragma unroll
                     for (int j = 0; j < MT; j++) {
-                        join[row * LD + j * 16 + g] = o[j][n][e];
-                        join[row * LD + j * 16 + 8 + g] = o[j][n][2 + e];
+                        to[at(n * 8 + 2 * t + e, j * 16 + g)] = o[j][n][e];
+                        to[at(n * 8 + 2 * t + e, j * 16 + 8 + g)] = o[j][n][2 + e];
                     }
-                    if (g == 0) {
-                        s_m[row] = mt[n][e];      // (every warp has read these)
-                        s_l[row] = lt[n][e];
-                    }
-                }
-            __syncwarp();
-            float* dst = P.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * Lay::PART;
+        };
+        constexpr int JW = Lay::JOIN_W;
+        if (JW < kWarps) {
+            if (warp >= JW) put(join + (warp - JW) * R * D);
+            __syncthreads();
+            if (warp < JW) {
+                float* own = join + warp * R * D;
 #pragma unroll
-            for (int c = lane; c < R * D / 4; c += 32) {
-                const int row = c / (D / 4), d0 = c % (D / 4) * 4;
-                const float4 x = *reinterpret_cast<const float4*>(join + row * LD + d0);
-                const float mr = s_m[row], lr = s_l[row];
-                if (!(begins && ends)) {
-                    *reinterpret_cast<float4*>(dst + row * D + d0) = x;
-                    if (d0 == 0) {
-                        dst[R * D + row] = mr;
-                        dst[R * D + R + row] = lr;
-                    }
-                    continue;
-                }
-                const int i = (cur.tile * R + row) / G, a = cur.tile * R + row - i * G;
-                if (i < cur.r.n) {
-                    const float inv = lr > 0.0f ? 1.0f / lr : (lr == lr ? 0.0f : lr);
-                    const int64_t token = cur.r.q0 + i;
-                    const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), y1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-                    *reinterpret_cast<uint2*>(P.a.out + token * P.a.ldo + (int64_t)(cur.h * G + a) * D + d0) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
-                    if (P.a.lse && d0 == 0)
-                        P.a.lse[token * P.a.heads_q + cur.h * G + a] =
-                            lr > 0.0f ? (mr - kPShift + __log2f(lr)) * kLn2 : (lr == lr ? -INFINITY : lr);
-                }
+                for (int n = 0; n < NR; n++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int j = 0; j < MT; j++) {
+                            o[j][n][e] += own[at(n * 8 + 2 * t + e, j * 16 + g)];
+                            o[j][n][2 + e] += own[at(n * 8 + 2 * t + e, j * 16 + 8 + g)];
+                        }
+                put(own);                         // the places that this thread has read
             }
-            if (!(begins && ends) && lane == 0) {
-                if (begins) {                     // the joining launch starts here
-                    header[2] = 0;
-                    header[3] = cur.r.q0;
-                    header[4] = cur.r.n;
-                    header[5] = cur.tile * R;
-                    header[6] = cur.h;
-                } else {
-                    header[0] = 0;
-                    header[1] = !ends;            // goes on in the next CTA
+        } else {
+            put(join + warp * R * D);
+        }
+        __syncthreads();
+        const bool begins = sub == 0, ends = sub + here == cur.r.subs;
+        float* dst = P.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * Lay::PART;
+#pragma unroll
+        for (int c = threadIdx.x; c < R * D / 4; c += kThreads) {     // four channels of a row per thread
+            const int row = c / (D / 4), d0 = c % (D / 4) * 4;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float mr = -INFINITY, lr = 0.0f;
+#pragma unroll
+            for (int w = 0; w < JW; w++) {
+                const float4 y = *reinterpret_cast<const float4*>(join + w * R * D + at(row, d0));
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+            }
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) mr = fmaxf(mr, s_m[w * 16 + row]);
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float mw = s_m[w * 16 + row], lw = s_l[w * 16 + row];
+                lr += mw == -INFINITY && lw == 0.0f ? 0.0f : lw * ex2(mw - mr);
+            }
+            if (!(begins && ends)) {
+                *reinterpret_cast<float4*>(dst + row * D + d0) = x;
+                if (d0 == 0) {
+                    dst[R * D + row] = mr;
+                    dst[R * D + R + row] = lr;
                 }
+                continue;
+            }
+            const int i = (cur.tile * R + row) / G, a = cur.tile * R + row - i * G;
+            if (i < cur.r.n) {
+                const float inv = lr > 0.0f ? 1.0f / lr : (lr == lr ? 0.0f : lr);
+                const int64_t token = cur.r.q0 + i;
+                const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), y1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+                *reinterpret_cast<uint2*>(P.a.out + token * P.a.ldo + (int64_t)(cur.h * G + a) * D + d0) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+                if (P.a.lse && d0 == 0)
+                    P.a.lse[token * P.a.heads_q + cur.h * G + a] =
+                        lr > 0.0f ? (mr - kPShift + __log2f(lr)) * kLn2 : (lr == lr ? -INFINITY : lr);
             }
         }
+        if (!(begins && ends) && threadIdx.x == 0) {
+            if (begins) {                         // the joining launch starts here
+                header[2] = 0;
+                header[3] = cur.r.q0;
+                header[4] = cur.r.n;
+                header[5] = cur.tile * R;
+                header[6] = cur.h;
+            } else {
+                header[0] = 0;
+                header[1] = !ends;                // goes on in the next CTA
+            }
+        }
+        __syncthreads();                          // the states, s_m and s_l have been read
         unit += here;
         cur = nxt;
     }
