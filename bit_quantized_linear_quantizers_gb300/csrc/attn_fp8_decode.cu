@@ -47,6 +47,7 @@ __device__ unsigned int g_attn_decode_err;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 32;                         // keys of a unit
 constexpr int kStages = 3;
+constexpr int kWholeKeys = 1024;                  // keys up to which few items take a CTA each
 constexpr int kItemCost = 18;                     // units that an item's q, joining and output take (6: 98 us for 64 x <= 8192 keys,
                                                   // 12: 91.4, 24: 89.9)
 constexpr float kPShift = 8.0f, kGrow = 6.0f;      // p = 2^(t - m + 8); growth of the maximum that m lets pass
@@ -86,6 +87,7 @@ struct DecodeParams {
     AttnArgs a;
     int shift;                                    // log2 page_size
     int max_rows;                                 // requests with more rows per KV head are not taken
+    int whole;                                    // one item per CTA (row tiles per request and head), no joining launch; 0: shares
     int beside;                                   // the launch before is the prefill kernel on other requests: wait at the end
     int* head;                                    // [CTAs][8]: what the CTA left for the joining launch: 0: the part of an
                                                   // item begun before (0 or -1), 1: it goes on, 2: an item that goes on
@@ -184,66 +186,76 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     if (!P.beside) pdl_wait();
     pdl_trigger();                                // the joining launch may come up; it waits for this one's end
 
-    // ---- the CTA's share: all units counted, then the request that holds its first one
-    auto units_of = [&](int b) -> int64_t {
-        if (b >= P.a.B) return 0;
-        const Req r = load_req<R>(P, b, G);
-        return (int64_t)P.a.kv.heads * r.tiles * (r.subs + kItemCost);
-    };
-    const int64_t mine0 = units_of(threadIdx.x);
-    int64_t sum = mine0;
-    for (int b = threadIdx.x + kThreads; b < P.a.B; b += kThreads) sum += units_of(b);
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kWarps; w++) total += s_sum[w];
-    const int64_t per = max((int64_t)(kWarps + kItemCost), (total + gridDim.x - 1) / gridDim.x);
-    const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
     int* header = P.head + blockIdx.x * 8;
-    if (threadIdx.x == 0) header[0] = header[2] = -1;
-    if (u0 >= u1) {
-        if (P.beside) pdl_wait();
-        return;
-    }
-    int64_t before = 0;
-    for (int b0 = 0; b0 < P.a.B; b0 += kThreads) {
-        int64_t v = b0 == 0 ? mine0 : units_of(b0 + threadIdx.x);
-        const int64_t own = v;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
-        }
-        __syncthreads();
-        if (lane == 31) s_sum[warp] = v;
-        __syncthreads();
-        int64_t all = 0, base = before;
-        for (int w = 0; w < kWarps; w++) {
-            if (w < warp) base += s_sum[w];
-            all += s_sum[w];
-        }
-        const int64_t first = base + v - own;
-        if (u0 >= first && u0 < first + own) {
-            s_start[0] = b0 + threadIdx.x;
-            *reinterpret_cast<int64_t*>(s_start + 2) = u0 - first;
-        }
-        before += all;
-        if (before > u0) break;                   // uniform
-    }
-    __syncthreads();
-
     Walk<R> cur;
-    cur.b = s_start[0];
-    cur.r = load_req<R>(P, cur.b, G);
-    cur.share = (int)(u1 - u0);                   // (a share of 2^31 units would be 2^36 keys)
-    {
-        const int64_t inside = *reinterpret_cast<int64_t*>(s_start + 2), len = cur.r.subs + kItemCost;
-        const int item0 = (int)(inside / len);
-        cur.h = item0 / cur.r.tiles;
-        cur.tile = item0 % cur.r.tiles;
-        cur.a = -(int)(inside % len);
+    if (P.whole) {
+        const int id = blockIdx.x / P.whole;
+        cur.tile = blockIdx.x % P.whole;
+        cur.h = id % P.a.kv.heads;
+        cur.b = id / P.a.kv.heads;
+        cur.r = load_req<R>(P, cur.b, G);
+        cur.a = 0;
+        cur.share = cur.tile < cur.r.tiles ? kItemCost + cur.r.subs : 0;
+    } else {
+        // ---- the CTA's share: all units counted, then the request that holds its first one
+        auto units_of = [&](int b) -> int64_t {
+            if (b >= P.a.B) return 0;
+            const Req r = load_req<R>(P, b, G);
+            return (int64_t)P.a.kv.heads * r.tiles * (r.subs + kItemCost);
+        };
+        const int64_t mine0 = units_of(threadIdx.x);
+        int64_t sum = mine0;
+        for (int b = threadIdx.x + kThreads; b < P.a.B; b += kThreads) sum += units_of(b);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        int64_t total = 0;
+        for (int w = 0; w < kWarps; w++) total += s_sum[w];
+        const int64_t per = max((int64_t)(kWarps + kItemCost), (total + gridDim.x - 1) / gridDim.x);
+        const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
+        if (threadIdx.x == 0) header[0] = header[2] = -1;
+        if (u0 >= u1) {
+            if (P.beside) pdl_wait();
+            return;
+        }
+        int64_t before = 0;
+        for (int b0 = 0; b0 < P.a.B; b0 += kThreads) {
+            int64_t v = b0 == 0 ? mine0 : units_of(b0 + threadIdx.x);
+            const int64_t own = v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = v;
+            __syncthreads();
+            int64_t all = 0, base = before;
+            for (int w = 0; w < kWarps; w++) {
+                if (w < warp) base += s_sum[w];
+                all += s_sum[w];
+            }
+            const int64_t first = base + v - own;
+            if (u0 >= first && u0 < first + own) {
+                s_start[0] = b0 + threadIdx.x;
+                *reinterpret_cast<int64_t*>(s_start + 2) = u0 - first;
+            }
+            before += all;
+            if (before > u0) break;                   // uniform
+        }
+        __syncthreads();
+
+        cur.b = s_start[0];
+        cur.r = load_req<R>(P, cur.b, G);
+        cur.share = (int)(u1 - u0);                   // (a share of 2^31 units would be 2^36 keys)
+        {
+            const int64_t inside = *reinterpret_cast<int64_t*>(s_start + 2), len = cur.r.subs + kItemCost;
+            const int item0 = (int)(inside / len);
+            cur.h = item0 / cur.r.tiles;
+            cur.tile = item0 % cur.r.tiles;
+            cur.a = -(int)(inside % len);
+        }
     }
-    if (!cur.mine()) cur.next_mine(P, G);
+    if (!P.whole && !cur.mine()) cur.next_mine(P, G);
 
     // q of an item: row g of each 8, channels t*16 .. of each 64-channel half, as it lies in memory
     uint4 raw[NR][D / 32];
@@ -746,13 +758,19 @@ attn_join_kernel(const __grid_constant__ DecodeParams P, int parts) {
 }
 
 template <int D, int R>
-qz_status launch_decode(DecodeParams& P, void* ws, cudaStream_t st) {
+qz_status launch_decode(DecodeParams& P, int64_t most_rows, void* ws, cudaStream_t st) {
     using Lay = DecodeLayout<D, R>;
-    const int ctas = num_sms();
+    // Few and short items (by the table's width): a CTA each, which spares the shares' reckoning and the joining
+    // launch (one request on 8 KV heads, whole against split: 517 keys 7.9 against 10.7 us, 2048 keys 14.6
+    // against 12.4).
+    const int64_t tiles = (most_rows + R - 1) / R, items = (int64_t)P.a.B * P.a.kv.heads * tiles;
+    P.whole = items <= num_sms() && (int64_t)P.a.max_blocks * P.a.kv.page_size <= kWholeKeys ? (int)tiles : 0;
+    const int ctas = P.whole ? (int)items : num_sms();
     P.head = reinterpret_cast<int*>(ws);
     P.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)ctas * 32 + 255) / 256 * 256);
     QZ_TRY(opt_in_smem((const void*)attn_decode_kernel<D, R>, Lay::SMEM));
     QZ_TRY(launch_pdl(attn_decode_kernel<D, R>, dim3(ctas), dim3(kThreads), Lay::SMEM, st, P));
+    if (P.whole) return QZ_OK;
     return launch_pdl(attn_join_kernel<D, R>, dim3(ctas), dim3(256), 0, st, P, ctas);
 }
 
@@ -780,8 +798,8 @@ qz_status attn_decode_launch(const AttnArgs& a, int max_rows, bool beside, void*
         return QZ_ERR_CUDA;
     const int64_t most = std::min<int64_t>((int64_t)a.max_q * (a.heads_q / a.kv.heads), max_rows);
     if (most <= 8)
-        return D == 64 ? launch_decode<64, 8>(P, ws, st) : launch_decode<128, 8>(P, ws, st);
-    return D == 64 ? launch_decode<64, 16>(P, ws, st) : launch_decode<128, 16>(P, ws, st);
+        return D == 64 ? launch_decode<64, 8>(P, most, ws, st) : launch_decode<128, 8>(P, most, ws, st);
+    return D == 64 ? launch_decode<64, 16>(P, most, ws, st) : launch_decode<128, 16>(P, most, ws, st);
 }
 
 qz_status attn_decode_error_read_and_clear() {
