@@ -40,7 +40,7 @@ namespace {
 
 __device__ unsigned int g_attn_prefill_err;
 
-constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 13 items, 14-15 MMA
+constexpr int kThreads = 512;                     // warps 0-7 softmax, 8-11 widen V, 12 TMA, 13 items, 14 MMA
 constexpr int kM = 128, kRows = 2 * kM, kN = 128; // rows of a tile, of a CTA; keys of a tile
 constexpr int kKStages = 3, kVStages = 2, kScStages = 4;
 constexpr int kSplitKeys = 512;
@@ -99,18 +99,25 @@ __device__ __forceinline__ uint32_t sdesc_v_lo(uint32_t saddr) {
 }
 constexpr uint32_t kDescVHi = 1024u >> 4 | 1u << 14 | 2u << 29;
 
+// The MMA warp issues them converged, through an elected lane: operands of a branch of one
+// lane are moved to the uniform registers anew for every MMA (8k keys x 4864 rows: 543 us so, 503 elected).
 __device__ __forceinline__ void mma_s(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
-    asm volatile("{ .reg .pred p; .reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+    asm volatile("{ .reg .pred p, q; .reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0; elect.sync _|q, 0xffffffff;\n\t"
                  "mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p; }"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p; }"
                  ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
 __device__ __forceinline__ void mma_o(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool acc) {
-    asm volatile("{ .reg .pred p; .reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+    asm volatile("{ .reg .pred p, q; .reg .b64 b;\n\tsetp.ne.b32 p, %5, 0; elect.sync _|q, 0xffffffff;\n\t"
                  "mov.b64 b, {%2, %3};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }"
                  ::"r"(d), "r"(a), "r"(b_lo), "r"(kDescVHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
+    asm volatile("{ .reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar) : "memory");
+}
+
 // (a, b) * s + c and (a, b) += (x, y) on the paired fp32 instructions.
 __device__ __forceinline__ void fma2(float a, float b, float s, float c, float& x, float& y) {
     asm("{ .reg .b64 v, m, k, r;\n\tmov.b64 v, {%2, %3}; mov.b64 m, {%4, %4}; mov.b64 k, {%5, %5};\n\t"
@@ -166,10 +173,9 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     auto bar = [&](int i) { return smem_u32(bars + i); };
     // barriers: K full/empty, raw V full/empty, widened V full/empty, scales full, S full, P full, O done, q, drain,
-    // turn, item full/empty, scheduler
+    // item full/empty, scheduler
     constexpr int KF = 0, KE = KF + kKStages, VF = KE + kKStages, VE = VF + kVStages, HF = VE + kVStages, HE = HF + 2,
-                  SC = HE + 2, SF = SC + kScStages, PF = SF + 2, OD = PF + 2, QF = OD + 2, DR = QF + 2, TN = DR + 2,
-                  IF = TN + 2, IE = IF + 2, CB = IE + 2, NBAR = CB + 1;
+                  SC = HE + 2, SF = SC + kScStages, PF = SF + 2, OD = PF + 2, QF = OD + 2, DR = QF + 2, IF = DR + 1, IE = IF + 2, CB = IE + 2, NBAR = CB + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
     uint8_t* canceled = smem + L::BAR_OFF + 384;                    // 16 bytes
     Item* items = reinterpret_cast<Item*>(smem + L::BAR_OFF + 400); // two: a role's current one stays here, not in registers
@@ -179,24 +185,23 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = P.a.heads_q / P.a.kv.heads;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kKStages; s++) { mbar_init(bar(KF + s), 1); mbar_init(bar(KE + s), 2); }
+        for (int s = 0; s < kKStages; s++) { mbar_init(bar(KF + s), 1); mbar_init(bar(KE + s), 1); }
         for (int s = 0; s < kVStages; s++) { mbar_init(bar(VF + s), 1); mbar_init(bar(VE + s), 4); }
         for (int s = 0; s < 2; s++) {
             mbar_init(bar(HF + s), 4);
-            mbar_init(bar(HE + s), 2);
+            mbar_init(bar(HE + s), 1);
             mbar_init(bar(SF + s), 1);
             mbar_init(bar(PF + s), 4);
             mbar_init(bar(OD + s), 1);
             mbar_init(bar(QF + s), 4);
-            mbar_init(bar(DR + s), 1);
-            mbar_init(bar(TN + s), 1);
         }
         for (int s = 0; s < kScStages; s++) mbar_init(bar(SC + s), 1);
         for (int s = 0; s < 2; s++) {
             mbar_init(bar(IF + s), 1);
-            mbar_init(bar(IE + s), 15);           // 8 softmax, 4 widening, 1 TMA and 2 MMA warps
+            mbar_init(bar(IE + s), 14);           // 8 softmax, 4 widening, the TMA and the MMA warp
         }
         mbar_init(bar(CB), 1);
+        mbar_init(bar(DR), 1);
         fence_barrier_init();
         prefetch_tmap(&P.tm_k);
         prefetch_tmap(&P.tm_v);
@@ -670,73 +675,79 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                 asked++;
                 id = canceled_cta(smem_u32(canceled));
             }
-        } else {
-            // ----------------------------- MMA of row tile w: one warp each
-            const int w = warp - 14;
-            const uint32_t sd = tmem + L::S_COL + w * kN, od = tmem + L::O_COL + w * D;
-            const uint32_t qa = sdesc_k_lo<D>(sbase + L::Q_OFF + w * 2 * L::Q), k_lo = sdesc_k_lo<D>(sbase + L::K_OFF),
+        } else if (warp == 14) {
+            // -------------------------------------------------------- MMA
+            const uint32_t s0 = tmem + L::S_COL, o0 = tmem + L::O_COL;
+            const uint32_t q_lo = sdesc_k_lo<D>(sbase + L::Q_OFF), k_lo = sdesc_k_lo<D>(sbase + L::K_OFF),
                            v_lo = sdesc_v_lo(sbase + L::VH_OFF);
             bool ok = true;
-            int kt = 0, ks = 0, tw = 0, batch = 0;                    // key tiles; K stage; own key tiles; MMA batches
-            uint32_t kph = 0, qph = 0;
+            int kt = 0, ks = 0;                   // key tiles; K stage
+            uint32_t kph = 0, qph0 = 0, qph1 = 0, pph0 = 0, pph1 = 0;
             for (int k = 0; ok && has_item(k); k++) {
-                const int nkv = max(items[k & 1].nk[0], items[k & 1].nk[1]), nkw = items[k & 1].nk[w];
-                if (lane == 0 && nkv > 0) {
+                const int nk0 = items[k & 1].nk[0], nk1 = items[k & 1].nk[1], nkv = max(nk0, nk1);
+                if (nkv > 0) {                    // the whole warp; one lane's MMAs and commits
+                    // A wait that gives up leaves the warp together and the MMAs to run on what is there, until
+                    // the tile's vote: the election needs every lane.
                     auto wait = [&](int i, uint32_t parity) { ok = ok && warp_wait(bar(i), parity); };
-                    auto turn = [&]() {           // w = 0: after the partner's batch before, w = 1: after its batch
-                        wait(TN + w, (batch & 1) ^ 1 ^ w);
-                        batch++;
-                    };
-                    auto score = [&](uint32_t ka) {                   // S, both parts of q
+                    auto score = [&](const int w, uint32_t ka) {      // S of row tile w, both parts of q
+                        const uint32_t sd = s0 + w * kN, qa = q_lo + w * (2 * L::Q >> 4);
 #pragma unroll
                         for (int j = 0; j < D / 32; j++) mma_s(sd, qa + j * 2, ka + j * 2, sdesc_k_hi<D>(), L::IDESC_S, j > 0);
 #pragma unroll
                         for (int j = 0; j < D / 32; j++) mma_s(sd, qa + (L::Q >> 4) + j * 2, ka + j * 2, sdesc_k_hi<D>(), L::IDESC_S, true);
-                        tc_commit(bar(SF + w));
+                        commit_elect(bar(SF + w));
                     };
-                    // A row tile that sees fewer key tiles than its partner still releases every stage, and
-                    // only after it was filled: an arrival ahead of its phase would count for an earlier one.
+                    auto value = [&](const int w, uint32_t va, bool acc) {          // O += P V
+                        const uint32_t sd = s0 + w * kN, od = o0 + w * D;
+                        mma_o(od, sd, va, L::IDESC_O, acc);
+#pragma unroll
+                        for (int j = 1; j < kN / 16; j++) mma_o(od, sd + j * 8, va + j * (2048 >> 4), L::IDESC_O, true);
+                    };
                     wait(KF + ks, kph);
-                    if (nkw > 0) wait(QF + w, qph);
-                    turn();
-                    if (ok) {
+                    if (nk0 > 0) {
+                        wait(QF, qph0);
+                        qph0 ^= 1;
                         tc_fence_after();
-                        if (nkw > 0) score(k_lo + ks * (L::KT >> 4));
-                        mbar_arrive(bar(TN + 1 - w));
-                        tc_commit(bar(KE + ks));
+                        score(0, k_lo + ks * (L::KT >> 4));
                     }
+                    if (nk1 > 0) {
+                        wait(QF + 1, qph1);
+                        qph1 ^= 1;
+                        tc_fence_after();
+                        score(1, k_lo + ks * (L::KT >> 4));
+                    }
+                    commit_elect(bar(KE + ks));
+                    ok = __all_sync(0xffffffffu, ok);
                     for (int t = 0; t < nkv && ok; t++, kt++) {
                         if (++ks == kKStages) { ks = 0; kph ^= 1; }
                         wait(HF + (kt & 1), (kt >> 1) & 1);
                         if (t + 1 < nkv) wait(KF + ks, kph);
-                        turn();
-                        if (t < nkw) {
-                            wait(PF + w, tw & 1);
-                            tw++;
-                            if (!ok) break;
+                        const uint32_t ka = k_lo + ks * (L::KT >> 4), va = v_lo + (kt & 1) * (L::VH >> 4);
+                        if (t < nk0) {
+                            wait(PF, pph0);
+                            pph0 ^= 1;
                             tc_fence_after();
-                            const uint32_t va = v_lo + (kt & 1) * (L::VH >> 4);
-                            mma_o(od, sd, va, L::IDESC_O, t > 0);                    // O += P V
-#pragma unroll
-                            for (int j = 1; j < kN / 16; j++) mma_o(od, sd + j * 8, va + j * (2048 >> 4), L::IDESC_O, true);
-                            if (t + 1 < nkw) score(k_lo + ks * (L::KT >> 4));
-                            else tc_commit(bar(OD + w));
+                            value(0, va, t > 0);
+                            if (t + 1 < nk0) score(0, ka);
+                            else commit_elect(bar(OD));
                         }
-                        if (!ok) break;
-                        mbar_arrive(bar(TN + 1 - w));
-                        tc_commit(bar(HE + (kt & 1)));
-                        if (t + 1 < nkv) tc_commit(bar(KE + ks));
+                        if (t < nk1) {
+                            wait(PF + 1, pph1);
+                            pph1 ^= 1;
+                            tc_fence_after();
+                            value(1, va, t > 0);
+                            if (t + 1 < nk1) score(1, ka);
+                            else commit_elect(bar(OD + 1));
+                        }
+                        commit_elect(bar(HE + (kt & 1)));
+                        if (t + 1 < nkv) commit_elect(bar(KE + ks));
+                        ok = __all_sync(0xffffffffu, ok);
                     }
-                    qph ^= nkw > 0;
                 }
-                ok = __all_sync(0xffffffffu, ok);
                 done_item(k);
             }
-            if (lane == 0) {
-                tc_commit(bar(DR + w));           // no MMA outlives the CTA's tensor memory
-                warp_wait(bar(DR + w), 0);
-            }
-            __syncwarp();
+            commit_elect(bar(DR));                // no MMA outlives the CTA's tensor memory
+            warp_wait(bar(DR), 0);
         }
     }
     tc_fence_before();
