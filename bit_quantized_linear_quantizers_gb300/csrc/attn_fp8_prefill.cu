@@ -232,10 +232,50 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t s_addr = lane_base + L::S_COL + w * kN, o_addr = lane_base + L::O_COL + w * D;
         const int r = q * 32 + lane;              // row of the tile
-        auto q_row = [&](const Item& x, int i) {  // this thread's row of q: token i
-            return P.a.q + (int64_t)(x.q0 + i) * P.a.ldq + (int64_t)(x.h * G + x.row0 + w * kM + r - i * G) * D;
+        // The thread's row of an item's q as two E4M3 parts in shared memory, in the swizzled order of the
+        // K-major operand; returns the factor of its scores. The row tile's last S before has completed.
+        auto put_q = [&](const Item& x) {
+            if (x.nk[w] == 0) return 0.0f;
+            const int row = x.row0 + w * kM + r, i = row / G;
+            const uint16_t* src = P.a.q + (int64_t)(x.q0 + i) * P.a.ldq + (int64_t)(x.h * G + row - i * G) * D;
+            uint4 raw[D / 8];
+            float m = 0.0f;
+#pragma unroll
+            for (int c = 0; c < D / 8; c++)
+                raw[c] = i < x.n ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < D / 8; c++) {
+                const uint32_t y[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(y[e] << 16)), fabsf(__uint_as_float(y[e] & 0xFFFF0000u))));
+            }
+            float up, down;
+            row_scale(m, up, down);
+            const float factor = fabsf(P.a.sm_scale) * kLog2e * down;
+            if (P.a.sm_scale < 0.0f) up = -up;
+            uint8_t* hi = smem + L::Q_OFF + (w * 2) * L::Q + r * D;
+#pragma unroll
+            for (int c = 0; c < D / 16; c++) {    // 16 channels
+                uint32_t hw[4], lw[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const uint4 y = raw[2 * c + (e >> 1)];
+                    const uint32_t y0 = e & 1 ? y.z : y.x, y1 = e & 1 ? y.w : y.y;
+                    split4(__uint_as_float(y0 << 16) * up, __uint_as_float(y0 & 0xFFFF0000u) * up,
+                           __uint_as_float(y1 << 16) * up, __uint_as_float(y1 & 0xFFFF0000u) * up, hw[e], lw[e]);
+                }
+                const int ch = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+                *reinterpret_cast<uint4*>(hi + ch * 16) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                *reinterpret_cast<uint4*>(hi + L::Q + ch * 16) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(QF + w));
+            return factor;
         };
         bool more = has_item(0);
+        float next_crow = more ? put_q(items[0]) : 0.0f;
         uint32_t od = 0;                          // phase of the row tile's O
         int tw = 0;                               // key tiles that this row tile has taken, over all items
         int tc = 0;                               // key tiles of the CTA before this item
@@ -245,46 +285,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             const int nk = it.nk[w];
             const int i = (it.row0 + w * kM + r) / G;
             const bool there = i < it.n;
-            float crow = 0.0f;
-            if (nk > 0) {
-                uint4 raw[D / 8];                 // this thread's row of q, zeros where there is none
-                const uint16_t* src = q_row(it, i);
-#pragma unroll
-                for (int c = 0; c < D / 8; c++)
-                    raw[c] = there ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-                // the row's two E4M3 parts into shared memory, in the swizzled order of the K-major operand
-                // (the last S of the item before is complete: this warp has waited for it)
-                float m = 0.0f;
-#pragma unroll
-                for (int c = 0; c < D / 8; c++) {
-                    const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-                }
-                float up, down;
-                row_scale(m, up, down);
-                crow = fabsf(P.a.sm_scale) * kLog2e * down;
-                if (P.a.sm_scale < 0.0f) up = -up;
-                uint8_t* hi = smem + L::Q_OFF + (w * 2) * L::Q + r * D;
-#pragma unroll
-                for (int c = 0; c < D / 16; c++) {                    // 16 channels
-                    uint32_t hw[4], lw[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const uint4 x = raw[2 * c + (e >> 1)];
-                        const uint32_t y0 = e & 1 ? x.z : x.x, y1 = e & 1 ? x.w : x.y;
-                        split4(__uint_as_float(y0 << 16) * up, __uint_as_float(y0 & 0xFFFF0000u) * up,
-                               __uint_as_float(y1 << 16) * up, __uint_as_float(y1 & 0xFFFF0000u) * up, hw[e], lw[e]);
-                    }
-                    const int ch = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-                    *reinterpret_cast<uint4*>(hi + ch * 16) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                    *reinterpret_cast<uint4*>(hi + L::Q + ch * 16) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(QF + w));
-            }
+            const float crow = next_crow;
             // keys that the row sees, counted from the item's first key tile
             const int seen = (!there ? 0 : P.a.causal ? min(max(it.L - it.n + i + 1, 0), it.L) : it.L) - it.t0 * kN;
             // the fewest that a row of this warp sees (rows past the end see none, and are not stored)
@@ -303,11 +304,25 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                 // grown past f16's range (or no m is known yet) is the tile's maximum taken, m raised,
                 // O scaled and the pass made again. P stays in registers until all of S is read and
                 // found in range, since it takes S's columns.
+                if (edge) {                       // -inf where a row does not see a key: its score is -inf, its p 0
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {
+                        uint32_t x[32];
+                        tmem_ld32(s_addr + c * 32, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            if (e >= lim - c * 32) x[e] = 0xFF800000u;
+                        tmem_st32(s_addr + c * 32, x);
+                    }
+                    tmem_wait_st();
+                }
                 uint32_t pk[64];
                 float sum;
-                bool raise = m == -INFINITY && lim > 0;
+                bool raise = m == -INFINITY && lim > 0, raised = false;
                 while (true) {
                     if (__any_sync(0xffffffffu, raise)) {
+                        raised = true;
                         float mx = -INFINITY;
 #pragma unroll 1
                         for (int c = 0; c < 4; c++) {
@@ -319,7 +334,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                             for (int e = 0; e < 32; e++) {
                                 const float4& cn = e < 16 ? c0 : c1;
                                 const float v = fmaf(__uint_as_float(x[e]), fmaxf(crow * cn.x, kTiny), cn.y);
-                                if (c * 32 + e < lim) mx = fmaxf(mx, v);
+                                mx = fmaxf(mx, v);
                             }
                         }
                         const float m2 = raise ? fmaxf(m, mx) : m;
@@ -348,11 +363,6 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                         uint32_t* x = s[c & 1];
                         tmem_wait_ld();
                         if (c < 3) tmem_ld32(s_addr + (c + 1) * 32, s[(c + 1) & 1]);    // in flight during this chunk
-                        if (edge) {
-#pragma unroll
-                            for (int e = 0; e < 32; e++)
-                                if (c * 32 + e >= lim) x[e] = 0xFF800000u;              // -inf: its score is -inf, its p 0
-                        }
 #pragma unroll
                         for (int gr = 0; gr < 2; gr++) {
                             const float4 cn = con[c * 2 + gr];
@@ -373,9 +383,10 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                             sum = fmaf(both, cn.z, sum);
                         }
                     }
-                    // a p of the next pass is at most 2^8: no third one
+                    // Under the tile's own maximum a p is at most 2^8. (Scores so large that their rounding alone
+                    // exceeds that would come back for ever: m is raised once for a tile.)
                     raise = top > kMost && there;
-                    if (!__any_sync(0xffffffffu, raise)) break;
+                    if (raised || !__any_sync(0xffffffffu, raise)) break;
                 }
                 l += sum;
                 tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
@@ -386,18 +397,10 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                 if (lane == 0) mbar_arrive(bar(PF + w));
             }
             if (!ok) break;
-            // ---- the next item's q is on its way to the caches while this one's output leaves
+            // ---- the next item's q first: its S runs while this item's output leaves
             tc += max(it.nk[0], it.nk[1]);
             more = has_item(k + 1);
-            if (more) {
-                const Item& next = items[(k + 1) & 1];
-                const int i2 = (next.row0 + w * kM + r) / G;
-                if (i2 < next.n) {
-                    const uint16_t* src = q_row(next, i2);
-#pragma unroll
-                    for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(src + c));
-                }
-            }
+            if (more) next_crow = put_q(items[(k + 1) & 1]);
             if (nk > 0 && !warp_wait(bar(OD + w), od)) break;
             od ^= nk > 0;
             const int a = it.row0 + w * kM + r - i * G;
