@@ -385,6 +385,27 @@ def test_nan_in_one_request_stays_there():
         assert bool((got[keep] == want[keep]).all())
 
 
+@pytest.mark.parametrize("q_std", [1e6, 1e12, 1e25, 1e36])
+def test_logits_past_the_resolution_of_fp32_stay_in_their_rows(q_std):
+    """Where the rounding of a score is itself large, its row has no defined answer; the call ends and the others keep theirs."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    P, D, H = 16, 64, 1
+    kc, ks = quantized_pages(48, H, P, D, g)
+    vc, vs = quantized_pages(48, H, P, D, g)
+    cache = qz.PagedKV(kc, vc, ks, vs)
+    table, kv = torch.arange(48, dtype=torch.int32, device="cuda").view(3, 16), i32([256, 240, 250])
+    for n in (1, 200):
+        q = torch.randn((3 * n, 2, D), generator=g, device="cuda").to(torch.bfloat16)
+        args = (cache, table, kv, i32([0, n, 2 * n, 3 * n]), n, 100.0)
+        want, _ = qz.qz_attn_fp8_paged(q, *args)
+        q[n:2 * n, 1] *= q_std
+        got, _ = qz.qz_attn_fp8_paged(q, *args)
+        keep = torch.ones_like(got, dtype=torch.bool)
+        keep[n:2 * n, 1] = False
+        assert bool((got[keep] == want[keep]).all())
+    assert qz.qz_device_error() == 0
+
+
 def test_another_stream_and_reused_workspace():
     """Calls chained on a stream of their own give the same bits as alone, small and large in turn."""
     g = torch.Generator(device="cuda").manual_seed(0)
