@@ -128,6 +128,7 @@ block_tables_kernel(const int32_t* __restrict__ ctx_lens, const int32_t* __restr
 
 constexpr int kAppendThreads = 256;
 constexpr int kStrip = 16;                        // tokens that one warp holds in registers
+template <typename T> constexpr int kAppendCtas = sizeof(T) == 2 ? 4 : 3;        // CTAs that an SM holds
 
 __device__ __forceinline__ void e4m3_codes8(const float v[8], const Recip& d, uint32_t& lo, uint32_t& hi) {
     float y[8];
@@ -196,7 +197,7 @@ template <> struct Raw8<float> {
 // goes through shared memory. Bound by HBM for prompts and by latency for
 // single tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas<T>)
 kv_append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t tokens, int64_t ldk, int64_t ldv,
                  const int32_t* __restrict__ slot_map, qz_paged_kv c, int shift, int window) {
     constexpr int kWarps = kAppendThreads / 32;
@@ -293,8 +294,10 @@ qz_status append_launch(const T* k, const T* v, int64_t tokens, int64_t ldk, int
                         const qz_paged_kv& c, cudaStream_t st) {
     const int P = c.page_size, groups = kAppendThreads / 32 / (P / kStrip);
     // Window of a group: one token while that gives every group work at once
-    // (single tokens, each its own page), up to a page when there are many.
-    const int64_t units = tokens * c.heads * 2, room = (int64_t)num_sms() * 8 * groups;
+    // (single tokens, each its own page), up to a page when there are many. (1200 fp32 tokens of 4 heads
+    // of 64: 4.2 us so, 6.0 with windows of one token, which are mostly empty; 64 single tokens of 8 heads of 128: 5.4 us,
+    // 7.8 with windows that leave half the groups without one.)
+    const int64_t units = tokens * c.heads * 2, room = (int64_t)num_sms() * kAppendCtas<T> * groups;
     const int window = (int)std::min<int64_t>(P, std::max<int64_t>(1, units / room));
     const int64_t gx = (tokens + (int64_t)window * groups - 1) / ((int64_t)window * groups);
     if (gx > 0x7fffffff || c.heads > 32767) return QZ_ERR_SHAPE;
