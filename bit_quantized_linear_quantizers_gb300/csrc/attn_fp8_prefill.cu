@@ -348,6 +348,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                     while (true) {
                         if (__any_sync(0xffffffffu, raise)) {
                             raised = true;
+                            tmem_wait_st();       // P of keys 0-63 and a scaled O may still be on their way, and are read below
                             float mx = -INFINITY;
 #pragma unroll 1
                             for (int c = 4 * half; c < 8; c++) {

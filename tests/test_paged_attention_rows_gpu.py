@@ -52,3 +52,33 @@ def test_many_items(D, Hkv, G, P, causal):
         again, lse2 = qz.qz_attn_fp8_paged(*args, causal=causal, lse=True)
         assert torch.equal(out, again) and torch.equal(lse, lse2)
     assert qz.qz_device_error() == 0
+
+
+def rising(L, step, D, H, P, g):
+    """Keys whose products with the returned direction grow by `step` doublings (of 2^x) every 64 keys, and a little from key to key."""
+    u = torch.where(torch.rand(D, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    pages = -(-L // P)
+    j = torch.arange(pages * P, device="cuda")
+    a = (step * math.log(2.0) * torch.floor(j / 64.0) + torch.rand(pages * P, generator=g, device="cuda")) / D
+    k = a[:, None] * u[None] + 0.01 * torch.randn((H, pages * P, D), generator=g, device="cuda")
+    v = torch.randn((pages, H, P, D), generator=g, device="cuda")
+    k = encode(k.reshape(H, pages, P, D).transpose(0, 1).contiguous())
+    return u, k, encode(v)
+
+
+@pytest.mark.parametrize("D, P, causal", [(128, 16, True), (64, 64, False), (128, 128, False)])
+@pytest.mark.parametrize("step", [2.5, 6.0, 11.0])
+def test_maxima_that_rise_in_every_half_of_a_tile(D, P, causal, step):
+    """The stored P and O of a tile are scaled again and again; rows of other sizes rise elsewhere."""
+    g = torch.Generator(device="cuda").manual_seed(int(step * 2) + D)
+    L, n, H, G = 1100, 300, 2, 3
+    u, (kc, ks), (vc, vs) = rising(L, step, D, H, P, g)
+    cache = qz.PagedKV(kc, vc, ks, vs)
+    r = 0.3 + torch.rand((n, H * G, 1), generator=g, device="cuda")
+    q = (r * u + 0.05 * torch.randn((n, H * G, D), generator=g, device="cuda")).to(torch.bfloat16)
+    table = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None]
+    out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32([L]), i32([0, n]), n, 1.0, causal=causal, lse=True)
+    check(out, lse, formula(q, cache, table, [L], [0, n], 1.0, causal))
+    few, lse = qz.qz_attn_fp8_paged(q[:7], cache, table, i32([L]), i32([0, 7]), 7, 1.0, causal=causal, lse=True)
+    check(few, lse, formula(q[:7], cache, table, [L], [0, 7], 1.0, causal))
+    assert qz.qz_device_error() == 0
