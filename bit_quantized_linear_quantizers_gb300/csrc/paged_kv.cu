@@ -283,6 +283,7 @@ kv_append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t token
                     reinterpret_cast<uint2*>(base)[i] = o;
                 }
             if (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");   // `was` and `red` read by all
+            else __syncwarp();
             if (wig == 0 && lane == 0) scales[si] = s;
         }
     }
