@@ -705,9 +705,11 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         unit += here;
         cur = nxt;
     }
-    // copies still in flight (a wait that gave up): their stages must not outlive the CTA
+    // copies still in flight (a wait that gave up): their stages must not outlive the CTA. The units counted as issued
+    // after it had no copies: a wait for each of them would run its whole limit.
     if (dead)
-        for (int k = dead_at; k < issued; k++) mbar_wait(bar0 + k % kStages * 8, (k / kStages) & 1, &g_attn_decode_err);
+        for (int k = dead_at; k < min(issued, dead_at + kStages); k++)
+            mbar_wait(bar0 + k % kStages * 8, (k / kStages) & 1, &g_attn_decode_err);
     if (P.beside) pdl_wait();
 }
 
