@@ -309,11 +309,13 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
             float m = -INFINITY, l = 0.0f;
             for (int t = 0; t < nk; t++, tw++) {
                 const int ts = tc + t;
-                // S first: a row tile without keys in an item skips the phases of that item's scales, so its wait could come
-                // two uses of a slot early, where the parity is the same. The K of this tile was copied after the scales
-                // of the slot's last use were stored, so behind its S the parity is unambiguous.
-                if (!warp_wait(bar(SF + w), tw & 1)) { ok = false; break; }
+                // A row tile without keys in an item skips the phases of that item's scales, so the wait of its next tile could
+                // come two uses of a slot early, where the parity is the same. An item's first tile waits for its S
+                // before: K was copied after the scales of the slot's last use were stored. From then on the S of the tile
+                // before says so.
+                if (t == 0 && !warp_wait(bar(SF + w), tw & 1)) { ok = false; break; }
                 if (!warp_wait(bar(SC + ts % kScStages), (ts / kScStages) & 1)) { ok = false; break; }
+                if (!warp_wait(bar(SF + w), tw & 1)) { ok = false; break; }
                 tc_fence_after();
                 const float4* con = sc + (ts % kScStages) * 8;        // (k scale, log2 v scale, 1 / v scale) per 16 keys
                 const int lim = seen - t * kN;
