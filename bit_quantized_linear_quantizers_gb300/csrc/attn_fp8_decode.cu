@@ -103,11 +103,11 @@ struct Req {
 template <int R>
 __device__ __forceinline__ Req load_req(const DecodeParams& P, int b, int G) {
     Req r;
-    r.q0 = __ldg(P.a.cu_q + b);
-    r.n = min(__ldg(P.a.cu_q + b + 1) - r.q0, P.a.max_q);
+    r.q0 = P.a.cu_q[b];
+    r.n = min(P.a.cu_q[b + 1] - r.q0, P.a.max_q);
     r.n = (int)min((int64_t)r.n, P.a.tokens - r.q0);
     if (r.n < 0 || r.q0 < 0) r.n = 0;
-    r.L = (int)min((int64_t)max(__ldg(P.a.kv_lens + b), 0), (int64_t)P.a.max_blocks << P.shift);
+    r.L = (int)min((int64_t)max(P.a.kv_lens[b], 0), (int64_t)P.a.max_blocks << P.shift);
     const int64_t rows = (int64_t)r.n * G;
     r.tiles = rows > P.max_rows ? 0 : (int)((rows + R - 1) / R);
     r.subs = (r.L + kKeys - 1) / kKeys;
@@ -183,7 +183,10 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     // The prefill kernel lets this one start when its CTAs have waited for the stream's earlier work
     // themselves and begin to leave; the two share no memory that either writes. The wait for its end
     // comes last, so that whatever waits for this kernel waits for both.
-    if (!P.beside) pdl_wait();
+    // At the start a fence stands in for it: L1 may hold lines from before that earlier work, and the loads below
+    // are plain ones, not those of the read-only path, so that they stay behind it.
+    if (P.beside) __threadfence();
+    else pdl_wait();
     pdl_trigger();                                // the joining launch may come up; it waits for this one's end
 
     int* header = P.head + blockIdx.x * 8;
@@ -267,7 +270,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             const uint16_t* src = P.a.q + (int64_t)(it.r.q0 + i) * P.a.ldq + (int64_t)(it.h * G + a) * D + t * 16;
 #pragma unroll
             for (int j = 0; j < D / 32; j++)
-                raw[rr][j] = there ? __ldg(reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + (j & 1) * 8)) : make_uint4(0, 0, 0, 0);
+                raw[rr][j] = there ? *reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + (j & 1) * 8) : make_uint4(0, 0, 0, 0);
         }
     };
     load_q(cur);
@@ -289,8 +292,8 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             const int key = (w.lo() + u - base) * kKeys;
             k.y = (w.h << P.shift) + (key & ((1 << P.shift) - 1));
             const int32_t* row = P.a.block_table + (int64_t)w.b * P.a.ld_table + (key >> P.shift);
-            k.p0 = __ldg(row);
-            if (P.shift == 4 && key + 16 < w.r.L) k.p1 = __ldg(row + 1);
+            k.p0 = *row;
+            if (P.shift == 4 && key + 16 < w.r.L) k.p1 = row[1];
         }
         ahead_base = __shfl_sync(0xffffffffu, base, 31);              // (the last lane's item, or the end)
         ahead.b = __shfl_sync(0xffffffffu, w.b, 31);
@@ -311,13 +314,13 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         const int h = k.y >> P.shift;
         if (k.p0 >= 0) {
             const int64_t i = (int64_t)k.p0 * P.a.kv.heads + h;
-            k.k0 = __ldg(P.a.kv.k_scale + i);
-            k.v0 = __ldg(P.a.kv.v_scale + i);
+            k.k0 = P.a.kv.k_scale[i];
+            k.v0 = P.a.kv.v_scale[i];
         }
         if (P.shift == 4 && k.p1 >= 0) {
             const int64_t i = (int64_t)k.p1 * P.a.kv.heads + h;
-            k.k1 = __ldg(P.a.kv.k_scale + i);
-            k.v1 = __ldg(P.a.kv.v_scale + i);
+            k.k1 = P.a.kv.k_scale[i];
+            k.v1 = P.a.kv.v_scale[i];
         }
     };
     bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
