@@ -346,10 +346,11 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                 for (int half = 0; half < 2; half++) {
                     uint32_t pk[32];
                     float sum;
-                    bool raise = half == 0 && m == -INFINITY && lim > 0, raised = false;
+                    bool raise = half == 0 && m == -INFINITY && lim > 0;
+                    int raised = 0;
                     while (true) {
                         if (__any_sync(0xffffffffu, raise)) {
-                            raised = true;
+                            raised++;
                             tmem_wait_st();       // P of keys 0-63 and a scaled O may still be on their way, and are read below
                             float mx = -INFINITY;
 #pragma unroll 1
@@ -424,9 +425,10 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                             }
                         }
                         // Under a maximum taken here a p is at most 2^8. (Scores so large that their rounding alone
-                        // exceeds that would come back for ever: m is raised once for a half.)
+                        // exceeds that would come back for ever: m is raised twice for a half at most, once for rows without
+                        // an m, which rows of NaN are in every tile, and once for what has outgrown it.)
                         raise = top > kMost && there;
-                        if (raised || !__any_sync(0xffffffffu, raise)) break;
+                        if (raised == 2 || !__any_sync(0xffffffffu, raise)) break;
                     }
                     l += sum;
                     tmem_st32(s_addr + half * 32, pk);

@@ -82,3 +82,25 @@ def test_maxima_that_rise_in_every_half_of_a_tile(D, P, causal, step):
     few, lse = qz.qz_attn_fp8_paged(q[:7], cache, table, i32([L]), i32([0, 7]), 7, 1.0, causal=causal, lse=True)
     check(few, lse, formula(q[:7], cache, table, [L], [0, 7], 1.0, causal))
     assert qz.qz_device_error() == 0
+
+
+@pytest.mark.parametrize("D, P, causal", [(128, 16, True), (64, 64, False)])
+def test_a_nan_row_leaves_rows_that_rise_alone(D, P, causal):
+    """A row of NaN never finds a maximum; its neighbours in the warp raise theirs all the same."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    L, n, H, G = 900, 250, 1, 4
+    u, (kc, ks), (vc, vs) = rising(L, 10.0, D, H, P, g)
+    cache = qz.PagedKV(kc, vc, ks, vs)
+    q = (u + 0.05 * torch.randn((n, H * G, D), generator=g, device="cuda")).to(torch.bfloat16)
+    table = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None]
+    for rows in (n, 5):
+        args = (cache, table, i32([L]), i32([0, rows]), rows, 1.0)
+        want, want_lse = qz.qz_attn_fp8_paged(q[:rows], *args, causal=causal, lse=True)
+        check(want, want_lse, formula(q[:rows], cache, table, [L], [0, rows], 1.0, causal))
+        bad = q[:rows].clone()
+        bad[::7, 2, 5] = math.nan
+        got, lse = qz.qz_attn_fp8_paged(bad, *args, causal=causal, lse=True)
+        hit = torch.zeros((rows, H * G), dtype=torch.bool, device="cuda")
+        hit[::7, 2] = True
+        assert bool(got[hit].isnan().all()) and bool(lse[hit].isnan().all())
+        assert torch.equal(got[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
