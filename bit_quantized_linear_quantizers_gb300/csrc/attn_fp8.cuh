@@ -46,6 +46,10 @@ __device__ __forceinline__ void row_scale(float amax, float& up, float& down) {
     down = amax > 0.0f ? __uint_as_float((uint32_t)(254 - se) << 23) : 1.0f;
 }
 
+// Least value scale that enters the exponent and l = sum p / sv: p <= 2^15 and 2^31 keys leave l below 2^126. Pages
+// of this scale or less (0 among them) keep their share of l; their codes are taken as 0.
+constexpr float kLeastScale = 0x1p-80f;
+
 // 3-D TMA load of a box (channels, rows, page).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"

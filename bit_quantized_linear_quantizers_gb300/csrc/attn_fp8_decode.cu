@@ -276,7 +276,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
     load_q(cur);
 
     // ---- the warp's next 32 units, one per lane: pages, rows in them, scales
-    struct Batch { int p0, p1, y; float k0, v0, k1, v1; };            // y < 0: no unit; v < 0: no page
+    struct Batch { int p0, p1, y; float k0, v0, k1, v1; };            // y < 0: no unit; p < 0: no page
     Walk<R> ahead = cur;                          // at the item of the batch's first unit
     int ahead_base = 0, looked = warp;            // units of the share before that item; the batch's first unit
     auto look_up = [&]() {                        // leaves the walk at the next batch
@@ -287,7 +287,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             base += w.hi() - w.lo();
             w.next(P, G);
         }
-        Batch k = {-1, -1, -1, 0.0f, -1.0f, 0.0f, -1.0f};
+        Batch k = {-1, -1, -1, 0.0f, 1.0f, 0.0f, 1.0f};
         if (w.valid()) {
             const int key = (w.lo() + u - base) * kKeys;
             k.y = (w.h << P.shift) + (key & ((1 << P.shift) - 1));
@@ -315,12 +315,12 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         if (k.p0 >= 0) {
             const int64_t i = (int64_t)k.p0 * P.a.kv.heads + h;
             k.k0 = P.a.kv.k_scale[i];
-            k.v0 = P.a.kv.v_scale[i];
+            k.v0 = fmaxf(P.a.kv.v_scale[i], kLeastScale);
         }
         if (P.shift == 4 && k.p1 >= 0) {
             const int64_t i = (int64_t)k.p1 * P.a.kv.heads + h;
             k.k1 = P.a.kv.k_scale[i];
-            k.v1 = P.a.kv.v_scale[i];
+            k.v1 = fmaxf(P.a.kv.v_scale[i], kLeastScale);
         }
     };
     bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
@@ -363,7 +363,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
 #pragma unroll 1
     for (int s = 0; s < kStages; s++) issue(front);
     load_scales(front);
-    Batch back = front, next = {-1, -1, -1, 0.0f, -1.0f, 0.0f, -1.0f};
+    Batch back = front, next = {-1, -1, -1, 0.0f, 1.0f, 0.0f, 1.0f};
     int done = 0;                                 // units that this warp has computed
     int st = 0;                                   // stage of the warp's next unit, and its phase
     uint32_t phase = 0;
@@ -445,15 +445,14 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             const int key0 = (sub + (u - unit)) * kKeys;
             const int from = done & 31;
             if (from == 0) back = front;          // (the copies' batch turned over at most kStages units ago)
-            const float k0 = __shfl_sync(0xffffffffu, back.k0, from), r0 = __shfl_sync(0xffffffffu, back.v0, from);
-            float k1 = k0, r1 = r0;
+            const float k0 = __shfl_sync(0xffffffffu, back.k0, from), v0 = __shfl_sync(0xffffffffu, back.v0, from);
+            float k1 = k0, v1 = v0;
             bool p0 = __shfl_sync(0xffffffffu, back.p0, from) >= 0, p1 = p0;
             if (P.shift == 4) {
                 k1 = __shfl_sync(0xffffffffu, back.k1, from);
-                r1 = __shfl_sync(0xffffffffu, back.v1, from);
+                v1 = __shfl_sync(0xffffffffu, back.v1, from);
                 p1 = __shfl_sync(0xffffffffu, back.p1, from) >= 0;
             }
-            const float v0 = fmaxf(fabsf(r0), 1.2e-38f), v1 = fmaxf(fabsf(r1), 1.2e-38f);
             if (!dead && !mbar_wait<false>(bar0 + st * 8, phase, &g_attn_decode_err)) dead = true;
             if (__any_sync(0xffffffffu, dead) && dead_at < 0) dead = true, dead_at = done;
             uint8_t* kt = smem + (warp * kStages + st) * Lay::STAGE;
@@ -488,7 +487,8 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
             }
             const float lv[2] = {__log2f(v0), __log2f(v1)}, iv[2] = {__frcp_rn(v0), __frcp_rn(v1)};
             const int live = cur.r.L - key0;      // keys of the unit that exist
-            const bool edge = live < kKeys || !p0 || !p1 || (P.a.causal && key0 + kKeys > cur.r.L - cur.r.n + 1);
+            const bool nil0 = !p0 || v0 <= kLeastScale, nil1 = !p1 || v1 <= kLeastScale;     // no values
+            const bool edge = live < kKeys || nil0 || nil1 || (P.a.causal && key0 + kKeys > cur.r.L - cur.r.n + 1);
             bool raise = false;
 #pragma unroll
             for (int n = 0; n < NR; n++)
@@ -507,7 +507,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                 }
             if (edge) {
                 // rows of V that were never written may hold NaN codes, and 0 * NaN is no 0
-                if (lane >= live || !(lane < 16 ? p0 : p1))
+                if (lane >= live || (lane < 16 ? nil0 : nil1))
 #pragma unroll
                     for (int c = 0; c < D / 16; c++)
                         *reinterpret_cast<uint4*>(kt + Lay::HALF + lane * D + c * 16) = make_uint4(0, 0, 0, 0);

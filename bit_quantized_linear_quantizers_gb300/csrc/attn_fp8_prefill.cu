@@ -589,8 +589,9 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                         tma_load_3d(sbase + L::K_OFF + ks * L::KT + (lane << P.shift) * D, &P.tm_k, 0, h << P.shift, p, bar(KF + ks));
                     // scales per 16 keys (a page covers page_size / 16 of them)
                     const int reps = 1 << (P.shift - 4);
+                    const int pv = cn.z <= kLeastScale ? P.a.kv.num_pages : p;       // no values: zeros
                     if (p < P.a.kv.num_pages) {
-                        const float v = fmaxf(cn.z, 1.2e-38f);
+                        const float v = fmaxf(cn.z, kLeastScale);
                         cn.y = __log2f(v);
                         cn.z = __frcp_rn(v);
                     }
@@ -605,7 +606,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                     if (lane == 0) mbar_arrive_expect_tx(bar(VF + vs), L::KT);
                     __syncwarp();
                     if (lane < pages_tile)
-                        tma_load_3d(sbase + L::V_OFF + vs * L::KT + (lane << P.shift) * D, &P.tm_v, 0, h << P.shift, p, bar(VF + vs));
+                        tma_load_3d(sbase + L::V_OFF + vs * L::KT + (lane << P.shift) * D, &P.tm_v, 0, h << P.shift, pv, bar(VF + vs));
                     p = p1;
                     p1 = p2;
                     cn = cn1;

@@ -104,3 +104,24 @@ def test_a_nan_row_leaves_rows_that_rise_alone(D, P, causal):
         hit[::7, 2] = True
         assert bool(got[hit].isnan().all()) and bool(lse[hit].isnan().all())
         assert torch.equal(got[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, 2.0 ** -100, 2.0 ** -79])
+@pytest.mark.parametrize("where", ["first", "middle", "last", "alone"])
+@pytest.mark.parametrize("n, causal", [(1, True), (6, False), (200, True), (200, False)])
+def test_value_scales_down_to_zero(n, causal, where, scale):
+    """Pages of zeros as a quantizer without a floor leaves them, and codes under scales too small to matter: their
+    keys count in the denominator, their values as good as nothing."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    P, D, H, G, L = 32, 64, 2, 2, 470
+    kc, ks = encode(torch.randn((15, H, P, D), generator=g, device="cuda"))
+    vc, vs = encode(torch.randn((15, H, P, D), generator=g, device="cuda"))
+    pages = {"first": slice(0, 5), "middle": slice(6, 9), "last": slice(11, 15), "alone": slice(0, 15)}[where]
+    vs[pages, 0] = scale
+    if scale == 0:
+        vc[pages, 0] = 0
+    cache = qz.PagedKV(kc, vc, ks, vs)
+    q = torch.randn((n, H * G, D), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.arange(15, dtype=torch.int32, device="cuda")[None]
+    out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32([L]), i32([0, n]), n, 0.125, causal=causal, lse=True)
+    check(out, lse, formula(q, cache, table, [L], [0, n], 0.125, causal))
