@@ -315,12 +315,12 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         if (k.p0 >= 0) {
             const int64_t i = (int64_t)k.p0 * P.a.kv.heads + h;
             k.k0 = P.a.kv.k_scale[i];
-            k.v0 = fmaxf(P.a.kv.v_scale[i], kLeastScale);
+            k.v0 = value_scale(P.a.kv.v_scale[i]);
         }
         if (P.shift == 4 && k.p1 >= 0) {
             const int64_t i = (int64_t)k.p1 * P.a.kv.heads + h;
             k.k1 = P.a.kv.k_scale[i];
-            k.v1 = fmaxf(P.a.kv.v_scale[i], kLeastScale);
+            k.v1 = value_scale(P.a.kv.v_scale[i]);
         }
     };
     bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones

@@ -591,7 +591,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                     const int reps = 1 << (P.shift - 4);
                     const int pv = cn.z <= kLeastScale ? P.a.kv.num_pages : p;       // no values: zeros
                     if (p < P.a.kv.num_pages) {
-                        const float v = fmaxf(cn.z, kLeastScale);
+                        const float v = value_scale(cn.z);
                         cn.y = __log2f(v);
                         cn.z = __frcp_rn(v);
                     }

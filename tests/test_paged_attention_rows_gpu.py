@@ -125,3 +125,32 @@ def test_value_scales_down_to_zero(n, causal, where, scale):
     table = torch.arange(15, dtype=torch.int32, device="cuda")[None]
     out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32([L]), i32([0, n]), n, 0.125, causal=causal, lse=True)
     check(out, lse, formula(q, cache, table, [L], [0, n], 0.125, causal))
+
+
+def three_requests(n, g, P=16, D=64, H=2, G=2):
+    kc, ks = encode(torch.randn((12, H, P, D), generator=g, device="cuda"))
+    vc, vs = encode(torch.randn((12, H, P, D), generator=g, device="cuda"))
+    q = torch.randn((3 * n, H * G, D), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+    return q, qz.PagedKV(kc, vc, ks, vs), table, [60, 50, 64], [0, n, 2 * n, 3 * n]
+
+
+def poisoned(run, spoil, rows, heads):
+    """run() before and after spoil(): NaN in these rows and heads, every other bit as before."""
+    want, want_lse = run()
+    spoil()
+    got, lse = run()
+    hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    hit[rows, heads] = True
+    assert bool(got[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(got[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+
+
+@pytest.mark.parametrize("n", [1, 60])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -1.0])
+@pytest.mark.parametrize("page", [0, 2])
+def test_value_scales_that_are_no_sizes(n, bad, page):
+    """NaN, infinite and negative value scales are NaN in the rows that see them, in both kernels."""
+    q, cache, table, kv, cu = three_requests(n, torch.Generator(device="cuda").manual_seed(n))
+    run = lambda: qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.125, causal=False, lse=True)  # noqa: E731
+    poisoned(run, lambda: cache.v_scale[4 + page, :1].fill_(bad), slice(n, 2 * n), slice(0, 2))
