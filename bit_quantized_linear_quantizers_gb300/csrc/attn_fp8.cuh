@@ -52,6 +52,9 @@ constexpr float kLeastScale = 0x1p-80f;
 __device__ __forceinline__ float value_scale(float v) {               // NaN and negative scales: NaN
     return v >= 0.0f ? fmaxf(v, kLeastScale) : __int_as_float(0x7FFFFFFF);
 }
+__device__ __forceinline__ float key_scale(float k) {                 // infinite scales: NaN
+    return fabsf(k) < INFINITY ? k : __int_as_float(0x7FFFFFFF);
+}
 
 // 3-D TMA load of a box (channels, rows, page).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {

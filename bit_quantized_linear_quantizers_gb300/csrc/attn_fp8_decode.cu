@@ -315,12 +315,12 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         if (k.p0 >= 0) {
             const int64_t i = (int64_t)k.p0 * P.a.kv.heads + h;
             k.k0 = P.a.kv.k_scale[i];
-            k.v0 = value_scale(P.a.kv.v_scale[i]);
+            k.v0 = P.a.kv.v_scale[i];
         }
         if (P.shift == 4 && k.p1 >= 0) {
             const int64_t i = (int64_t)k.p1 * P.a.kv.heads + h;
             k.k1 = P.a.kv.k_scale[i];
-            k.v1 = value_scale(P.a.kv.v_scale[i]);
+            k.v1 = P.a.kv.v_scale[i];
         }
     };
     bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
@@ -444,7 +444,13 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         for (int u = first; u < unit + here; u += kWarps) {
             const int key0 = (sub + (u - unit)) * kKeys;
             const int from = done & 31;
-            if (from == 0) back = front;          // (the copies' batch turned over at most kStages units ago)
+            if (from == 0) {                      // (the copies' batch turned over at most kStages units ago)
+                back = front;
+                back.k0 = key_scale(back.k0);     // here, where the loads have arrived
+                back.k1 = key_scale(back.k1);
+                back.v0 = value_scale(back.v0);
+                back.v1 = value_scale(back.v1);
+            }
             const float k0 = __shfl_sync(0xffffffffu, back.k0, from), v0 = __shfl_sync(0xffffffffu, back.v0, from);
             float k1 = k0, v1 = v0;
             bool p0 = __shfl_sync(0xffffffffu, back.p0, from) >= 0, p1 = p0;

@@ -53,7 +53,7 @@ constexpr int kKStages = 3, kVStages = 2, kScStages = 4;
 constexpr int kSplitKeys = 512;
 constexpr float kPShift = 8.0f;
 constexpr float kMost = 32768.0f;                  // a sum of 16 p up to which each fits f16 (largest 65504)
-constexpr float kTiny = 1e-30f;                   // least factor of a raw score: -inf stays -inf under it
+constexpr float kTiny = 1e-30f;                   // added to the factor of a raw score: an infinite one stays so under it
 
 struct PrefillParams {
     CUtensorMap tm_k, tm_v;                       // codes as (head_dim, heads * page_size, num_pages), one page's rows a box
@@ -317,18 +317,19 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                 if (!warp_wait(bar(SC + ts % kScStages), (ts / kScStages) & 1)) { ok = false; break; }
                 if (!warp_wait(bar(SF + w), tw & 1)) { ok = false; break; }
                 tc_fence_after();
-                const float4* con = sc + (ts % kScStages) * 8;        // (k scale, log2 v scale, 1 / v scale) per 16 keys
+                const float4* con = sc + (ts % kScStages) * 8;        // (k scale, log2 v scale, 1 / v scale, +-kTiny) per 16 keys
                 const int lim = seen - t * kN;
                 const bool edge = least < (t + 1) * kN;                   // some row of the warp does not see the whole tile
-                if (edge) {                       // -inf where a row does not see a key: its score is -inf, its p 0
+                if (edge) {                       // infinite, against the scale's sign, where a row does not see a key: p 0
 #pragma unroll 1
                     for (int c = 0; c < kN; c += 16) {
                         uint32_t x[16];
                         tmem_ld16(s_addr + c, x);
+                        const uint32_t out = 0xFF800000u ^ (__float_as_uint(con[c >> 4].w) & 0x80000000u);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; e++)
-                            if (e >= lim - c) x[e] = 0xFF800000u;
+                            if (e >= lim - c) x[e] = out;
                         tmem_st16(s_addr + c, x);
                     }
                     tmem_wait_st();
@@ -359,7 +360,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                                 tmem_ld16(s_addr + c * 16, x);
                                 const float4 cn = con[c];
                                 tmem_wait_ld();
-                                const float ca = fmaxf(crow * cn.x, kTiny);
+                                const float ca = fmaf(crow, cn.x, cn.w);
 #pragma unroll
                                 for (int e = 0; e < 16; e++) mx = fmaxf(mx, fmaf(__uint_as_float(x[e]), ca, cn.y));
                             }
@@ -408,7 +409,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                             for (int gr = 0; gr < 2; gr++) {
                                 const float4 cn = con[half * 4 + cc * 2 + gr];
                                 const uint32_t* y = s[cc] + gr * 16;
-                                const float ca = fmaxf(crow * cn.x, kTiny), cb = cn.y + off;
+                                const float ca = fmaf(crow, cn.x, cn.w), cb = cn.y + off;
                                 float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                                 for (int e = 0; e < 16; e += 2) {
@@ -565,7 +566,7 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                     return p >= 0 && p < P.a.kv.num_pages ? p : P.a.kv.num_pages;
                 };
                 auto scales_of = [&](int p) {
-                    float4 cn = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+                    float4 cn = make_float4(0.0f, -INFINITY, 0.0f, kTiny);
                     if (lane < pages_tile && p < P.a.kv.num_pages) {
                         const int64_t i = (int64_t)p * P.a.kv.heads + h;
                         cn.x = __ldg(P.a.kv.k_scale + i);
@@ -594,6 +595,8 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                         const float v = value_scale(cn.z);
                         cn.y = __log2f(v);
                         cn.z = __frcp_rn(v);
+                        cn.x = key_scale(cn.x);
+                        cn.w = copysignf(kTiny, cn.x);
                     }
                     if (lane < pages_tile)
                         for (int j = 0; j < reps; j++) sc[(kt % kScStages) * 8 + lane * reps + j] = cn;

@@ -575,8 +575,10 @@ qz_status qz_kv_append_fp8_paged(const void* k, const void* v, qz_dtype xt, int6
  * are cut off there. Entries of block_table past a request's pages are not read;
  * entries outside the cache count as keys that are not seen. What lies in a page
  * behind the last token may hold any codes. A value scale of at most 2^-80 counts as 0,
- * whatever the codes under it; a negative one as NaN. Inf and NaN in q or a scale reach
- * their own request's rows only.
+ * whatever the codes under it; a negative one as NaN. Key scales may have either sign; an
+ * infinite one counts as NaN. A NaN scale makes every row NaN that sees a key under it and
+ * may do so to other rows of its request and head, but to none of another request.
+ * Inf and NaN in q reach their own request's rows only.
  * Shapes: heads_q % heads == 0, heads_q / heads <= 256, max_blocks * page_size < 2^31.
  * Alignment: q, out 16 B, ldq, ldo multiples of 8.
  * ws: qz_workspace_size(QZ_OP_ATTN_FP8_PAGED, max_q * heads_q / heads, head_dim, 0). */

@@ -154,3 +154,25 @@ def test_value_scales_that_are_no_sizes(n, bad, page):
     q, cache, table, kv, cu = three_requests(n, torch.Generator(device="cuda").manual_seed(n))
     run = lambda: qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.125, causal=False, lse=True)  # noqa: E731
     poisoned(run, lambda: cache.v_scale[4 + page, :1].fill_(bad), slice(n, 2 * n), slice(0, 2))
+
+
+@pytest.mark.parametrize("n", [1, 60])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("page", [0, 2])
+def test_key_scales_that_are_no_numbers(n, bad, page):
+    """NaN and infinite key scales are NaN in the rows that see them, in both kernels."""
+    q, cache, table, kv, cu = three_requests(n, torch.Generator(device="cuda").manual_seed(n))
+    run = lambda: qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.125, causal=False, lse=True)  # noqa: E731
+    poisoned(run, lambda: cache.k_scale[4 + page, :1].fill_(bad), slice(n, 2 * n), slice(0, 2))
+
+
+@pytest.mark.parametrize("n", [1, 60, 300])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("small", [1.0, 1e-35])
+def test_key_scales_keep_their_sign(n, causal, small):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    q, cache, table, _, cu = three_requests(n, g)
+    cache.k_scale *= torch.where(torch.rand(cache.k_scale.shape, generator=g, device="cuda") < 0.5, -small, 1.0)
+    kv = [60, 50, 17]
+    out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.3, causal=causal, lse=True)
+    check(out, lse, formula(q, cache, table, kv, cu, 0.3, causal))
