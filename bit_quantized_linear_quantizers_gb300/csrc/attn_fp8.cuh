@@ -38,11 +38,13 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
 }
 
 // The power of two that brings a row's amax into [128, 256), and its inverse
-// (both normal numbers: amax below 2^-106 is scaled by 2^113 only); 1 for a row of zeros.
+// (both normal numbers: amax below 2^-106 is scaled by 2^113 only); 1 for a row of zeros. A row
+// with an infinity is made NaN: every score of it is infinite or NaN, so its softmax is NaN.
 __device__ __forceinline__ void row_scale(float amax, float& up, float& down) {
     const int ex = (int)(__float_as_uint(amax) >> 23) & 255;
     const int se = min(max(134 + 127 - ex, 6), 240);
     up = amax > 0.0f ? __uint_as_float((uint32_t)se << 23) : 1.0f;
+    if (ex == 255) up = __int_as_float(0x7FFFFFFF);
     down = amax > 0.0f ? __uint_as_float((uint32_t)(254 - se) << 23) : 1.0f;
 }
 

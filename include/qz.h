@@ -578,7 +578,7 @@ qz_status qz_kv_append_fp8_paged(const void* k, const void* v, qz_dtype xt, int6
  * whatever the codes under it; a negative one as NaN. Key scales may have either sign; an
  * infinite one counts as NaN. A NaN scale makes every row NaN that sees a key under it and
  * may do so to other rows of its request and head, but to none of another request.
- * Inf and NaN in q reach their own request's rows only.
+ * Inf or NaN in a row of q makes that row NaN where it sees a key, and no other row.
  * Shapes: heads_q % heads == 0, heads_q / heads <= 256, max_blocks * page_size < 2^31.
  * Alignment: q, out 16 B, ldq, ldo multiples of 8.
  * ws: qz_workspace_size(QZ_OP_ATTN_FP8_PAGED, max_q * heads_q / heads, head_dim, 0). */

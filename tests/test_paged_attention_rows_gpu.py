@@ -176,3 +176,25 @@ def test_key_scales_keep_their_sign(n, causal, small):
     kv = [60, 50, 17]
     out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.3, causal=causal, lse=True)
     check(out, lse, formula(q, cache, table, kv, cu, 0.3, causal))
+
+
+@pytest.mark.parametrize("n", [1, 60])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_queries_that_are_no_numbers(n, bad):
+    """NaN and infinite queries are NaN in their own rows, in both kernels; a row that sees no key stays 0."""
+    q, cache, table, kv, cu = three_requests(n, torch.Generator(device="cuda").manual_seed(n))
+    run = lambda: qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.125, causal=True, lse=True)  # noqa: E731
+    poisoned(run, lambda: q[n:2 * n, 3, 40].fill_(bad), slice(2 * n - min(n, 50), 2 * n), slice(3, 4))
+
+
+def test_queries_that_are_no_numbers_alone_with_one_sign():
+    """An infinite query against keys that all lie to one side: every score is infinite, the row NaN."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for n in (1, 60):
+        q, cache, table, kv, cu = three_requests(n, g)
+        cache.k_codes.view(torch.float8_e4m3fn)[:, :, :, 7] = 2.0
+        for bad in (math.inf, -math.inf):
+            q[:, 1, 7] = bad
+            out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.125, causal=False, lse=True)
+            assert bool(out[:, 1].isnan().all()) and bool(lse[:, 1].isnan().all())
+            assert not bool(out[:, 0].isnan().any())
