@@ -101,7 +101,7 @@ block_tables_kernel(const int32_t* __restrict__ ctx_lens, const int32_t* __restr
                 int32_t* row = block_table + (int64_t)(b0 + lo) * ld_table;
                 const int p = j < had ? row[j] : __ldg(free_pages + s_at[lo] + (j - had));
                 if ((pos & mask) == 0) row[j] = p;
-                slot = p >= 0 ? (p << shift) + (pos & mask) : -1;
+                slot = p >= 0 && p <= 0x7fffffff >> shift ? (p << shift) + (pos & mask) : -1;
             }
             if (t < n_slots) {
                 slot_map[t] = slot;

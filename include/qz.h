@@ -531,7 +531,8 @@ typedef struct qz_paged_kv {
  *   cu_new[B + 1]   exclusive sums of new_lens (tokens of a step are packed)
  *   kv_lens[b]      ctx + new, or ctx where refused
  *   slot_map[t]     page * page_size + offset of token t, -1 where its request was
- *                   refused and for t past the last token (padding of a fixed-size step)
+ *                   refused, where its page is negative or its slots would pass 2^31,
+ *                   and for t past the last token (padding of a fixed-size step)
  *   positions[t]    position of token t in its request (nullable; 0 in the padding)
  *   free_head_out   the first entry of free_pages still free
  * n_slots: entries of slot_map and positions; tokens past it are not mapped, but
