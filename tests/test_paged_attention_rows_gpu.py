@@ -198,3 +198,17 @@ def test_queries_that_are_no_numbers_alone_with_one_sign():
             out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), n, 0.125, causal=False, lse=True)
             assert bool(out[:, 1].isnan().all()) and bool(lse[:, 1].isnan().all())
             assert not bool(out[:, 0].isnan().any())
+
+
+@pytest.mark.parametrize("kv, n", [([256], [256]), ([5000], [256]), ([300], [40]), ([0], [50]), ([517], [1]), ([700, 3], [1, 1]),
+                                   ([900, 64], [100, 1])])
+def test_a_block_table_much_wider_than_the_keys(kv, n):
+    """The parts that a wide table makes of the keys, most of them empty, against the formula."""
+    g = torch.Generator(device="cuda").manual_seed(kv[0])
+    P, D, Hkv, G = 64, 128, 2, 4
+    table, pages = page_tables(kv, P, 2, g, width=32768 // P)
+    k, v = (encode(torch.randn((pages, Hkv, P, D), generator=g, device="cuda")) for _ in range(2))
+    cache, cu = qz.PagedKV(k[0], v[0], k[1], v[1]), sums(n)
+    q = torch.randn((cu[-1], Hkv * G, D), generator=g, device="cuda").to(torch.bfloat16)
+    out, lse = qz.qz_attn_fp8_paged(q, cache, table, i32(kv), i32(cu), max(n), 0.09, lse=True)
+    check(out, lse, formula(q, cache, table, kv, cu, 0.09, True))
