@@ -51,12 +51,8 @@ __device__ __forceinline__ void row_scale(float amax, float& up, float& down) {
 // Least value scale that enters the exponent and l = sum p / sv: p <= 2^15 and 2^31 keys leave l below 2^126. Pages
 // of this scale or less (0 among them) keep their share of l; their codes are taken as 0.
 constexpr float kLeastScale = 0x1p-80f;
-__device__ __forceinline__ float value_scale(float v) {               // NaN and negative scales: NaN
-    return v >= 0.0f ? fmaxf(v, kLeastScale) : __int_as_float(0x7FFFFFFF);
-}
-__device__ __forceinline__ float key_scale(float k) {                 // infinite scales: NaN
-    return fabsf(k) < INFINITY ? k : __int_as_float(0x7FFFFFFF);
-}
+// NaN stays, and the logarithm of a negative scale is NaN.
+__device__ __forceinline__ float value_scale(float v) { return fabsf(v) < kLeastScale ? kLeastScale : v; }
 
 // 3-D TMA load of a box (channels, rows, page).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {

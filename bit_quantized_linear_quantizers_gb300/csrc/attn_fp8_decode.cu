@@ -315,12 +315,12 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         if (k.p0 >= 0) {
             const int64_t i = (int64_t)k.p0 * P.a.kv.heads + h;
             k.k0 = P.a.kv.k_scale[i];
-            k.v0 = P.a.kv.v_scale[i];
+            k.v0 = value_scale(P.a.kv.v_scale[i]);
         }
         if (P.shift == 4 && k.p1 >= 0) {
             const int64_t i = (int64_t)k.p1 * P.a.kv.heads + h;
             k.k1 = P.a.kv.k_scale[i];
-            k.v1 = P.a.kv.v_scale[i];
+            k.v1 = value_scale(P.a.kv.v_scale[i]);
         }
     };
     bool dead = false;                            // a wait gave up: no more copies, and no waits but the last ones
@@ -444,13 +444,7 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
         for (int u = first; u < unit + here; u += kWarps) {
             const int key0 = (sub + (u - unit)) * kKeys;
             const int from = done & 31;
-            if (from == 0) {                      // (the copies' batch turned over at most kStages units ago)
-                back = front;
-                back.k0 = key_scale(back.k0);     // here, where the loads have arrived
-                back.k1 = key_scale(back.k1);
-                back.v0 = value_scale(back.v0);
-                back.v1 = value_scale(back.v1);
-            }
+            if (from == 0) back = front;          // (the copies' batch turned over at most kStages units ago)
             const float k0 = __shfl_sync(0xffffffffu, back.k0, from), v0 = __shfl_sync(0xffffffffu, back.v0, from);
             float k1 = k0, v1 = v0;
             bool p0 = __shfl_sync(0xffffffffu, back.p0, from) >= 0, p1 = p0;
@@ -491,7 +485,8 @@ attn_decode_kernel(const __grid_constant__ DecodeParams P) {
                     }
                 }
             }
-            const float lv[2] = {__log2f(v0), __log2f(v1)}, iv[2] = {__frcp_rn(v0), __frcp_rn(v1)};
+            // (a term of 0 that is NaN under an infinite key scale)
+            const float lv[2] = {fmaf(k0, 0.0f, __log2f(v0)), fmaf(k1, 0.0f, __log2f(v1))}, iv[2] = {__frcp_rn(v0), __frcp_rn(v1)};
             const int live = cur.r.L - key0;      // keys of the unit that exist
             const bool nil0 = !p0 || v0 <= kLeastScale, nil1 = !p1 || v1 <= kLeastScale;     // no values
             const bool edge = live < kKeys || nil0 || nil1 || (P.a.causal && key0 + kKeys > cur.r.L - cur.r.n + 1);

@@ -593,9 +593,8 @@ attn_prefill_kernel(const __grid_constant__ PrefillParams P) {
                     const int pv = cn.z <= kLeastScale ? P.a.kv.num_pages : p;       // no values: zeros
                     if (p < P.a.kv.num_pages) {
                         const float v = value_scale(cn.z);
-                        cn.y = __log2f(v);
+                        cn.y = fmaf(cn.x, 0.0f, __log2f(v));        // (NaN under an infinite key scale)
                         cn.z = __frcp_rn(v);
-                        cn.x = key_scale(cn.x);
                         cn.w = copysignf(kTiny, cn.x);
                     }
                     if (lane < pages_tile)
