@@ -11,9 +11,9 @@ namespace {
 // Rows per KV head up to which a request takes the decode kernel, which reads the
 // keys once per 16 rows; the prefill kernel reads them once per 256 but computes
 // 128 rows at least. Measured, decode against prefill kernel, 8 KV heads of 128, 4096 keys
-// and more: 32 requests of 32 rows 119 against 128 us, of 64 rows 217 against 128, of
-// 128 rows 413 against 131; one request of 32 rows 20.1 against 23.0, of 64 rows 20.9
-// against 23.1, of 128 rows 27.3 against 23.5.
+// and more: 32 requests of 32 rows 119 against 131 us, of 64 rows 226 against 131, of
+// 128 rows 432 against 134; one request of 32 rows 20.1 against 23.1, of 64 rows 20.9
+// against 23.1, of 128 rows 27.5 against 23.6.
 constexpr int kDecodeRows = 32;
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }

@@ -25,8 +25,8 @@
 // other's P V and next S do. S's TMEM columns hold P afterwards. A pair of row tiles
 // takes 32 MMAs of 64 cycles for 128 keys; the S products read both operands from shared
 // memory at its full 128 bytes a cycle. Measured, graph replays: 8192 tokens, 32 heads on
-// 8 KV heads of 128, causal: 433 us (1.27 PFLOP/s, 66 % of the 1.91 that a bf16 product
-// reaches); 4864 rows a head by 8192 keys without a mask: 466 us (73 %). What is missing is
+// 8 KV heads of 128, causal: 435 us (1.26 PFLOP/s, 66 % of the 1.91 that a bf16 product
+// reaches); 4864 rows a head by 8192 keys without a mask: 471 us (72 %). What is missing is
 // the chain S -> softmax -> P V of a row tile, which its partner's MMAs do not cover to the
 // end: the same hand-offs without any arithmetic take 2290 to 2760 cycles a pair
 // of tiles against 2048 of MMAs.

@@ -195,9 +195,10 @@ template <> struct Raw8<float> {
 // lies in its window of `window` tokens, for one head of K or V (blockIdx.y).
 // Warp w of the group holds tokens 16w .. 16w+15 of the page's run in
 // registers, D / 8 lanes of 8 values per token, so x is read once; the amax
-// goes through shared memory. Bound by HBM for prompts (16 thousand bf16 tokens, 8 heads
-// of 128, pages of 16: 27 us, 62 % of the measured copy rate; 5, 6 or 8 CTAs on an SM 36, 40, 46: they spill) and by
-// latency for single tokens (64 of them: 5.4 us).
+// goes through shared memory. A group takes page after page in series: slots, rows,
+// maximum, codes. Prompts are bound by that chain rather than by a unit (16 thousand bf16 tokens, 8 heads of
+// 128, pages of 16: 27 us, 62 % of the measured copy rate, SMs 55 % busy; 5, 6 or 8 CTAs on an SM 36, 40, 46: they
+// spill), single tokens by latency (64 of them: 5.4 us).
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas<T>)
 kv_append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t tokens, int64_t ldk, int64_t ldv,

@@ -567,19 +567,22 @@ qz_status qz_kv_append_fp8_paged(const void* k, const void* v, qz_dtype xt, int6
  *   seen: j < L, and for causal j <= L - n + i (the last query sees every key)
  *   O[i] = sum_j softmax_j(x[i, j]) V[j];  lse[i] = ln sum_j exp(x[i, j])
  * A row that sees nothing gives O = 0 and lse = -inf. Not causal: a cross
- * attention to states of another length. Numerics: q enters as two E4M3 parts whose
- * sum keeps 8 significant bits (exact for elements above 2^-10 of their row's amax),
- * sums in fp32; the probabilities are rounded to 8 significant bits or more before
- * they meet V; O is rounded once to bf16.
+ * attention to states of another length.
+ * Numerics: q enters as two E4M3 parts, exact for elements above 2^-10 of their row's amax
+ * and off by at most 2^-17 of it below; requests of few rows a KV head (n * heads_q / heads,
+ * up to 32) as f16 instead, exact down to 2^-29 of the amax. Sums are fp32. The
+ * probabilities are rounded to f16 before they meet V (11 bits; one whose product with its
+ * value scale is below 2^-31 of the row's largest may be lost). O is rounded once to bf16.
  * q: bf16 [tokens, heads_q, head_dim], rows ldq elements apart; out: bf16, rows ldo
- * apart; lse: nullable fp32 [tokens, heads_q]. max_q: the largest n; longer requests
- * are cut off there. Entries of block_table past a request's pages are not read;
- * entries outside the cache count as keys that are not seen. What lies in a page
- * behind the last token may hold any codes. A value scale of at most 2^-80 counts as 0,
- * whatever the codes under it; a negative one as NaN. Key scales may have either sign; an
- * infinite one counts as NaN. A NaN scale makes every row NaN that sees a key under it and
- * may do so to other rows of its request and head, but to none of another request.
- * Inf or NaN in a row of q makes that row NaN where it sees a key, and no other row.
+ * apart; lse: nullable fp32 [tokens, heads_q]. Rows of no request are not written.
+ * max_q: the largest n; longer requests are cut off there. Entries of block_table past a
+ * request's pages are not read; entries outside the cache count as keys that are not seen.
+ * What lies in a page behind the last token may hold any codes.
+ * A value scale of at most 2^-80 counts as 0, whatever the codes under it; a negative or
+ * infinite one as NaN. Key scales may have either sign; an infinite one counts as NaN. A NaN
+ * scale or code makes every row NaN that sees its key and may do so to other rows of its
+ * request and KV head, but to none of another request. Inf or NaN in a row of q makes
+ * that row NaN where it sees a key, and no other row.
  * Shapes: heads_q % heads == 0, heads_q / heads <= 256, max_blocks * page_size < 2^31.
  * Alignment: q, out 16 B, ldq, ldo multiples of 8.
  * ws: qz_workspace_size(QZ_OP_ATTN_FP8_PAGED, max_q * heads_q / heads, head_dim, 0). */
