@@ -578,8 +578,8 @@ qz_status qz_kv_append_fp8_paged(const void* k, const void* v, qz_dtype xt, int6
  * max_q: the largest n; longer requests are cut off there. Entries of block_table past a
  * request's pages are not read; entries outside the cache count as keys that are not seen.
  * What lies in a page behind the last token may hold any codes.
- * A value scale of at most 2^-80 counts as 0, whatever the codes under it; a negative or
- * infinite one as NaN. Key scales may have either sign; an infinite one counts as NaN. A NaN
+ * A value scale of magnitude 2^-80 or less counts as 0, whatever the codes under it; other
+ * negative ones and infinite ones as NaN. Key scales may have either sign; an infinite one counts as NaN. A NaN
  * scale or code makes every row NaN that sees its key and may do so to other rows of its
  * request and KV head, but to none of another request. Inf or NaN in a row of q makes
  * that row NaN where it sees a key, and no other row.
