@@ -846,6 +846,10 @@ def qz_block_tables(ctx_lens, new_lens, block_table, free_pages, free_head, page
     requests whose ctx_lens + new_lens tokens need them (block_table is updated in place). All
     tensors int32. Returns (slot_map [n_slots], positions [n_slots], cu_new [B + 1], kv_lens [B],
     free_head_out [1]); tokens of requests that could not be admitted have slot -1."""
+    if stream is not None:                       # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return qz_block_tables(ctx_lens, new_lens, block_table, free_pages, free_head, page_size, n_slots, kv_lens,
+                                   cu_new, slot_map, positions, free_head_out)
     d = _device()
     tab, B, blocks, ld = _table(block_table, "block_table", d)
     i32, dev = torch.int32, block_table.device
@@ -865,7 +869,7 @@ def qz_block_tables(ctx_lens, new_lens, block_table, free_pages, free_head, page
         _i32(free_pages, "free_pages", d, n_free), n_free, _i32(free_head, "free_head", d, 1),
         _i32(kv_lens, "kv_lens", d, B), _i32(cu_new, "cu_new", d, B + 1), _i32(slot_map, "slot_map", d, n_slots),
         _i32(positions, "positions", d, n_slots), n_slots, _i32(free_head_out, "free_head_out", d, 1),
-        _raw_stream(stream, d))
+        _raw_stream(None, d))
     if st:
         raise QZError(st, "qz_block_tables")
     return slot_map, positions, cu_new, kv_lens, free_head_out
@@ -900,6 +904,9 @@ def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int,
     most max_q) over the first kv_lens[b] tokens of the cache pages block_table[b]. causal: the last
     query of a request sees all its keys; otherwise every query does (cross attention). Returns
     (out bf16 like q, lse); lse=True allocates fp32 [tokens, heads_q], None leaves it out."""
+    if stream is not None:                       # out, lse and workspace belong to the stream that writes them
+        with torch.cuda.stream(stream):
+            return qz_attn_fp8_paged(q, cache, block_table, kv_lens, cu_q, max_q, scale, causal, out, lse, ws)
     d = _device()
     _on_cache(cache, d)
     dim = cache.head_dim
@@ -922,7 +929,7 @@ def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int,
     buf, nb = _ws(ws, qz_workspace_size(OP_ATTN_FP8_PAGED, max_q * (hq // cache.heads), dim), d)
     st = lib.qz_attn_fp8_paged(q.data_ptr(), ldq, tokens, hq, p_cu, B, max_q, cache._ref, tab,
                                blocks, ld, p_kv, scale, 1 if causal else 0, out.data_ptr(), ldo,
-                               p_lse, _ptr(buf), nb, _raw_stream(stream, d))
+                               p_lse, _ptr(buf), nb, _raw_stream(None, d))
     if st:
         raise QZError(st, "qz_attn_fp8_paged")
     return out, lse

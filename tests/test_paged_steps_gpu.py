@@ -108,3 +108,30 @@ def test_two_streams_at_once():
             for j in range(5):
                 assert torch.equal(outs[i][r * 5 + j], alone[(j + r % 5) % 5]), (i, r, j)
     assert qz.qz_device_error() == 0
+
+
+def test_outputs_belong_to_the_stream_of_the_call():
+    """Memory that the current stream has freed but still writes to does not become the output, lse, workspace or slot
+    map of a call on another stream."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    P, D, H, L = 32, 128, 2, 3000
+    k, v = (encode(torch.randn((L // P + 1, H, P, D), generator=g, device="cuda")) for _ in range(2))
+    cache, table = qz.PagedKV(k[0], v[0], k[1], v[1]), torch.arange(L // P + 1, dtype=torch.int32, device="cuda")[None]
+    side = torch.cuda.Stream()
+    for n in (1, 100):
+        q = torch.randn((n, 8 * H, D), generator=g, device="cuda").to(torch.bfloat16)
+        args = (q, cache, table, i32([L]), i32([0, n]), n, 0.1)
+        lens, free, head = (i32([0, 40]), i32([n, 7])), torch.arange(300, dtype=torch.int32, device="cuda"), i32([5])
+        tables = [torch.zeros((2, 200), dtype=torch.int32, device="cuda") for _ in range(2)]
+        want = qz.qz_attn_fp8_paged(*args, lse=True)
+        want += qz.qz_block_tables(*lens, tables[0], free, head, P, n + 7)
+        torch.cuda.synchronize()
+        need = qz.qz_workspace_size(qz.OP_ATTN_FP8_PAGED, n * 8, D)
+        torch.cuda._sleep(100_000_000)                        # the current stream is behind
+        for shape, dtype in ((q.shape, torch.bfloat16), (q.shape[:2], torch.float32), ((need,), torch.uint8), ((n + 7,), torch.int32)):
+            for _ in range(3):
+                torch.empty(shape, dtype=dtype, device="cuda").fill_(7)
+        got = qz.qz_attn_fp8_paged(*args, lse=True, stream=side)
+        got += qz.qz_block_tables(*lens, tables[1], free, head, P, n + 7, stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
