@@ -27,6 +27,7 @@ __all__ = [
     "qz_gemm_int8", "qz_gemm_fp8_block_quant", "qz_gemm_nvfp4_quant", "qz_gemm_mxfp4_quant", "SMOOTH_NONE",
     "SMOOTH_DIVIDE",
     "SMOOTH_MULTIPLY", "PagedKV", "qz_block_tables", "qz_kv_append_fp8_paged", "qz_attn_fp8_paged",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "qz_moe_route", "qz_moe_gemm_fp8", "qz_moe_gemm_fp8_swiglu", "qz_residual_rmsnorm",
 ]
 
 F32, BF16 = 0, 1
@@ -36,7 +37,8 @@ OP_QUANTIZE_FP8, OP_QUANTIZE_NVFP4, OP_KV_WRITE_FP8 = 0, 1, 2
 OP_GEMM_W4A16, OP_GEMM_FP8_BLOCK, OP_GEMM_NVFP4, OP_GEMM_MXFP4 = 3, 4, 5, 6
 OP_GEMM_NVFP4_GROUPED, OP_PREPARE_FP4_SCALES, OP_QUANTIZE_NVFP4_GROUPED = 7, 8, 9
 OP_KV_WRITE_FP8_PER_HEAD, OP_KV_WRITE_FP8_CHANNEL_ZP, OP_COL_AMAX = 10, 11, 12
-OP_ATTN_FP8_PAGED = 13
+OP_ATTN_FP8_PAGED, OP_MOE_ROUTE = 13, 14
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 SMOOTH_NONE, SMOOTH_DIVIDE, SMOOTH_MULTIPLY = 0, 1, 2
 
 if not os.path.exists(LIB):
@@ -66,6 +68,16 @@ class _Nvfp4Tensor(ctypes.Structure):
 class _PagedKV(ctypes.Structure):
     _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scale", _P), ("v_scale", _P), ("page_stride", _I64),
                 ("num_pages", _I), ("page_size", _I), ("heads", _I), ("head_dim", _I)]
+
+
+class _MoeRouting(ctypes.Structure):
+    _fields_ = [("experts", _I), ("top_k", _I), ("score", _I), ("renormalize", _I), ("scale", ctypes.c_float),
+                ("groups", _I), ("top_groups", _I), ("group_best", _I)]
+
+
+class _BlockOutput(ctypes.Structure):
+    _fields_ = [("y", _P), ("rows", _I64), ("ldy", _I64), ("k", _I), ("token_row", _P), ("weights", _P),
+                ("alpha", ctypes.c_float), ("gamma", _P)]
 
 
 _SIGS = {
@@ -104,6 +116,11 @@ _SIGS = {
     "qz_attn_fp8_paged": (_I, [_P, _I64, _I64, _I, _P, _I, _I, ctypes.POINTER(_PagedKV), _P, _I, _I64, _P,
                                ctypes.c_float, _I, _P, _I64, _P, _P, _SZ, _P]),
     "qz_gemm_mxfp4_quant": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "qz_moe_route": (_I, [_P, _I, _I64, _I64, _P, _P, ctypes.POINTER(_MoeRouting), _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "qz_moe_gemm_fp8": (_I, [_P, _P, _I64, _P, _I64, _P, _I, _P, _P, _P, _I, _I, _P]),
+    "qz_moe_gemm_fp8_swiglu": (_I, [_P, _P, _I64, _P, _I64, _P, _I, _P, _P, _P, _P, _I, _I, _P]),
+    "qz_residual_rmsnorm": (_I, [_P, _I, _I64, _I, _I64, ctypes.POINTER(_BlockOutput), _P, _I64, _P, ctypes.c_float,
+                                 _P, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -933,3 +950,149 @@ def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int,
     if st:
         raise QZError(st, "qz_attn_fp8_paged")
     return out, lse
+
+
+# ------------------------------------------------- a block of experts in FP8
+
+def qz_moe_route(logits, top_k: int, score: int = SCORE_SOFTMAX, renormalize: bool = True, scale: float = 1.0, bias=None,
+                 groups: int = 1, top_groups: int = 1, group_best: int = 1, n_tokens=None, ids=None, weights=None,
+                 offsets=None, row_token=None, token_row=None, ws=None, stream=None):
+    """Route logits [tokens, experts] (fp32 or bf16; rows may be strided) to the top_k experts of each token.
+    bias (fp32 [experts]) enters the choice alone; groups of consecutive experts are chosen first, by the
+    sum of their group_best best keys. n_tokens (int32 [1] on the GPU): tokens from there on are padding.
+    Returns (ids i32 [tokens, top_k], weights f32 [tokens, top_k], offsets i32 [experts + 1], row_token i32
+    [tokens * top_k], token_row i32 [tokens, top_k]): the experts' rows, as the products take them."""
+    if stream is not None:                       # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return qz_moe_route(logits, top_k, score, renormalize, scale, bias, groups, top_groups, group_best, n_tokens,
+                                ids, weights, offsets, row_token, token_row, ws)
+    d = _device()
+    T, E, ld = _rows_cols_ld(logits)
+    lt = _dtype_code(logits)
+    _on(logits, "logits", d)
+    dev, n = logits.device, T * top_k
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    if row_token is None:
+        row_token = torch.empty((n,), dtype=torch.int32, device=dev)
+    if token_row is None:
+        token_row = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    r = _MoeRouting(E, top_k, score, 1 if renormalize else 0, scale, groups, top_groups, group_best)
+    args = (_opt(bias, "bias", d, torch.float32, E), None if n_tokens is None else _i32(n_tokens, "n_tokens", d, 1),
+            ctypes.byref(r), _i32(ids, "ids", d, n), _arg(weights, "weights", d, torch.float32, n),
+            _i32(offsets, "offsets", d, E + 1), _i32(row_token, "row_token", d, n), _i32(token_row, "token_row", d, n))
+    buf, nb = _ws(ws, qz_workspace_size(OP_MOE_ROUTE, T, E, top_k), d)
+    st = lib.qz_moe_route(logits.data_ptr(), lt, T, ld, *args, _ptr(buf), nb, _raw_stream(None, d))
+    if st:
+        raise QZError(st, "qz_moe_route")
+    return ids, weights, offsets, row_token, token_row
+
+
+def _experts(qA, sA, qW, sW, offsets, row_token, d):
+    if qW.dim() != 3 or qA.dim() != 2 or qA.shape[1] != qW.shape[2]:
+        raise ValueError(f"expected qA [tokens, K] and qW [experts, N, K], got {tuple(qA.shape)} and {tuple(qW.shape)}")
+    tokens, K = qA.shape
+    E, N, _ = qW.shape
+    rows = tokens if row_token is None else row_token.numel()
+    args = (_arg(qA, "qA", d, 1, tokens * K), _arg(sA, "sA", d, torch.float32, tokens * (K // 128)), tokens,
+            None if row_token is None else _i32(row_token, "row_token", d, rows), rows,
+            _i32(offsets, "offsets", d, E + 1), E, _arg(qW, "qW", d, 1, E * N * K),
+            _arg(sW, "sW", d, torch.float32, E * (N // 128) * (K // 128)))
+    return args, rows, N, K
+
+
+def qz_moe_gemm_fp8(qA, sA, qW, sW, offsets, row_token=None, Y=None, stream=None):
+    """The experts' products: row r of expert e (offsets[e] <= r < offsets[e + 1]) is row row_token[r] of qA (row r
+    without row_token) times qW[e]^T. qA [tokens, K] with scales [tokens, K/128], qW [experts, N, K] with scales
+    [experts, N/128, K/128]: E4M3 codes and fp32 scales. Returns Y bf16 [rows, N]; rows of no expert are not written."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qz_moe_gemm_fp8(qA, sA, qW, sW, offsets, row_token, Y)
+    d = _device()
+    args, rows, N, K = _experts(qA, sA, qW, sW, offsets, row_token, d)
+    if Y is None:
+        Y = torch.empty((rows, N), dtype=torch.bfloat16, device=qA.device)
+    st = lib.qz_moe_gemm_fp8(*args, _arg(Y, "Y", d, torch.bfloat16, rows * N), N, K, _raw_stream(None, d))
+    if st:
+        raise QZError(st, "qz_moe_gemm_fp8")
+    return Y
+
+
+def qz_moe_gemm_fp8_swiglu(qA, sA, qW, sW, offsets, row_token=None, codes=None, scales=None, stream=None):
+    """The experts' gate and up products (qW [experts, 2 I, K]: gate rows, then up rows) with h = silu(gate) * up
+    encoded in the epilogue. Otherwise as qz_moe_gemm_fp8. Returns (codes u8 [rows, I], scales f32 [rows, I/128])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qz_moe_gemm_fp8_swiglu(qA, sA, qW, sW, offsets, row_token, codes, scales)
+    d = _device()
+    args, rows, N, K = _experts(qA, sA, qW, sW, offsets, row_token, d)
+    if N % 2:
+        raise ValueError(f"qW: expected as many gate rows as up rows, got {N} rows")
+    I = N // 2  # noqa: E741
+    if codes is None:
+        codes = torch.empty((rows, I), dtype=torch.uint8, device=qA.device)
+    if scales is None:
+        scales = torch.empty((rows, I // 128), dtype=torch.float32, device=qA.device)
+    st = lib.qz_moe_gemm_fp8_swiglu(*args, _arg(codes, "codes", d, 1, rows * I),
+                                    _arg(scales, "scales", d, torch.float32, rows * (I // 128)), I, K, _raw_stream(None, d))
+    if st:
+        raise QZError(st, "qz_moe_gemm_fp8_swiglu")
+    return codes, scales
+
+
+def _rows2(t, name, d, cols, dtype):
+    """[rows, cols] with dense rows; returns the stride between rows."""
+    if t.get_device() != d or t.dtype is not dtype or t.dim() != 2 or t.shape[1] != cols or (t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected {dtype} [rows, {cols}] with dense rows on cuda:{d}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def qz_residual_rmsnorm(x, gamma=None, y=None, token_row=None, weights=None, alpha: float = 1.0, gamma_y=None,
+                        eps: float = 1e-6, out=True, normed=None, fp8=None, stream=None):
+    """r = x + alpha * z and its RMSNorm n = r * gamma / sqrt(mean(r^2) + eps), in one pass. z: the block's output y
+    (bf16 [tokens, hidden]), or with token_row [tokens, k] (and weights [tokens, k], fp32) the sum of that many rows of
+    y; gamma_y: z is normed before it is added. x: fp32 or bf16 [tokens, hidden], gammas of its type.
+    out: True allocates r in x's type, a tensor takes it (x itself may), None leaves it out; normed: the same for n in
+    bf16; fp8: the same for n's E4M3 codes and scales per 128 columns, a pair of tensors or True.
+    Returns (r, normed, codes, scales), None where left out."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qz_residual_rmsnorm(x, gamma, y, token_row, weights, alpha, gamma_y, eps, out, normed, fp8)
+    d = _device()
+    T, H, ldx = _rows_cols_ld(x)
+    xt = _dtype_code(x)
+    _on(x, "x", d)
+    block = None
+    if y is not None:
+        k = token_row.shape[1] if token_row is not None and token_row.dim() == 2 else (
+            weights.shape[1] if weights is not None and weights.dim() == 2 else 1)
+        block = _BlockOutput(y.data_ptr(), y.shape[0], _rows2(y, "y", d, H, torch.bfloat16), k,
+                             None if token_row is None else _i32(token_row, "token_row", d, T * k),
+                             _opt(weights, "weights", d, torch.float32, T * k), alpha, _opt(gamma_y, "gamma_y", d, x.dtype, H))
+    elif token_row is not None or weights is not None or gamma_y is not None:
+        raise ValueError("token_row, weights and gamma_y belong to a block's output y")
+    if out is True:
+        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    if normed is True:
+        normed = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    if fp8 is True:
+        fp8 = (torch.empty((T, H), dtype=torch.uint8, device=x.device),
+               torch.empty((T, H // 128), dtype=torch.float32, device=x.device))
+    codes, scales = fp8 if fp8 is not None else (None, None)
+    ldo = 0
+    if out is not None:
+        ldo = _rows2(out, "out", d, H, x.dtype)
+        if out.shape[0] != T:
+            raise ValueError(f"out: expected {T} rows, got {out.shape[0]}")
+    st = lib.qz_residual_rmsnorm(x.data_ptr(), xt, T, H, ldx, None if block is None else ctypes.byref(block), _ptr(out), ldo,
+                                 _opt(gamma, "gamma", d, x.dtype, H), eps, _opt(normed, "normed", d, torch.bfloat16, T * H),
+                                 _opt(codes, "codes", d, 1, T * H), _opt(scales, "scales", d, torch.float32, T * (H // 128)),
+                                 _raw_stream(None, d))
+    if st:
+        raise QZError(st, "qz_residual_rmsnorm")
+    return out, normed, codes, scales

@@ -87,8 +87,9 @@ typedef enum qz_op {
     QZ_OP_KV_WRITE_FP8_PER_HEAD = 10, /* d0 = B*H, d1 = T*D                   */
     QZ_OP_KV_WRITE_FP8_CHANNEL_ZP = 11, /* d0 = B*H, d1 = T, d2 = D           */
     QZ_OP_COL_AMAX = 12,                /* d0 = rows, d1 = cols               */
-    QZ_OP_ATTN_FP8_PAGED = 13           /* d0 = query rows of the largest request per KV
+    QZ_OP_ATTN_FP8_PAGED = 13,          /* d0 = query rows of the largest request per KV
                                            head (max_q * heads_q / heads), d1 = head_dim */
+    QZ_OP_MOE_ROUTE = 14                /* d0 = tokens, d1 = experts, d2 = top_k */
 } qz_op;
 
 typedef enum qz_smooth_op {
@@ -590,6 +591,105 @@ qz_status qz_attn_fp8_paged(const uint16_t* q, int64_t ldq, int64_t tokens, int 
                             int max_q, const qz_paged_kv* cache, const int32_t* block_table, int max_blocks,
                             int64_t ld_table, const int32_t* kv_lens, float sm_scale, int causal, uint16_t* out,
                             int64_t ldo, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------- a block of experts in FP8
+ * What a decoder block of experts needs around the products that quantized weights are
+ * for: the choice of experts and the order of their rows (qz_moe_route), the products
+ * over those rows (qz_moe_gemm_fp8_swiglu, qz_moe_gemm_fp8), and the residual norm that
+ * joins the experts' rows by their gates and encodes the next product's input
+ * (qz_residual_rmsnorm). None of them needs a count on the host, so a step can be
+ * captured into a CUDA graph and replayed with other routings. */
+
+typedef enum qz_score {
+    QZ_SCORE_SOFTMAX = 0,     /* s = softmax over the token's experts */
+    QZ_SCORE_SIGMOID = 1      /* s = 1 / (1 + exp(-l))                */
+} qz_score;
+
+typedef struct qz_moe_routing {
+    int experts;              /* 1..512 */
+    int top_k;                /* 1..16, <= top_groups * experts / groups */
+    qz_score score;
+    int renormalize;          /* 1: the chosen scores are divided by their sum */
+    float scale;              /* finite factor of the weights */
+    int groups;               /* divides experts, 1..32; experts of a group are consecutive */
+    int top_groups;           /* 1..groups */
+    int group_best;           /* 1 or 2 (<= experts / groups): how many of its best keys make a group's score */
+} qz_moe_routing;
+
+/* Routing of tokens to experts. logits: [tokens, experts] of type lt, rows ldl elements
+ * apart. A NaN logit counts as -inf, +inf as the largest fp32 value. For token t:
+ *   s[e] the score of expert e;  key[e] = s[e] + bias[e] (bias: nullable fp32 [experts])
+ *   experts with logit -inf, or with bias NaN or -inf, are closed (a bias of +inf counts as the
+ *   largest fp32 value)
+ *   groups > 1: a group's score is the sum of the group_best largest keys of its open experts (of
+ *   as many as there are); experts outside the best top_groups groups are closed
+ *   ids[t, :] = the top_k open experts by key, in descending order (without bias by logit,
+ *   which orders them alike); ties, of groups too, go to the lowest index
+ *   weights[t, j] = scale * s[ids[t, j]], divided by the sum over j where renormalize is set
+ * Keys are compared as in 64 bits, where 32 would decide otherwise too. Where fewer than
+ * top_k experts are open, the rest of the token's ids is -1 with weight 0.
+ * n_tokens: nullable device int32; tokens from *n_tokens on are padding of a fixed-size step:
+ * all their ids are -1.
+ * The plan of the products: the pairs (t, j) with ids[t, j] = e have the rows offsets[e] ..
+ * offsets[e + 1] - 1, in the order of t. offsets: [experts + 1]; row_token[r] = t (-1 from row
+ * offsets[experts] on); token_row[t, j] = r (-1 where ids is).
+ * ids, weights, token_row: [tokens, top_k]; row_token: [tokens * top_k].
+ * Shapes: tokens * top_k < 2^31. Alignment: logits its element size, the others 4 B.
+ * ws: qz_workspace_size(QZ_OP_MOE_ROUTE, tokens, experts, top_k). tokens == 0 writes offsets. */
+qz_status qz_moe_route(const void* logits, qz_dtype lt, int64_t tokens, int64_t ldl, const float* bias,
+                       const int32_t* n_tokens, const qz_moe_routing* routing, int32_t* ids, float* weights,
+                       int32_t* offsets, int32_t* row_token, int32_t* token_row, void* ws, size_t ws_bytes, void* stream);
+
+/* The experts' products, block-scaled FP8 as qz_gemm_fp8_block ("量化部署实战", 练习 2). Row r
+ * with offsets[e] <= r < offsets[e + 1] is multiplied by the weight of expert e:
+ *   P[r, n] = sum_kb sA[a, kb] * sW[e, n/128, kb] * sum_{k in kb} qA[a, k] * qW[e, n, k],
+ *   a = row_token[r], or r where row_token is NULL;  fp32 accumulation
+ * qz_moe_gemm_fp8:        Y[r, :] = bf16_rne(P[r, :]), Y bf16 [rows, N]
+ * qz_moe_gemm_fp8_swiglu: N = 2 I, rows 0 .. I-1 of a weight are the gate's, the others the up
+ *   projection's: h = g * u / (1 + exp(-g)) with g = P[r, i], u = P[r, I + i] in fp32, encoded as
+ *   qz_quantize_fp8(GROUP_1x128) encodes h: y_codes [rows, I], y_scales fp32 [rows, I/128]
+ * qA: E4M3 [tokens, K], sA: fp32 [tokens, K/128] (qz_quantize_fp8 GROUP_1x128, or
+ * qz_residual_rmsnorm). qW: E4M3 [experts, N, K], sW: fp32 [experts, N/128, K/128]
+ * (qz_quantize_fp8 BLOCK_128x128 on the weights as one tensor of experts * N rows).
+ * offsets: device int32 [experts + 1], ascending, as qz_moe_route writes them; what lies outside
+ * 0 .. rows is cut off. Rows of no expert are not written. A row whose row_token lies outside
+ * 0 .. tokens-1 is a row of zeros. A NaN in a row of qA or sA reaches that row alone.
+ * Shapes: experts 1..512, rows and tokens < 2^31, experts * N < 2^31, K % 128 == 0, N % 128 == 0 (I % 128 == 0).
+ * Alignment: qA, qW, outputs 16 B, the others 4 B. rows == 0 is a no-op. No workspace. */
+qz_status qz_moe_gemm_fp8(const uint8_t* qA, const float* sA, int64_t tokens, const int32_t* row_token, int64_t rows,
+                          const int32_t* offsets, int experts, const uint8_t* qW, const float* sW, uint16_t* Y, int N,
+                          int K, void* stream);
+qz_status qz_moe_gemm_fp8_swiglu(const uint8_t* qA, const float* sA, int64_t tokens, const int32_t* row_token,
+                                 int64_t rows, const int32_t* offsets, int experts, const uint8_t* qW, const float* sW,
+                                 uint8_t* y_codes, float* y_scales, int I, int K, void* stream);
+
+/* What a block adds to the residual stream (qz_residual_rmsnorm). */
+typedef struct qz_block_output {
+    const uint16_t* y;        /* bf16 [rows, hidden], rows ldy elements apart */
+    int64_t rows, ldy;
+    int k;                    /* rows of y per token, 1..16 */
+    const int32_t* token_row; /* [tokens, k]: their places in y, those outside 0 .. rows-1 add nothing; NULL:
+                                 token t has the rows t*k .. t*k + k-1 */
+    const float* weights;     /* nullable fp32 [tokens, k]: the gates */
+    float alpha;              /* finite scale of the block's output */
+    const void* gamma;        /* nullable [hidden], of x's type: norm of the block's output */
+} qz_block_output;
+
+/* Residual, norm and quantization around a block, in one pass:
+ *   z[t] = sum_j weights[t, j] * y[token_row[t, j]];  with block->gamma: z *= block->gamma / sqrt(mean(z^2) + eps)
+ *   r = x + alpha * z (r = x where block is NULL);  n = r * gamma / sqrt(mean(r^2) + eps)
+ * x: [tokens, hidden] of type xt, rows ldx elements apart. x_out: nullable, r in xt, rows ldo
+ * apart; it may be x itself. gamma: nullable [hidden] of type xt; without it there are no n and no
+ * codes. normed: nullable, n in bf16, dense. codes, scales: nullable together, n as
+ * qz_quantize_fp8(GROUP_1x128) encodes it: [tokens, hidden] and fp32 [tokens, hidden/128].
+ * All sums are fp32 and n, its codes and x_out come from the unrounded fp32 r, each rounded once. A
+ * row whose sum of squares passes fp32's range gives n = 0, one with an infinity or NaN gives NaN;
+ * neither reaches another row.
+ * Shapes: hidden % 8 == 0, 8..16384; hidden % 128 == 0 with codes. eps finite, > 0. tokens < 2^31.
+ * Alignment: x, x_out, y, gammas, normed, codes 16 B, ldx, ldo, ldy multiples of 16 bytes, the others 4 B. */
+qz_status qz_residual_rmsnorm(const void* x, qz_dtype xt, int64_t tokens, int hidden, int64_t ldx,
+                              const qz_block_output* block, void* x_out, int64_t ldo, const void* gamma, float eps,
+                              uint16_t* normed, uint8_t* codes, float* scales, void* stream);
 
 #ifdef __cplusplus
 }
