@@ -1,107 +1,569 @@
-// moe_gemm_fp8.cu -- the experts' products over ragged rows, block-scaled FP8:
+// moe_gemm_fp8.cu -- the experts' products over ragged rows, block-scaled FP8 on tcgen05:
 //   P[r, n] = sum_kb sA[a, kb] sW[e, n/128, kb] sum_{k in kb} qA[a, k] qW[e, n, k]
 // with a = row_token[r] and e the expert whose rows contain r; output in bf16, or SwiGLU of
 // the gate and up columns encoded as E4M3 with a scale per 128 columns.
 //
-// Simple form: a CTA takes 16 rows of one expert and 128 columns (of gate and of up with SwiGLU),
-// a thread one column; the rows' codes lie in shared memory, widened, a block of 128 of K at a time.
+// A work item is 128 rows of one expert by 256 columns (two boxes of 128 weight rows; with
+// SwiGLU one of the gate and the same one of the up projection, so that h is made where P
+// is). The number of items is known on the GPU alone: a warp reads the offsets and hands the
+// items out through a ring in shared memory, an expert's row tiles before its next columns,
+// so that the CTAs of one moment share weights and rows in L2.
+//
+// CTA of 12 warps, one per SM:
+//  warp 0     weights: TMA boxes of 128 x 128 bytes into a 4-stage ring
+//  warp 1     MMA: per block of 128 of K four tcgen05.mma (M 128, N 256, K 32) into one of two
+//             accumulators of 256 columns in tensor memory
+//  warp 2     rows: gathered by their tokens, four a copy (gather4), a lane for each four; as
+//             one box where a tile is full and in order
+//  warp 3     items
+//  warps 4-11 promotion: block scales are fp32, so every block's partial sums leave tensor
+//             memory to be added as acc += P_kb * (sA sW). A thread holds one row of 64 columns of
+//             each of the two boxes.
+// What bounds it with many rows is the cycle of an accumulator: MMA 512 cycles, hand-off, promotion,
+// hand-off, for two blocks of K by turns. So a promotion is kept short: 224 registers a
+// thread (the other warps give theirs up) hold the 128 sums and two 32-column reads, one in
+// flight while the other is added, and scales are read four blocks at a time.
+// With few rows the bound is the weights' way from memory, and the promotion and the gather of rows that
+// are not there are left out. Where items are fewer than SMs (rows <= 32), a cluster shares an item's K.
 #include "qz_moe.cuh"
+#include "qz_tc.cuh"
+
+#include <algorithm>
+#include <cstring>
 
 namespace qz {
 
 namespace {
 
-constexpr int kRows = 16;
+__device__ unsigned int g_moe_err;
 
+constexpr int BM = 128, BN = 256, BK = 128, STAGES = 4;
+constexpr int A_BYTES = BM * BK, HALF_BYTES = 128 * BK;
+constexpr int STAGE_BYTES = A_BYTES + 2 * HALF_BYTES;
+constexpr int EPI_WARPS = 8, THREADS = 128 + EPI_WARPS * 32;
+constexpr int REGS_FEED = 56, REGS_EPI = 224;     // 128 * 56 + 256 * 224 = 384 * 168, what the CTA is launched with
+constexpr int INFO = 4;                           // items in flight
+constexpr uint32_t TMEM_COLS = 2 * BN;
+constexpr int STG_WARP = 32 * 128;                // a warp's output: 32 rows of 64 bf16
+constexpr int STG_OFF = STAGES * STAGE_BYTES;
+constexpr int INFO_OFF = STG_OFF + EPI_WARPS * STG_WARP;
+constexpr int BAR_OFF = INFO_OFF + INFO * 16;
+constexpr int BARS = 2 * STAGES + 4 + 2 * INFO;
+constexpr int SMEM_BYTES = BAR_OFF + BARS * 8 + 16 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory of a CTA");
+constexpr int SPLIT_ROWS = 32, MAX_SPLITS = 4;    // rows of a shared item: one warp's lanes
+constexpr int PART_BYTES = SPLIT_ROWS * BN * 4;
+static_assert((MAX_SPLITS - 1) * PART_BYTES <= STAGES * STAGE_BYTES, "the others' sums fit in the ring");
+
+template <int REGS> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
+
+// acc (two fp32 lanes) += v * s per lane, each lane one correctly rounded fma.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s2) {
+    asm("{ .reg .b64 t; mov.b64 t, {%1, %2}; fma.rn.f32x2 %0, t, %3, %0; }" : "+l"(acc) : "r"(v0), "r"(v1), "l"(s2));
+}
+__device__ __forceinline__ uint64_t twice(float v) {
+    return ((uint64_t)__float_as_uint(v) << 32) | __float_as_uint(v);
+}
+__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// The reads in flight have arrived; the registers pass through, so that no use of them moves before it.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Four rows (their first coordinate x) of a tensor whose map has a box one row high.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int x, int4 rows, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                 ::"r"(dst), "l"(tmap), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// An expert's rows, cut to those that exist.
+__device__ __forceinline__ int2 expert_rows(const MoeGemmArgs& a, int e) {
+    const int R = (int)a.rows, b = min(max(a.offsets[e], 0), R);
+    return make_int2(b, min(max(a.offsets[e + 1], b), R));
+}
+__device__ __forceinline__ int row_tiles(int2 r) { return (r.y - r.x) / BM + ((r.y - r.x) % BM != 0); }
+
+// nt: column tiles of an expert. splits: CTAs (a cluster) that share an item's blocks of K.
 template <bool SWIGLU>
-__global__ void __launch_bounds__(SWIGLU ? 256 : 128)
-moe_gemm_kernel(const MoeGemmArgs a) {
-    __shared__ float sx[kRows][128];
-    __shared__ float ss[kRows];
-    __shared__ int64_t sat[kRows];
-    pdl_wait();
-    // the expert and the rows of tile blockIdx.y
-    int e = 0, lo = 0, hi = 0;
-    int64_t left = blockIdx.y;
-    for (; e < a.experts; e++) {
-        lo = (int)min(max((int64_t)a.offsets[e], (int64_t)0), a.rows);
-        hi = (int)min(max((int64_t)a.offsets[e + 1], (int64_t)lo), a.rows);
-        const int64_t tiles = (hi - lo + kRows - 1) / kRows;
-        if (left < tiles) break;
-        left -= tiles;
-    }
-    if (e == a.experts) return;
-    const int r0 = lo + (int)left * kRows, nr = min(kRows, hi - r0), nkb = a.K / 128;
-    const int half = threadIdx.x >> 7, c = threadIdx.x & 127;
-    const int n0 = blockIdx.x * 128 + (half ? a.N / 2 : 0);
-    if (threadIdx.x < kRows) {
-        int64_t at = -1;
-        if ((int)threadIdx.x < nr) at = a.row_token ? a.row_token[r0 + threadIdx.x] : r0 + threadIdx.x;
-        sat[threadIdx.x] = at < a.tokens ? at : -1;
-    }
-    __syncthreads();
-    const uint8_t* w = a.qW + ((int64_t)e * a.N + n0 + c) * a.K;
-    const float* ws = a.sW + ((int64_t)e * (a.N / 128) + n0 / 128) * nkb;
-    float acc[kRows] = {};
-    for (int kb = 0; kb < nkb; kb++) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRows * 128; i += blockDim.x) {
-            const int64_t at = sat[i >> 7];
-            sx[i >> 7][i & 127] = at >= 0 ? e4m3_value(a.qA[at * a.K + kb * 128 + (i & 127)]) : 0.0f;
+__global__ void __launch_bounds__(THREADS, 1)
+moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmG,
+                const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY, const MoeGemmArgs a,
+                const int nt, const int splits) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bars = sbase + BAR_OFF;
+    volatile int4* info = reinterpret_cast<volatile int4*>(smem + INFO_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + BAR_OFF + BARS * 8);
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (STAGES + s); };
+    auto tfull = [&](int b) { return bars + 8 * (2 * STAGES + b); };
+    auto tempty = [&](int b) { return bars + 8 * (2 * STAGES + 2 + b); };
+    auto ifull = [&](int i) { return bars + 8 * (2 * STAGES + 4 + i); };
+    auto iempty = [&](int i) { return bars + 8 * (2 * STAGES + 4 + INFO + i); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nkb = a.K / BK;
+    const int rank = splits > 1 ? (int)cluster_rank() : 0;
+    const int kb0 = (int)((int64_t)nkb * rank / splits), kb1 = (int)((int64_t)nkb * (rank + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; s++) {
+            mbar_init(full(s), 2);                // the weights' and the rows' producer
+            mbar_init(empty(s), 1);
         }
-        if (threadIdx.x < kRows) ss[threadIdx.x] = sat[threadIdx.x] >= 0 ? a.sA[sat[threadIdx.x] * nkb + kb] : 0.0f;
-        __syncthreads();
-        float p[kRows] = {};
-        for (int k = 0; k < 128; k += 4) {
-            const uint32_t q = *reinterpret_cast<const uint32_t*>(w + kb * 128 + k);
-            for (int j = 0; j < 4; j++) {
-                const float v = e4m3_value(q >> (8 * j));
+        for (int b = 0; b < 2; b++) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), EPI_WARPS);
+        }
+        for (int i = 0; i < INFO; i++) {
+            mbar_init(ifull(i), 1);
+            mbar_init(iempty(i), 3 + EPI_WARPS);
+        }
+        fence_barrier_init();
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmG);
+        prefetch_tmap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+
+    // The next item (x < 0: no more); every warp but warp 3 takes each of them once.
+    uint32_t taken = 0;
+    auto next_item = [&](int4& it) {
+        const int i = taken % INFO;
+        if (!mbar_wait(ifull(i), (taken / INFO) & 1, &g_moe_err)) return false;
+        it.x = info[i].x;
+        it.y = info[i].y;
+        it.z = info[i].z;
+        it.w = info[i].w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty(i));
+        taken++;
+        return it.x >= 0;
+    };
+
+    if (warp < 4) {
+        reg_dec<REGS_FEED>();
+        int4 item;                                 // expert, first row, rows, column tile
+        if (warp == 0) {
+            // --------------------------------------------------------- weights
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && next_item(item)) {
+                const int n0 = item.x * a.N + item.w * (SWIGLU ? 128 : BN);
+                const bool two = SWIGLU || item.w * BN + 128 < a.N;
+                for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
+                    const int s = it % STAGES;
+                    ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
+                    if (ok && lane == 0) {
+                        const uint32_t dst = sbase + s * STAGE_BYTES + A_BYTES;
+                        mbar_arrive_expect_tx(full(s), two ? 2 * HALF_BYTES : HALF_BYTES);
+                        tma_load_2d(dst, &tmB, kb * BK, n0, full(s));
+                        if (two) tma_load_2d(dst + HALF_BYTES, &tmB, kb * BK, n0 + (SWIGLU ? a.N / 2 : 128), full(s));
+                    }
+                    __syncwarp();
+                }
+            }
+            // all copies into this CTA's shared memory have landed before it may exit
+            for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; j++)
+                mbar_wait(empty(j % STAGES), (j / STAGES) & 1, &g_moe_err);
+        } else if (warp == 1) {
+            // ------------------------------------------------------------- MMA
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && next_item(item)) {
+                const bool two = SWIGLU || item.w * BN + 128 < a.N;
+                const uint32_t idesc = two ? idesc_dense(0u, 0u, BM, BN) : idesc_dense(0u, 0u, BM, 128);
+                for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
+                    const int b = it & 1, s = it % STAGES;
+                    ok = mbar_wait(tempty(b), ((it >> 1) & 1) ^ 1, &g_moe_err) && mbar_wait(full(s), (it / STAGES) & 1, &g_moe_err);
+                    if (ok && lane == 0) {
+                        tc_fence_after();
+                        const uint64_t ad = sdesc_k_sw128(sbase + s * STAGE_BYTES);
+                        const uint64_t bd = sdesc_k_sw128(sbase + s * STAGE_BYTES + A_BYTES);
+                        const uint32_t d = tmem_base + b * BN;
 #pragma unroll
-                for (int r = 0; r < kRows; r++) p[r] = fmaf(sx[r][k + j], v, p[r]);
+                        for (int ks = 0; ks < BK / 32; ks++)                 // K = 32 bytes per MMA
+                            mma_f8f6f4(d, ad + (uint64_t)(ks * 2), bd + (uint64_t)(ks * 2), idesc, ks > 0);
+                        tc_commit(empty(s));
+                        tc_commit(tfull(b));
+                    }
+                    __syncwarp();
+                }
+            }
+            // the last accumulators are complete before tensor memory is released
+            if (it > 0) mbar_wait(tfull((it - 1) & 1), ((it - 1) >> 1) & 1, &g_moe_err);
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ rows
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && next_item(item)) {
+                const bool box = !a.row_token && item.z == BM;
+                const int groups = (item.z + 3) / 4;
+                // Rows of the tile behind its last one repeat it; a row whose token is not there is any row
+                // here, the promotion writes zeros for it.
+                int at[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int r = item.y + min(4 * lane + j, item.z - 1);
+                    const int t = a.row_token && !box ? a.row_token[r] : r;
+                    at[j] = t >= 0 && t < a.tokens ? t : 0;
+                }
+                const int4 rows = make_int4(at[0], at[1], at[2], at[3]);
+                for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
+                    const int s = it % STAGES;
+                    ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
+                    if (ok) {
+                        const uint32_t dst = sbase + s * STAGE_BYTES;
+                        if (lane == 0) mbar_arrive_expect_tx(full(s), box ? A_BYTES : groups * 512);
+                        __syncwarp();
+                        if (box) {
+                            if (lane == 0) tma_load_2d(dst, &tmA, kb * BK, item.y, full(s));
+                        } else if (lane < groups) {
+                            tma_gather4(dst + lane * 512, &tmG, kb * BK, rows, full(s));
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        } else {
+            // ----------------------------------------------------------- items
+            // lane l: the row tiles before expert l * per; an item of the list is row tile p of an
+            // expert's column tile n, p running first
+            const int per = (a.experts + 31) / 32, e0 = lane * per;
+            int mine = 0;
+            for (int j = 0; j < per && e0 + j < a.experts; j++) mine += row_tiles(expert_rows(a, e0 + j));
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const int64_t total = (int64_t)__shfl_sync(0xffffffffu, upto, 31) * nt;
+            const int64_t first = (int64_t)(upto - mine) * nt;
+            uint32_t n = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x / splits; ok; i += gridDim.x / splits, n++) {
+                int4 v = make_int4(-1, 0, 0, 0);
+                // a cluster has one item: more than the host's bound come from offsets that do not ascend
+                if (i < total && (splits == 1 || n == 0)) {
+                    // the lane whose experts hold the item, then the expert among them
+                    const uint32_t who = __ballot_sync(0xffffffffu, first <= i && mine > 0);
+                    const int l = 31 - __clz(who);
+                    const int64_t base = __shfl_sync(0xffffffffu, first, l);
+                    const int e = l * per + lane;
+                    const bool in = lane < per && e < a.experts;
+                    const int2 r = in ? expert_rows(a, e) : make_int2(0, 0);
+                    const int tiles = row_tiles(r);
+                    int before = tiles;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int u = __shfl_up_sync(0xffffffffu, before, o);
+                        if (lane >= o) before += u;
+                    }
+                    const int64_t at = i - base - (int64_t)(before - tiles) * nt;       // within this lane's expert
+                    const uint32_t mark = __ballot_sync(0xffffffffu, at >= 0 && at < (int64_t)tiles * nt);
+                    const int w = __ffs(mark) - 1;
+                    if (lane == w) {
+                        const int p = (int)(at % tiles);
+                        v = make_int4(e, r.x + p * BM, min(BM, r.y - r.x - p * BM), (int)(at / tiles));
+                    }
+                    v.x = __shfl_sync(0xffffffffu, v.x, w);
+                    v.y = __shfl_sync(0xffffffffu, v.y, w);
+                    v.z = __shfl_sync(0xffffffffu, v.z, w);
+                    v.w = __shfl_sync(0xffffffffu, v.w, w);
+                }
+                const int slot = n % INFO;
+                ok = mbar_wait(iempty(slot), ((n / INFO) & 1) ^ 1, &g_moe_err);
+                if (ok && lane == 0) {
+                    info[slot].x = v.x;
+                    info[slot].y = v.y;
+                    info[slot].z = v.z;
+                    info[slot].w = v.w;
+                    mbar_arrive(ifull(slot));
+                }
+                __syncwarp();
+                if (v.x < 0) break;
             }
         }
-#pragma unroll
-        for (int r = 0; r < kRows; r++) acc[r] = fmaf(p[r], ss[r] * ws[kb], acc[r]);
-    }
-    if constexpr (!SWIGLU) {
-        for (int r = 0; r < nr; r++) {
-            const __nv_bfloat16 y = __float2bfloat16_rn(acc[r]);
-            a.Y[(int64_t)(r0 + r) * a.N + n0 + c] = *reinterpret_cast<const uint16_t*>(&y);
+        if (splits > 1) {
+            cluster_sync();
+            cluster_sync();
         }
     } else {
-        __syncthreads();
-        if (half)
+        // ------------------------------------------------- promotion and output
+        reg_inc<REGS_EPI>();
+        const int q = warp & 3, h = (warp - 4) >> 2;          // lane quarter of tensor memory, half of each box
+        const int r = q * 32 + lane;                          // row of the tile
+        uint8_t* stg = smem + STG_OFF + (warp - 4) * STG_WARP;
+        uint32_t it = 0;
+        int done = 0;
+        bool ok = true, synced = false;
+        int4 item;
+        while (ok && next_item(item)) {
+            const bool active = q * 32 < item.z;              // some row of the warp exists
+            const int row = item.y + min(r, item.z - 1);
+            const int token = a.row_token ? a.row_token[row] : row;
+            const bool there = token >= 0 && token < a.tokens;
+            const bool two = SWIGLU || item.w * BN + 128 < a.N;
+            const float* sa = a.sA + (size_t)(there ? token : 0) * nkb;
+            const float* sw0 = a.sW + ((size_t)item.x * (a.N / 128) + (SWIGLU ? item.w : 2 * item.w)) * nkb;
+            const float* sw1 = two ? sw0 + (size_t)(SWIGLU ? a.N / 256 : 1) * nkb : sw0;
+            const bool vec = (nkb & 3) == 0 && (kb0 & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sA) & 15) == 0;
+            uint64_t acc[64];                                 // 64 columns of the first box, 64 of the second
 #pragma unroll
-            for (int r = 0; r < kRows; r++) sx[r][c] = acc[r];
-        __syncthreads();
-        float h[kRows];
-        if (!half)
+            for (int i = 0; i < 64; i++) acc[i] = 0ull;
+            // the next four blocks' row scales, the next block's weight scales
+            float4 na = make_float4(0.f, 0.f, 0.f, 0.f);
+            float nw0 = 0.f, nw1 = 0.f;
+            auto load4 = [&](int kb) {
+                if (!there || !active) return;
+                if (vec && kb + 4 <= kb1) {
+                    na = __ldg(reinterpret_cast<const float4*>(sa + kb));
+                } else {
+                    na.x = kb < kb1 ? __ldg(sa + kb) : 0.f;
+                    na.y = kb + 1 < kb1 ? __ldg(sa + kb + 1) : 0.f;
+                    na.z = kb + 2 < kb1 ? __ldg(sa + kb + 2) : 0.f;
+                    na.w = kb + 3 < kb1 ? __ldg(sa + kb + 3) : 0.f;
+                }
+            };
+            load4(kb0);
+            if (active) {
+                nw0 = __ldg(sw0 + kb0);
+                nw1 = __ldg(sw1 + kb0);
+            }
+            for (int kb4 = kb0; kb4 < kb1 && ok; kb4 += 4) {
+                const float4 ca = na;
+                load4(kb4 + 4);
 #pragma unroll
-            for (int r = 0; r < kRows; r++) h[r] = acc[r] / (1.0f + expf(-acc[r])) * sx[r][c];
-        __syncthreads();
-        if (!half)
+                for (int u = 0; u < 4; u++) {
+                    const int kb = kb4 + u;
+                    if (kb >= kb1 || !ok) break;
+                    const float c = u == 0 ? ca.x : u == 1 ? ca.y : u == 2 ? ca.z : ca.w;
+                    const uint64_t s0 = twice(c * nw0), s1 = twice(c * nw1);
+                    if (active && kb + 1 < kb1) {
+                        nw0 = __ldg(sw0 + kb + 1);
+                        nw1 = __ldg(sw1 + kb + 1);
+                    }
+                    const int b = it & 1;
+                    ok = mbar_wait(tfull(b), (it >> 1) & 1, &g_moe_err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (active) {
+                        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * BN + h * 64;
+                        uint32_t x[32], y[32];
+                        tmem_ld32(t, x);
+                        tmem_arrived(x);
+                        tmem_ld32(t + 32, y);
 #pragma unroll
-            for (int r = 0; r < kRows; r++) sx[r][c] = h[r];
-        __syncthreads();
-        if (half) return;
-        const int I = a.N / 2;
-        for (int r = 0; r < nr; r++) {
-            float am = 0.0f;
-            for (int i = 0; i < 128; i++) am = fmaxf(am, fabsf(sx[r][i]));
-            const float sc = div1(fmaxf(am, kAmaxMin), Recip(kFp8Max));
-            const float v = sx[r][c];
-            a.codes[(int64_t)(r0 + r) * I + n0 + c] = (uint8_t)e4m3_code(sign_of(div1(v, Recip(sc)), v));
-            if (c == 0) a.scales[(int64_t)(r0 + r) * (I / 128) + n0 / 128] = sc;
+                        for (int i = 0; i < 16; i++) fma2(acc[i], x[2 * i], x[2 * i + 1], s0);
+                        tmem_arrived(y);
+                        tmem_ld32(t + 128, x);
+#pragma unroll
+                        for (int i = 0; i < 16; i++) fma2(acc[16 + i], y[2 * i], y[2 * i + 1], s0);
+                        tmem_arrived(x);
+                        tmem_ld32(t + 160, y);
+#pragma unroll
+                        for (int i = 0; i < 16; i++) fma2(acc[32 + i], x[2 * i], x[2 * i + 1], s1);
+                        tmem_arrived(y);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(tempty(b));            // all of it is in registers
+#pragma unroll
+                        for (int i = 0; i < 16; i++) fma2(acc[48 + i], y[2 * i], y[2 * i + 1], s1);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(tempty(b));
+                    }
+                    it++;
+                }
+            }
+            if (!ok) break;
+            if (splits > 1) {
+                // the sums of an item's parts meet in rank 0, in the order of the ranks
+                cluster_sync();                               // its ring is free
+                const uint32_t mine = sbase + ((h * 32) * 32 + lane) * 16;
+                if (rank > 0 && q == 0) {
+                    uint32_t dst;
+                    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(mine + (rank - 1) * PART_BYTES));
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(dst + i * 512), "l"(acc[2 * i]), "l"(acc[2 * i + 1]) : "memory");
+                }
+                cluster_sync();
+                synced = true;
+                if (rank > 0) break;
+                if (q == 0)
+                    for (int p = 0; p < splits - 1; p++)
+#pragma unroll
+                        for (int i = 0; i < 32; i++) {
+                            const float4 v = *reinterpret_cast<const float4*>(smem + ((h * 32) * 32 + lane) * 16 + p * PART_BYTES + i * 512);
+                            acc[2 * i] = ((uint64_t)__float_as_uint(hi(acc[2 * i]) + v.y) << 32) | __float_as_uint(lo(acc[2 * i]) + v.x);
+                            acc[2 * i + 1] = ((uint64_t)__float_as_uint(hi(acc[2 * i + 1]) + v.w) << 32) | __float_as_uint(lo(acc[2 * i + 1]) + v.z);
+                        }
+            }
+            if (!there) {
+#pragma unroll
+                for (int i = 0; i < 64; i++) acc[i] = 0ull;
+            }
+            const size_t out = (size_t)(item.y + r);
+            if constexpr (SWIGLU) {
+                // column i of h: gate acc[i / 2], up acc[32 + i / 2]; a scale's 128 columns lie in two threads
+                float* peak = reinterpret_cast<float*>(smem + STG_OFF) + (done & 1) * 256;
+                float am = 0.0f;
+                if (active) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const float g0 = lo(acc[i]), g1 = hi(acc[i]);
+                        const float h0 = g0 / (1.0f + expf(-g0)) * lo(acc[32 + i]), h1 = g1 / (1.0f + expf(-g1)) * hi(acc[32 + i]);
+                        am = fmaxf(am, fmaxf(fabsf(h0), fabsf(h1)));
+                        acc[i] = ((uint64_t)__float_as_uint(h1) << 32) | __float_as_uint(h0);
+                    }
+                }
+                peak[h * 128 + r] = am;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (r < item.z) {
+                    const float sc = div1(fmaxf(fmaxf(am, peak[(h ^ 1) * 128 + r]), kAmaxMin), Recip(kFp8Max));
+                    const Recip d(sc);
+                    const int I = a.N / 2;
+                    uint4* codes = reinterpret_cast<uint4*>(a.codes + out * I + item.w * 128 + h * 64);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        uint32_t p[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const float v = lo(acc[8 * j + e]), w = hi(acc[8 * j + e]);
+                            p[e] = e4m3x2(sign_of(div1(v, d), v), sign_of(div1(w, d), w));
+                        }
+                        codes[j] = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                                              __byte_perm(p[4], p[5], 0x5410), __byte_perm(p[6], p[7], 0x5410));
+                    }
+                    if (h == 0) a.scales[out * (I / 128) + item.w] = sc;
+                }
+                done++;
+            } else if (active) {
+#pragma unroll
+                for (int s = 0; s < 2; s++) {
+                    if (s == 1 && !two) break;
+                    const int c0 = item.w * BN + s * 128 + h * 64;
+                    if (lane == 0) bulk_wait_read0();                     // the previous store has read the block
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const uint64_t v = acc[s * 32 + j * 4 + e];
+                            const __nv_bfloat162 p = __floats2bfloat162_rn(lo(v), hi(v));
+                            w[e] = *reinterpret_cast<const uint32_t*>(&p);
+                        }
+                        *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (q * 32 + 32 <= item.z) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tma_store_2d(&tmY, smem_u32(stg), c0, item.y + q * 32);
+                    } else {
+                        // the tile's last rows: what lies behind them is another expert's
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const int rr = 4 * j + (lane >> 3), ch = lane & 7;
+                            if (q * 32 + rr < item.z)
+                                *reinterpret_cast<uint4*>(a.Y + (size_t)(item.y + q * 32 + rr) * a.N + c0 + ch * 8) =
+                                    *reinterpret_cast<const uint4*>(stg + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
         }
+        if (!SWIGLU && lane == 0) bulk_wait_all0();           // stores complete before the CTA exits
+        __syncwarp();
+        if (splits > 1 && !synced) {
+            cluster_sync();
+            cluster_sync();
+        }
+    }
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
 } // namespace
 
+qz_status moe_gemm_error_read_and_clear() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_moe_err, sizeof(v)) != cudaSuccess) return QZ_ERR_CUDA;
+    if (v && cudaMemcpyToSymbol(g_moe_err, &z, sizeof(z)) != cudaSuccess) return QZ_ERR_CUDA;
+    return v ? QZ_ERR_TIMEOUT : QZ_OK;
+}
+
 qz_status moe_gemm_fp8_launch(const MoeGemmArgs& a, cudaStream_t st) {
-    const int64_t tiles = a.rows / kRows + (a.rows < a.experts ? a.rows : a.experts);
-    if (a.Y) return launch_pdl(moe_gemm_kernel<false>, dim3(a.N / 128, (unsigned)tiles), dim3(128), 0, st, a);
-    return launch_pdl(moe_gemm_kernel<true>, dim3(a.N / 256, (unsigned)tiles), dim3(256), 0, st, a);
+    CUtensorMap ta, tg, tb, ty;
+    // without tokens every row is one of zeros: nothing that the maps of the rows reach is used
+    const void* rows = a.tokens ? a.qA : a.qW;
+    const uint64_t tokens = a.tokens ? (uint64_t)a.tokens : 1, K = (uint64_t)a.K;
+    if (!encode_tmap_2d_u8(&ta, rows, K, tokens, K, BK, BM) || !encode_tmap_2d_u8(&tg, rows, K, tokens, K, BK, 1) ||
+        !encode_tmap_2d_u8(&tb, a.qW, K, (uint64_t)a.experts * a.N, K, BK, 128))
+        return QZ_ERR_CUDA;
+    memset(&ty, 0, sizeof(ty));                   // SwiGLU's codes are stored without TMA
+    if (a.Y && !encode_tmap_2d_swz(&ty, a.Y, 2, (uint64_t)a.N, (uint64_t)a.rows, (uint64_t)a.N * 2, 64, 32, 128))
+        return QZ_ERR_CUDA;
+    const int nt = a.Y ? (a.N + BN - 1) / BN : a.N / 256;
+    const int64_t items = (a.rows / BM + std::min<int64_t>(a.experts, a.rows)) * nt;       // at most
+    const int sms = num_sms(), nkb = a.K / BK;
+    int splits = 1;
+    while (a.rows <= SPLIT_ROWS && splits < MAX_SPLITS && 2 * splits * items <= sms && nkb >= 4 * splits) splits *= 2;
+    const int grid = splits > 1 ? (int)items * splits : (int)std::min<int64_t>(items, sms);
+    const void* fn = a.Y ? (const void*)moe_gemm_kernel<false> : (const void*)moe_gemm_kernel<true>;
+    QZ_TRY(opt_in_smem(fn, SMEM_BYTES));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t r = a.Y ? cudaLaunchKernelEx(&cfg, moe_gemm_kernel<false>, ta, tg, tb, ty, a, nt, splits)
+                              : cudaLaunchKernelEx(&cfg, moe_gemm_kernel<true>, ta, tg, tb, ty, a, nt, splits);
+    return r == cudaSuccess ? launch_status() : QZ_ERR_CUDA;
 }
 
 } // namespace qz

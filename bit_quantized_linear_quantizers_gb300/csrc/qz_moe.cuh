@@ -39,6 +39,7 @@ struct MoeGemmArgs {
     int N, K;
 };
 qz_status moe_gemm_fp8_launch(const MoeGemmArgs& a, cudaStream_t st);
+qz_status moe_gemm_error_read_and_clear();
 
 struct NormArgs {
     const void* x;
