@@ -13,16 +13,18 @@
 //  warp 0     weights: TMA boxes of 128 x 128 bytes into a 4-stage ring
 //  warp 1     MMA: per block of 128 of K four tcgen05.mma (M 128, N 256, K 32) into one of two
 //             accumulators of 256 columns in tensor memory
-//  warp 2     rows: gathered by their tokens, four a copy (gather4), a lane for each four; as
-//             one box where a tile is full and in order
-//  warp 3     items
+//  warp 2     rows: gathered by their tokens in copies of 16 bytes (cp.async), as TMA boxes of 32 rows where
+//             they lie in order. (Gathered by TMA, four rows a copy, a block of 128 rows took 2400 cycles.) The
+//             copies arrive on the stage's barrier by themselves, and the MMA's thread orders them
+//             before its own reads.
+//  warp 3     items, and the block scales of an accumulator's rows and columns into shared memory
 //  warps 4-11 promotion: block scales are fp32, so every block's partial sums leave tensor
 //             memory to be added as acc += P_kb * (sA sW). A thread holds one row of 64 columns of
 //             each of the two boxes.
 // What bounds it with many rows is the cycle of an accumulator: MMA 512 cycles, hand-off, promotion,
-// hand-off, for two blocks of K by turns. So a promotion is kept short: 224 registers a
-// thread (the other warps give theirs up) hold the 128 sums and two 32-column reads, one in
-// flight while the other is added, and scales are read four blocks at a time.
+// hand-off, for two blocks of K by turns. So a promotion is kept short: REGS_EPI registers a
+// thread (the other warps give theirs up) hold the 128 sums and two reads of 32 columns; the scales lie
+// ready when the accumulator does.
 // With few rows the bound is the weights' way from memory, and the promotion and the gather of rows that
 // are not there are left out. Where items are fewer than SMs (rows <= 32), a cluster shares an item's K.
 #include "qz_moe.cuh"
@@ -46,7 +48,10 @@ constexpr int INFO = 4;                           // items in flight
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int STG_WARP = 32 * 128;                // a warp's output: 32 rows of 64 bf16
 constexpr int STG_OFF = STAGES * STAGE_BYTES;
-constexpr int INFO_OFF = STG_OFF + EPI_WARPS * STG_WARP;
+constexpr int SCALE_OFF = STG_OFF + EPI_WARPS * STG_WARP;
+constexpr int SCALE_BYTES = BM * 4 + 16;          // an accumulator's row scales, then its two boxes'
+constexpr int ROW_OFF = SCALE_OFF + 2 * SCALE_BYTES;
+constexpr int INFO_OFF = ROW_OFF + BM * 4;
 constexpr int BAR_OFF = INFO_OFF + INFO * 16;
 constexpr int BARS = 2 * STAGES + 4 + 2 * INFO;
 constexpr int SMEM_BYTES = BAR_OFF + BARS * 8 + 16 + 1024;
@@ -69,19 +74,23 @@ __device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float((uint32
 __device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // The reads in flight have arrived; the registers pass through, so that no use of them moves before it.
-__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+#define QZ_R32(r)                                                                                                       \
+    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), \
+    "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),    \
+    "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),    \
+    "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+__device__ __forceinline__ void tmem_arrived(uint32_t (&x)[32], uint32_t (&y)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QZ_R32(x)::"memory");
+    asm volatile("" : QZ_R32(y)::"memory");
 }
+#undef QZ_R32
 
-// Four rows (their first coordinate x) of a tensor whose map has a box one row high.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int x, int4 rows, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                 ::"r"(dst), "l"(tmap), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
+}
+// An arrival on `bar` (one of those it counts) once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -103,8 +112,8 @@ __device__ __forceinline__ int row_tiles(int2 r) { return (r.y - r.x) / BM + ((r
 // nt: column tiles of an expert. splits: CTAs (a cluster) that share an item's blocks of K.
 template <bool SWIGLU>
 __global__ void __launch_bounds__(THREADS, 1)
-moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmG,
-                const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmY, const MoeGemmArgs a,
+moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ MoeGemmArgs a,
                 const int nt, const int splits) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -126,11 +135,11 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
-            mbar_init(full(s), 2);                // the weights' and the rows' producer
+            mbar_init(full(s), a.row_token ? 33 : 2);     // the weights' producer and the rows': a thread, or 32 that copy
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; b++) {
-            mbar_init(tfull(b), 1);
+            mbar_init(tfull(b), 2);               // the MMAs and the scales
             mbar_init(tempty(b), EPI_WARPS);
         }
         for (int i = 0; i < INFO; i++) {
@@ -139,7 +148,6 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         fence_barrier_init();
         prefetch_tmap(&tmA);
-        prefetch_tmap(&tmG);
         prefetch_tmap(&tmB);
     }
     if (warp == 1) {
@@ -199,10 +207,15 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             while (ok && next_item(item)) {
                 const bool two = SWIGLU || item.w * BN + 128 < a.N;
                 const uint32_t idesc = two ? idesc_dense(0u, 0u, BM, BN) : idesc_dense(0u, 0u, BM, 128);
-                for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
-                    const int b = it & 1, s = it % STAGES;
-                    ok = mbar_wait(tempty(b), ((it >> 1) & 1) ^ 1, &g_moe_err) && mbar_wait(full(s), (it / STAGES) & 1, &g_moe_err);
-                    if (ok && lane == 0) {
+                if (lane == 0) {
+                    uint32_t i = it;
+                    for (int kb = kb0; kb < kb1; kb++, i++) {
+                        const int b = i & 1, s = i % STAGES;
+                        if (!mbar_wait(full(s), (i / STAGES) & 1, &g_moe_err) || !mbar_wait(tempty(b), ((i >> 1) & 1) ^ 1, &g_moe_err)) {
+                            ok = false;
+                            break;
+                        }
+                        if (a.row_token) fence_proxy_async_smem();           // the gathered rows came by the generic proxy
                         tc_fence_after();
                         const uint64_t ad = sdesc_k_sw128(sbase + s * STAGE_BYTES);
                         const uint64_t bd = sdesc_k_sw128(sbase + s * STAGE_BYTES + A_BYTES);
@@ -213,42 +226,60 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         tc_commit(empty(s));
                         tc_commit(tfull(b));
                     }
-                    __syncwarp();
+                    it = i;
                 }
+                it = __shfl_sync(0xffffffffu, it, 0);
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             }
             // the last accumulators are complete before tensor memory is released
             if (it > 0) mbar_wait(tfull((it - 1) & 1), ((it - 1) >> 1) & 1, &g_moe_err);
         } else if (warp == 2) {
             // ------------------------------------------------------------ rows
+            int* at = reinterpret_cast<int*>(smem + ROW_OFF);  // the tile's rows in qA
             uint32_t it = 0;
             bool ok = true;
             while (ok && next_item(item)) {
-                const bool box = !a.row_token && item.z == BM;
-                const int groups = (item.z + 3) / 4;
-                // Rows of the tile behind its last one repeat it; a row whose token is not there is any row
-                // here, the promotion writes zeros for it.
-                int at[4];
+                if (!a.row_token) {
+                    const int boxes = (item.z + 31) / 32;
+                    for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
+                        const int s = it % STAGES;
+                        ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
+                        if (ok && lane == 0) mbar_arrive_expect_tx(full(s), boxes * 32 * BK);
+                        __syncwarp();
+                        if (ok && lane < boxes) tma_load_2d(sbase + s * STAGE_BYTES + lane * 32 * BK, &tmA, kb * BK, item.y + 32 * lane, full(s));
+                    }
+                    continue;
+                }
+                // Lane l copies chunk l % 8 of rows l / 8, l / 8 + 4, ... A row whose token is not there is any
+                // row here, the promotion writes zeros for it.
+                const int c = lane & 7, steps = (item.z + 3) / 4;
+                __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const int r = item.y + min(4 * lane + j, item.z - 1);
-                    const int t = a.row_token && !box ? a.row_token[r] : r;
-                    at[j] = t >= 0 && t < a.tokens ? t : 0;
+                    const int r = 32 * j + lane, tok = r < item.z ? a.row_token[item.y + r] : 0;
+                    at[(r & 3) * 32 + (r >> 2)] = tok >= 0 && tok < a.tokens ? tok : 0;
                 }
-                const int4 rows = make_int4(at[0], at[1], at[2], at[3]);
+                __syncwarp();
+                const uint8_t* src = (a.tokens ? a.qA : a.qW) + 16 * c;
                 for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
                     const int s = it % STAGES;
                     ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
-                    if (ok) {
-                        const uint32_t dst = sbase + s * STAGE_BYTES;
-                        if (lane == 0) mbar_arrive_expect_tx(full(s), box ? A_BYTES : groups * 512);
-                        __syncwarp();
-                        if (box) {
-                            if (lane == 0) tma_load_2d(dst, &tmA, kb * BK, item.y, full(s));
-                        } else if (lane < groups) {
-                            tma_gather4(dst + lane * 512, &tmG, kb * BK, rows, full(s));
-                        }
+                    if (!ok) break;
+                    const uint32_t dst = sbase + s * STAGE_BYTES + (lane >> 3) * BK;
+                    const uint8_t* from = src + kb * BK;
+                    // swizzle of row 4 j + l / 8: its lowest three bits are those of an even or an odd j
+                    const uint32_t even = (c ^ (lane >> 3)) << 4, odd = (c ^ (4 + (lane >> 3))) << 4;
+#pragma unroll 1
+                    for (int j = 0; j < steps; j += 8) {
+                        int4 tok[2];
+                        tok[0] = *reinterpret_cast<const int4*>(at + (lane >> 3) * 32 + j);
+                        tok[1] = *reinterpret_cast<const int4*>(at + (lane >> 3) * 32 + j + 4);
+                        const int* k = reinterpret_cast<const int*>(tok);
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            if (j + i < steps) cp_async16(dst + 4 * (j + i) * BK + (i & 1 ? odd : even), from + (int64_t)k[i] * a.K);
                     }
-                    __syncwarp();
+                    cp_async_arrive(full(s));
                 }
             }
         } else {
@@ -267,9 +298,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int64_t total = (int64_t)__shfl_sync(0xffffffffu, upto, 31) * nt;
             const int64_t first = (int64_t)(upto - mine) * nt;
             uint32_t n = 0;
-            bool ok = true;
-            for (int64_t i = blockIdx.x / splits; ok; i += gridDim.x / splits, n++) {
-                int4 v = make_int4(-1, 0, 0, 0);
+            // the n-th item of this CTA, into the ring; x < 0: there is none
+            auto hand_out = [&](int4& v) {
+                const int64_t i = blockIdx.x / splits + (int64_t)n * (gridDim.x / splits);
+                v = make_int4(-1, 0, 0, 0);
                 // a cluster has one item: more than the host's bound come from offsets that do not ascend
                 if (i < total && (splits == 1 || n == 0)) {
                     // the lane whose experts hold the item, then the expert among them
@@ -277,8 +309,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const int l = 31 - __clz(who);
                     const int64_t base = __shfl_sync(0xffffffffu, first, l);
                     const int e = l * per + lane;
-                    const bool in = lane < per && e < a.experts;
-                    const int2 r = in ? expert_rows(a, e) : make_int2(0, 0);
+                    const int2 r = lane < per && e < a.experts ? expert_rows(a, e) : make_int2(0, 0);
                     const int tiles = row_tiles(r);
                     int before = tiles;
 #pragma unroll
@@ -287,8 +318,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         if (lane >= o) before += u;
                     }
                     const int64_t at = i - base - (int64_t)(before - tiles) * nt;       // within this lane's expert
-                    const uint32_t mark = __ballot_sync(0xffffffffu, at >= 0 && at < (int64_t)tiles * nt);
-                    const int w = __ffs(mark) - 1;
+                    const int w = __ffs(__ballot_sync(0xffffffffu, at >= 0 && at < (int64_t)tiles * nt)) - 1;
                     if (lane == w) {
                         const int p = (int)(at % tiles);
                         v = make_int4(e, r.x + p * BM, min(BM, r.y - r.x - p * BM), (int)(at / tiles));
@@ -299,8 +329,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     v.w = __shfl_sync(0xffffffffu, v.w, w);
                 }
                 const int slot = n % INFO;
-                ok = mbar_wait(iempty(slot), ((n / INFO) & 1) ^ 1, &g_moe_err);
-                if (ok && lane == 0) {
+                if (!mbar_wait(iempty(slot), ((n / INFO) & 1) ^ 1, &g_moe_err)) return false;
+                if (lane == 0) {
                     info[slot].x = v.x;
                     info[slot].y = v.y;
                     info[slot].z = v.z;
@@ -308,7 +338,58 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     mbar_arrive(ifull(slot));
                 }
                 __syncwarp();
-                if (v.x < 0) break;
+                n++;
+                return true;
+            };
+            int4 next;
+            bool ok = hand_out(item) && (item.x < 0 || hand_out(next));
+            uint32_t it = 0;
+            while (ok && item.x >= 0) {
+                // lane l: the scales of rows l, l + 32, l + 64 and l + 96; four blocks of K a read where they are aligned
+                const bool two = SWIGLU || item.w * BN + 128 < a.N;
+                const float* sw = a.sW + ((size_t)item.x * (a.N / 128) + (SWIGLU ? item.w : 2 * item.w)) * nkb;
+                if (lane == 1 && two) sw += (size_t)(SWIGLU ? a.N / 256 : 1) * nkb;
+                const float* sa[4];
+                bool there[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int r = 32 * j + lane;
+                    const int tok = r >= item.z ? -1 : a.row_token ? a.row_token[item.y + r] : item.y + r;
+                    there[j] = tok >= 0 && tok < a.tokens;
+                    sa[j] = a.sA + (size_t)(there[j] ? tok : 0) * nkb;
+                }
+                const bool vec = ((nkb | kb0) & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sA) & 15) == 0;
+                for (int kb4 = kb0; kb4 < kb1 && ok; kb4 += 4) {
+                    float c[4][4], w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        if (vec && kb4 + 4 <= kb1 && there[j]) {
+                            *reinterpret_cast<float4*>(c[j]) = __ldg(reinterpret_cast<const float4*>(sa[j] + kb4));
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 4; u++) c[j][u] = there[j] && kb4 + u < kb1 ? __ldg(sa[j] + kb4 + u) : 0.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; u++) w[u] = lane < 2 && kb4 + u < kb1 ? __ldg(sw + kb4 + u) : 0.0f;
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        if (kb4 + u >= kb1) break;
+                        const int b = it & 1;
+                        ok = mbar_wait(tempty(b), ((it >> 1) & 1) ^ 1, &g_moe_err);
+                        if (!ok) break;
+                        float* s = reinterpret_cast<float*>(smem + SCALE_OFF + b * SCALE_BYTES);
+#pragma unroll
+                        for (int j = 0; j < 4; j++) s[32 * j + lane] = c[j][u];
+                        if (lane < 2) s[BM + lane] = w[u];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(tfull(b));
+                        it++;
+                    }
+                }
+                if (!ok) break;
+                item = next;
+                if (item.x >= 0) ok = hand_out(next);
             }
         }
         if (splits > 1) {
@@ -327,81 +408,43 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int4 item;
         while (ok && next_item(item)) {
             const bool active = q * 32 < item.z;              // some row of the warp exists
-            const int row = item.y + min(r, item.z - 1);
-            const int token = a.row_token ? a.row_token[row] : row;
-            const bool there = token >= 0 && token < a.tokens;
             const bool two = SWIGLU || item.w * BN + 128 < a.N;
-            const float* sa = a.sA + (size_t)(there ? token : 0) * nkb;
-            const float* sw0 = a.sW + ((size_t)item.x * (a.N / 128) + (SWIGLU ? item.w : 2 * item.w)) * nkb;
-            const float* sw1 = two ? sw0 + (size_t)(SWIGLU ? a.N / 256 : 1) * nkb : sw0;
-            const bool vec = (nkb & 3) == 0 && (kb0 & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sA) & 15) == 0;
             uint64_t acc[64];                                 // 64 columns of the first box, 64 of the second
 #pragma unroll
             for (int i = 0; i < 64; i++) acc[i] = 0ull;
-            // the next four blocks' row scales, the next block's weight scales
-            float4 na = make_float4(0.f, 0.f, 0.f, 0.f);
-            float nw0 = 0.f, nw1 = 0.f;
-            auto load4 = [&](int kb) {
-                if (!there || !active) return;
-                if (vec && kb + 4 <= kb1) {
-                    na = __ldg(reinterpret_cast<const float4*>(sa + kb));
+            for (int kb = kb0; kb < kb1; kb++, it++) {
+                const int b = it & 1;
+                ok = mbar_wait(tfull(b), (it >> 1) & 1, &g_moe_err);
+                if (!ok) break;
+                tc_fence_after();
+                if (active) {
+                    const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * BN + h * 64;
+                    uint32_t x[32], y[32];
+                    tmem_ld32(t, x);
+                    tmem_ld32(t + 32, y);
+                    const float* s = reinterpret_cast<const float*>(smem + SCALE_OFF + b * SCALE_BYTES);
+                    const float c = s[r];
+                    const float2 w = *reinterpret_cast<const float2*>(s + BM);
+                    const uint64_t s0 = twice(c * w.x), s1 = twice(c * w.y);
+                    tmem_arrived(x, y);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) fma2(acc[i], x[2 * i], x[2 * i + 1], s0);
+                    tmem_ld32(t + 128, x);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) fma2(acc[16 + i], y[2 * i], y[2 * i + 1], s0);
+                    tmem_ld32(t + 160, y);
+                    tmem_arrived(x, y);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty(b));                // all of it is in registers
+#pragma unroll
+                    for (int i = 0; i < 16; i++) fma2(acc[32 + i], x[2 * i], x[2 * i + 1], s1);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) fma2(acc[48 + i], y[2 * i], y[2 * i + 1], s1);
                 } else {
-                    na.x = kb < kb1 ? __ldg(sa + kb) : 0.f;
-                    na.y = kb + 1 < kb1 ? __ldg(sa + kb + 1) : 0.f;
-                    na.z = kb + 2 < kb1 ? __ldg(sa + kb + 2) : 0.f;
-                    na.w = kb + 3 < kb1 ? __ldg(sa + kb + 3) : 0.f;
-                }
-            };
-            load4(kb0);
-            if (active) {
-                nw0 = __ldg(sw0 + kb0);
-                nw1 = __ldg(sw1 + kb0);
-            }
-            for (int kb4 = kb0; kb4 < kb1 && ok; kb4 += 4) {
-                const float4 ca = na;
-                load4(kb4 + 4);
-#pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const int kb = kb4 + u;
-                    if (kb >= kb1 || !ok) break;
-                    const float c = u == 0 ? ca.x : u == 1 ? ca.y : u == 2 ? ca.z : ca.w;
-                    const uint64_t s0 = twice(c * nw0), s1 = twice(c * nw1);
-                    if (active && kb + 1 < kb1) {
-                        nw0 = __ldg(sw0 + kb + 1);
-                        nw1 = __ldg(sw1 + kb + 1);
-                    }
-                    const int b = it & 1;
-                    ok = mbar_wait(tfull(b), (it >> 1) & 1, &g_moe_err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (active) {
-                        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * BN + h * 64;
-                        uint32_t x[32], y[32];
-                        tmem_ld32(t, x);
-                        tmem_arrived(x);
-                        tmem_ld32(t + 32, y);
-#pragma unroll
-                        for (int i = 0; i < 16; i++) fma2(acc[i], x[2 * i], x[2 * i + 1], s0);
-                        tmem_arrived(y);
-                        tmem_ld32(t + 128, x);
-#pragma unroll
-                        for (int i = 0; i < 16; i++) fma2(acc[16 + i], y[2 * i], y[2 * i + 1], s0);
-                        tmem_arrived(x);
-                        tmem_ld32(t + 160, y);
-#pragma unroll
-                        for (int i = 0; i < 16; i++) fma2(acc[32 + i], x[2 * i], x[2 * i + 1], s1);
-                        tmem_arrived(y);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(tempty(b));            // all of it is in registers
-#pragma unroll
-                        for (int i = 0; i < 16; i++) fma2(acc[48 + i], y[2 * i], y[2 * i + 1], s1);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(tempty(b));
-                    }
-                    it++;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty(b));
                 }
             }
             if (!ok) break;
@@ -428,7 +471,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             acc[2 * i + 1] = ((uint64_t)__float_as_uint(hi(acc[2 * i + 1]) + v.w) << 32) | __float_as_uint(lo(acc[2 * i + 1]) + v.z);
                         }
             }
-            if (!there) {
+            // a row whose token is not there was multiplied by 0, but what it was may be NaN
+            const int row = item.y + min(r, item.z - 1);
+            const int token = a.row_token ? a.row_token[row] : row;
+            if (token < 0 || token >= a.tokens) {
 #pragma unroll
                 for (int i = 0; i < 64; i++) acc[i] = 0ull;
             }
@@ -441,7 +487,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
                         const float g0 = lo(acc[i]), g1 = hi(acc[i]);
-                        const float h0 = g0 / (1.0f + expf(-g0)) * lo(acc[32 + i]), h1 = g1 / (1.0f + expf(-g1)) * hi(acc[32 + i]);
+                        const float h0 = __fdividef(g0, 1.0f + __expf(-g0)) * lo(acc[32 + i]), h1 = __fdividef(g1, 1.0f + __expf(-g1)) * hi(acc[32 + i]);
                         am = fmaxf(am, fmaxf(fabsf(h0), fabsf(h1)));
                         acc[i] = ((uint64_t)__float_as_uint(h1) << 32) | __float_as_uint(h0);
                     }
@@ -530,11 +576,11 @@ qz_status moe_gemm_error_read_and_clear() {
 }
 
 qz_status moe_gemm_fp8_launch(const MoeGemmArgs& a, cudaStream_t st) {
-    CUtensorMap ta, tg, tb, ty;
-    // without tokens every row is one of zeros: nothing that the maps of the rows reach is used
+    CUtensorMap ta, tb, ty;
+    // without tokens every row is one of zeros: what the map of the rows reaches is not used
     const void* rows = a.tokens ? a.qA : a.qW;
     const uint64_t tokens = a.tokens ? (uint64_t)a.tokens : 1, K = (uint64_t)a.K;
-    if (!encode_tmap_2d_u8(&ta, rows, K, tokens, K, BK, BM) || !encode_tmap_2d_u8(&tg, rows, K, tokens, K, BK, 1) ||
+    if (!encode_tmap_2d_u8(&ta, rows, K, tokens, K, BK, 32) ||
         !encode_tmap_2d_u8(&tb, a.qW, K, (uint64_t)a.experts * a.N, K, BK, 128))
         return QZ_ERR_CUDA;
     memset(&ty, 0, sizeof(ty));                   // SwiGLU's codes are stored without TMA
@@ -561,8 +607,8 @@ qz_status moe_gemm_fp8_launch(const MoeGemmArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t r = a.Y ? cudaLaunchKernelEx(&cfg, moe_gemm_kernel<false>, ta, tg, tb, ty, a, nt, splits)
-                              : cudaLaunchKernelEx(&cfg, moe_gemm_kernel<true>, ta, tg, tb, ty, a, nt, splits);
+    const cudaError_t r = a.Y ? cudaLaunchKernelEx(&cfg, moe_gemm_kernel<false>, ta, tb, ty, a, nt, splits)
+                              : cudaLaunchKernelEx(&cfg, moe_gemm_kernel<true>, ta, tb, ty, a, nt, splits);
     return r == cudaSuccess ? launch_status() : QZ_ERR_CUDA;
 }
 
