@@ -10,13 +10,12 @@
 // so that the CTAs of one moment share weights and rows in L2.
 //
 // CTA of 12 warps, one per SM:
-//  warp 0     weights: TMA boxes of 128 x 128 bytes into a 4-stage ring
+//  warps 0, 2 weights: TMA boxes of 128 x 128 bytes into a 4-stage ring; rows: gathered by their tokens in copies of
+//             16 bytes (cp.async), or TMA boxes of 32 rows where they lie in order. (Gathered by TMA, four rows
+//             a copy, a block of 128 rows took 2400 cycles; by one warp's copies 1900.) The copies arrive on the
+//             stage's barrier by themselves, and the MMA's thread orders them before its own reads.
 //  warp 1     MMA: per block of 128 of K four tcgen05.mma (M 128, N 256, K 32) into one of two
 //             accumulators of 256 columns in tensor memory
-//  warp 2     rows: gathered by their tokens in copies of 16 bytes (cp.async), as TMA boxes of 32 rows where
-//             they lie in order. (Gathered by TMA, four rows a copy, a block of 128 rows took 2400 cycles.) The
-//             copies arrive on the stage's barrier by themselves, and the MMA's thread orders them
-//             before its own reads.
 //  warp 3     items, and the block scales of an accumulator's rows and columns into shared memory
 //  warps 4-11 promotion: block scales are fp32, so every block's partial sums leave tensor
 //             memory to be added as acc += P_kb * (sA sW). A thread holds one row of 64 columns of
@@ -63,27 +62,30 @@ static_assert((MAX_SPLITS - 1) * PART_BYTES <= STAGES * STAGE_BYTES, "the others
 template <int REGS> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
 template <int REGS> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 
-// acc (two fp32 lanes) += v * s per lane, each lane one correctly rounded fma.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s2) {
-    asm("{ .reg .b64 t; mov.b64 t, {%1, %2}; fma.rn.f32x2 %0, t, %3, %0; }" : "+l"(acc) : "r"(v0), "r"(v1), "l"(s2));
+// acc += v * s. Volatile: it stays behind the wait for the reads of v. One lane an instruction: paired (fma.rn.f32x2),
+// with no register to spare, every pair of reads was moved into place first, and 32 pairs took 370 cycles.
+__device__ __forceinline__ void fma1(float& acc, uint32_t v, float s) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
 }
-__device__ __forceinline__ uint64_t twice(float v) {
-    return ((uint64_t)__float_as_uint(v) << 32) | __float_as_uint(v);
-}
-__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
-// The reads in flight have arrived; the registers pass through, so that no use of them moves before it.
-#define QZ_R32(r)                                                                                                       \
-    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), \
-    "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),    \
-    "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),    \
-    "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-__device__ __forceinline__ void tmem_arrived(uint32_t (&x)[32], uint32_t (&y)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : QZ_R32(x)::"memory");
-    asm volatile("" : QZ_R32(y)::"memory");
+// One block of K: D = A B^T of 128 x 128-byte and 256 x 128-byte tiles behind one another at `stage`, K = 32 bytes an
+// MMA, then arrivals on two barriers. The warp issues it converged, through an elected lane: operands of a branch of
+// one lane are moved to the uniform registers anew for every instruction (490 cycles a block so).
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t stage, uint32_t idesc, uint32_t bar0, uint32_t bar1) {
+    const uint64_t ad = sdesc_k_sw128(stage), bd = sdesc_k_sw128(stage + A_BYTES);
+    asm volatile("{ .reg .pred q, f, t; .reg .b64 a, b;\n\t"
+                 "elect.sync _|q, 0xffffffff; setp.eq.u32 t, 0, 0; setp.eq.u32 f, 0, 1;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+                 "add.s64 a, %1, 2; add.s64 b, %2, 2;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+                 "add.s64 a, %1, 4; add.s64 b, %2, 4;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+                 "add.s64 a, %1, 6; add.s64 b, %2, 6;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5]; }"
+                 ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(bar0), "r"(bar1) : "memory");
 }
-#undef QZ_R32
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
@@ -131,11 +133,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nkb = a.K / BK;
     const int rank = splits > 1 ? (int)cluster_rank() : 0;
-    const int kb0 = (int)((int64_t)nkb * rank / splits), kb1 = (int)((int64_t)nkb * (rank + 1) / splits);
+    int kb0 = nkb * rank / splits, kb1 = nkb * (rank + 1) / splits;
+    asm volatile("" : "+r"(kb0), "+r"(kb1));      // else the quotients are formed anew in every loop over blocks (400 cycles each)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
-            mbar_init(full(s), a.row_token ? 33 : 2);     // the weights' producer and the rows': a thread, or 32 that copy
+            mbar_init(full(s), a.row_token ? 65 : 2);     // the weights' thread and the rows': one, or 64 that copy
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; b++) {
@@ -144,7 +147,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         for (int i = 0; i < INFO; i++) {
             mbar_init(ifull(i), 1);
-            mbar_init(iempty(i), 3 + EPI_WARPS);
+            mbar_init(iempty(i), 3 + EPI_WARPS);  // all warps but the one that hands them out
         }
         fence_barrier_init();
         prefetch_tmap(&tmA);
@@ -178,23 +181,60 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (warp < 4) {
         reg_dec<REGS_FEED>();
         int4 item;                                 // expert, first row, rows, column tile
-        if (warp == 0) {
-            // --------------------------------------------------------- weights
+        if ((warp & 1) == 0) {
+            // ------------------------------------------------ weights and rows
+            // Gathered rows: groups of 32 by turns to the two warps; lane l copies chunk l % 8 of every fourth row
+            // from l / 8 on. A row whose token is not there is any row here, the promotion writes zeros for it.
+            const int part = warp >> 1, c = lane & 7, sub = lane >> 3;
+            int* at = reinterpret_cast<int*>(smem + ROW_OFF) + part * 64;    // this warp's rows of the tile, in qA
+            const uint8_t* src = (a.tokens ? a.qA : a.qW) + 16 * c;
+            const uint32_t even = (c ^ sub) << 4, odd = (c ^ (4 + sub)) << 4;   // swizzle of rows sub, 4 + sub, 8 + sub, ...
             uint32_t it = 0;
             bool ok = true;
             while (ok && next_item(item)) {
                 const int n0 = item.x * a.N + item.w * (SWIGLU ? 128 : BN);
                 const bool two = SWIGLU || item.w * BN + 128 < a.N;
-                for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
-                    const int s = it % STAGES;
-                    ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
-                    if (ok && lane == 0) {
-                        const uint32_t dst = sbase + s * STAGE_BYTES + A_BYTES;
-                        mbar_arrive_expect_tx(full(s), two ? 2 * HALF_BYTES : HALF_BYTES);
-                        tma_load_2d(dst, &tmB, kb * BK, n0, full(s));
-                        if (two) tma_load_2d(dst + HALF_BYTES, &tmB, kb * BK, n0 + (SWIGLU ? a.N / 2 : 128), full(s));
+                const int boxes = (item.z + 31) / 32;
+                if (a.row_token) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const int r = 64 * i + 32 * part + lane, tok = r < item.z ? a.row_token[item.y + r] : 0;
+                        at[32 * i + (lane & 3) * 8 + (lane >> 2)] = tok >= 0 && tok < a.tokens ? tok : 0;
                     }
                     __syncwarp();
+                }
+                for (int kb = kb0; kb < kb1; kb++, it++) {
+                    const int s = it % STAGES;
+                    ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
+                    if (!ok) break;
+                    const uint32_t stage = sbase + s * STAGE_BYTES;
+                    if (part == 0 && lane == 0) {
+                        mbar_arrive_expect_tx(full(s), two ? 2 * HALF_BYTES : HALF_BYTES);
+                        tma_load_2d(stage + A_BYTES, &tmB, kb * BK, n0, full(s));
+                        if (two) tma_load_2d(stage + A_BYTES + HALF_BYTES, &tmB, kb * BK, n0 + (SWIGLU ? a.N / 2 : 128), full(s));
+                    }
+                    __syncwarp();
+                    if (a.row_token) {
+                        const uint8_t* from = src + kb * BK;
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const int r0 = 64 * i + 32 * part + sub;
+                            if (r0 - sub >= item.z) break;
+                            int4 tok[2];
+                            tok[0] = *reinterpret_cast<const int4*>(at + 32 * i + sub * 8);
+                            tok[1] = *reinterpret_cast<const int4*>(at + 32 * i + sub * 8 + 4);
+                            const int* k = reinterpret_cast<const int*>(tok);
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                if (r0 - sub + 4 * j < item.z) cp_async16(stage + (r0 + 4 * j) * BK + (j & 1 ? odd : even), from + (int64_t)k[j] * a.K);
+                        }
+                        cp_async_arrive(full(s));
+                    } else if (part == 1) {
+                        if (lane == 0) mbar_arrive_expect_tx(full(s), boxes * 32 * BK);
+                        __syncwarp();
+                        if (lane < boxes) tma_load_2d(stage + lane * 32 * BK, &tmA, kb * BK, item.y + 32 * lane, full(s));
+                    }
                 }
             }
             // all copies into this CTA's shared memory have landed before it may exit
@@ -207,81 +247,18 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             while (ok && next_item(item)) {
                 const bool two = SWIGLU || item.w * BN + 128 < a.N;
                 const uint32_t idesc = two ? idesc_dense(0u, 0u, BM, BN) : idesc_dense(0u, 0u, BM, 128);
-                if (lane == 0) {
-                    uint32_t i = it;
-                    for (int kb = kb0; kb < kb1; kb++, i++) {
-                        const int b = i & 1, s = i % STAGES;
-                        if (!mbar_wait(full(s), (i / STAGES) & 1, &g_moe_err) || !mbar_wait(tempty(b), ((i >> 1) & 1) ^ 1, &g_moe_err)) {
-                            ok = false;
-                            break;
-                        }
-                        if (a.row_token) fence_proxy_async_smem();           // the gathered rows came by the generic proxy
-                        tc_fence_after();
-                        const uint64_t ad = sdesc_k_sw128(sbase + s * STAGE_BYTES);
-                        const uint64_t bd = sdesc_k_sw128(sbase + s * STAGE_BYTES + A_BYTES);
-                        const uint32_t d = tmem_base + b * BN;
-#pragma unroll
-                        for (int ks = 0; ks < BK / 32; ks++)                 // K = 32 bytes per MMA
-                            mma_f8f6f4(d, ad + (uint64_t)(ks * 2), bd + (uint64_t)(ks * 2), idesc, ks > 0);
-                        tc_commit(empty(s));
-                        tc_commit(tfull(b));
-                    }
-                    it = i;
+                for (int kb = kb0; kb < kb1; kb++, it++) {
+                    const int b = it & 1, s = it % STAGES;
+                    ok = mbar_wait(full(s), (it / STAGES) & 1, &g_moe_err) && mbar_wait(tempty(b), ((it >> 1) & 1) ^ 1, &g_moe_err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (a.row_token) fence_proxy_async_smem();               // the gathered rows came by the generic proxy
+                    tc_fence_after();
+                    mma_block(tmem_base + b * BN, sbase + s * STAGE_BYTES, idesc, empty(s), tfull(b));
                 }
-                it = __shfl_sync(0xffffffffu, it, 0);
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             }
             // the last accumulators are complete before tensor memory is released
             if (it > 0) mbar_wait(tfull((it - 1) & 1), ((it - 1) >> 1) & 1, &g_moe_err);
-        } else if (warp == 2) {
-            // ------------------------------------------------------------ rows
-            int* at = reinterpret_cast<int*>(smem + ROW_OFF);  // the tile's rows in qA
-            uint32_t it = 0;
-            bool ok = true;
-            while (ok && next_item(item)) {
-                if (!a.row_token) {
-                    const int boxes = (item.z + 31) / 32;
-                    for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
-                        const int s = it % STAGES;
-                        ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
-                        if (ok && lane == 0) mbar_arrive_expect_tx(full(s), boxes * 32 * BK);
-                        __syncwarp();
-                        if (ok && lane < boxes) tma_load_2d(sbase + s * STAGE_BYTES + lane * 32 * BK, &tmA, kb * BK, item.y + 32 * lane, full(s));
-                    }
-                    continue;
-                }
-                // Lane l copies chunk l % 8 of rows l / 8, l / 8 + 4, ... A row whose token is not there is any
-                // row here, the promotion writes zeros for it.
-                const int c = lane & 7, steps = (item.z + 3) / 4;
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int r = 32 * j + lane, tok = r < item.z ? a.row_token[item.y + r] : 0;
-                    at[(r & 3) * 32 + (r >> 2)] = tok >= 0 && tok < a.tokens ? tok : 0;
-                }
-                __syncwarp();
-                const uint8_t* src = (a.tokens ? a.qA : a.qW) + 16 * c;
-                for (int kb = kb0; kb < kb1 && ok; kb++, it++) {
-                    const int s = it % STAGES;
-                    ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
-                    if (!ok) break;
-                    const uint32_t dst = sbase + s * STAGE_BYTES + (lane >> 3) * BK;
-                    const uint8_t* from = src + kb * BK;
-                    // swizzle of row 4 j + l / 8: its lowest three bits are those of an even or an odd j
-                    const uint32_t even = (c ^ (lane >> 3)) << 4, odd = (c ^ (4 + (lane >> 3))) << 4;
-#pragma unroll 1
-                    for (int j = 0; j < steps; j += 8) {
-                        int4 tok[2];
-                        tok[0] = *reinterpret_cast<const int4*>(at + (lane >> 3) * 32 + j);
-                        tok[1] = *reinterpret_cast<const int4*>(at + (lane >> 3) * 32 + j + 4);
-                        const int* k = reinterpret_cast<const int*>(tok);
-#pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            if (j + i < steps) cp_async16(dst + 4 * (j + i) * BK + (i & 1 ? odd : even), from + (int64_t)k[i] * a.K);
-                    }
-                    cp_async_arrive(full(s));
-                }
-            }
         } else {
             // ----------------------------------------------------------- items
             // lane l: the row tiles before expert l * per; an item of the list is row tile p of an
@@ -409,9 +386,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         while (ok && next_item(item)) {
             const bool active = q * 32 < item.z;              // some row of the warp exists
             const bool two = SWIGLU || item.w * BN + 128 < a.N;
-            uint64_t acc[64];                                 // 64 columns of the first box, 64 of the second
+            float acc[128];                                   // 64 columns of the first box, 64 of the second
 #pragma unroll
-            for (int i = 0; i < 64; i++) acc[i] = 0ull;
+            for (int i = 0; i < 128; i++) acc[i] = 0.0f;
             for (int kb = kb0; kb < kb1; kb++, it++) {
                 const int b = it & 1;
                 ok = mbar_wait(tfull(b), (it >> 1) & 1, &g_moe_err);
@@ -425,22 +402,22 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const float* s = reinterpret_cast<const float*>(smem + SCALE_OFF + b * SCALE_BYTES);
                     const float c = s[r];
                     const float2 w = *reinterpret_cast<const float2*>(s + BM);
-                    const uint64_t s0 = twice(c * w.x), s1 = twice(c * w.y);
-                    tmem_arrived(x, y);
+                    const float s0 = c * w.x, s1 = c * w.y;
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i++) fma2(acc[i], x[2 * i], x[2 * i + 1], s0);
+                    for (int i = 0; i < 32; i++) fma1(acc[i], x[i], s0);
                     tmem_ld32(t + 128, x);
 #pragma unroll
-                    for (int i = 0; i < 16; i++) fma2(acc[16 + i], y[2 * i], y[2 * i + 1], s0);
+                    for (int i = 0; i < 32; i++) fma1(acc[32 + i], y[i], s0);
                     tmem_ld32(t + 160, y);
-                    tmem_arrived(x, y);
+                    tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(tempty(b));                // all of it is in registers
 #pragma unroll
-                    for (int i = 0; i < 16; i++) fma2(acc[32 + i], x[2 * i], x[2 * i + 1], s1);
+                    for (int i = 0; i < 32; i++) fma1(acc[64 + i], x[i], s1);
 #pragma unroll
-                    for (int i = 0; i < 16; i++) fma2(acc[48 + i], y[2 * i], y[2 * i + 1], s1);
+                    for (int i = 0; i < 32; i++) fma1(acc[96 + i], y[i], s1);
                 } else {
                     tc_fence_before();
                     __syncwarp();
@@ -457,7 +434,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(mine + (rank - 1) * PART_BYTES));
 #pragma unroll
                     for (int i = 0; i < 32; i++)
-                        asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(dst + i * 512), "l"(acc[2 * i]), "l"(acc[2 * i + 1]) : "memory");
+                        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * 512), "f"(acc[4 * i]),
+                                     "f"(acc[4 * i + 1]), "f"(acc[4 * i + 2]), "f"(acc[4 * i + 3]) : "memory");
                 }
                 cluster_sync();
                 synced = true;
@@ -467,8 +445,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                         for (int i = 0; i < 32; i++) {
                             const float4 v = *reinterpret_cast<const float4*>(smem + ((h * 32) * 32 + lane) * 16 + p * PART_BYTES + i * 512);
-                            acc[2 * i] = ((uint64_t)__float_as_uint(hi(acc[2 * i]) + v.y) << 32) | __float_as_uint(lo(acc[2 * i]) + v.x);
-                            acc[2 * i + 1] = ((uint64_t)__float_as_uint(hi(acc[2 * i + 1]) + v.w) << 32) | __float_as_uint(lo(acc[2 * i + 1]) + v.z);
+                            acc[4 * i] += v.x;
+                            acc[4 * i + 1] += v.y;
+                            acc[4 * i + 2] += v.z;
+                            acc[4 * i + 3] += v.w;
                         }
             }
             // a row whose token is not there was multiplied by 0, but what it was may be NaN
@@ -476,20 +456,18 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int token = a.row_token ? a.row_token[row] : row;
             if (token < 0 || token >= a.tokens) {
 #pragma unroll
-                for (int i = 0; i < 64; i++) acc[i] = 0ull;
+                for (int i = 0; i < 128; i++) acc[i] = 0.0f;
             }
             const size_t out = (size_t)(item.y + r);
             if constexpr (SWIGLU) {
-                // column i of h: gate acc[i / 2], up acc[32 + i / 2]; a scale's 128 columns lie in two threads
+                // column i of h: gate acc[i], up acc[64 + i]; a scale's 128 columns lie in two threads
                 float* peak = reinterpret_cast<float*>(smem + STG_OFF) + (done & 1) * 256;
                 float am = 0.0f;
                 if (active) {
 #pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const float g0 = lo(acc[i]), g1 = hi(acc[i]);
-                        const float h0 = __fdividef(g0, 1.0f + __expf(-g0)) * lo(acc[32 + i]), h1 = __fdividef(g1, 1.0f + __expf(-g1)) * hi(acc[32 + i]);
-                        am = fmaxf(am, fmaxf(fabsf(h0), fabsf(h1)));
-                        acc[i] = ((uint64_t)__float_as_uint(h1) << 32) | __float_as_uint(h0);
+                    for (int i = 0; i < 64; i++) {
+                        acc[i] = __fdividef(acc[i], 1.0f + __expf(-acc[i])) * acc[64 + i];
+                        am = fmaxf(am, fabsf(acc[i]));
                     }
                 }
                 peak[h * 128 + r] = am;
@@ -504,7 +482,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         uint32_t p[8];
 #pragma unroll
                         for (int e = 0; e < 8; e++) {
-                            const float v = lo(acc[8 * j + e]), w = hi(acc[8 * j + e]);
+                            const float v = acc[16 * j + 2 * e], w = acc[16 * j + 2 * e + 1];
                             p[e] = e4m3x2(sign_of(div1(v, d), v), sign_of(div1(w, d), w));
                         }
                         codes[j] = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
@@ -525,8 +503,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
-                            const uint64_t v = acc[s * 32 + j * 4 + e];
-                            const __nv_bfloat162 p = __floats2bfloat162_rn(lo(v), hi(v));
+                            const __nv_bfloat162 p = __floats2bfloat162_rn(acc[s * 64 + j * 8 + 2 * e], acc[s * 64 + j * 8 + 2 * e + 1]);
                             w[e] = *reinterpret_cast<const uint32_t*>(&p);
                         }
                         *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
