@@ -9,21 +9,21 @@
 // items out through a ring in shared memory, an expert's row tiles before its next columns,
 // so that the CTAs of one moment share weights and rows in L2.
 //
-// CTA of 12 warps, one per SM:
-//  warps 0, 2 weights: TMA boxes of 128 x 128 bytes into a 4-stage ring; rows: gathered by their tokens in copies of
-//             16 bytes (cp.async), or TMA boxes of 32 rows where they lie in order. (Gathered by TMA, four rows
-//             a copy, a block of 128 rows took 2400 cycles; by one warp's copies 1900.) The copies arrive on the
-//             stage's barrier by themselves, and the MMA's thread orders them before its own reads.
-//  warp 1     MMA: per block of 128 of K four tcgen05.mma (M 128, N 256, K 32) into one of two
-//             accumulators of 256 columns in tensor memory
-//  warp 3     items, and the block scales of an accumulator's rows and columns into shared memory
-//  warps 4-11 promotion: block scales are fp32, so every block's partial sums leave tensor
-//             memory to be added as acc += P_kb * (sA sW). A thread holds one row of 64 columns of
-//             each of the two boxes.
+// CTA of 16 warps, one per SM:
+//  warp 0      weights: TMA boxes of 128 x 128 bytes into a 4-stage ring
+//  warp 1      MMA: per block of 128 of K four tcgen05.mma (M 128, N 256, K 32) into one of two
+//              accumulators of 256 columns in tensor memory
+//  warp 2      items (warp 3 completes the warpgroup)
+//  warps 4-7   rows: gathered by their tokens in copies of 16 bytes (cp.async), as TMA boxes of 32 rows where
+//              they lie in order. The copies arrive on the stage's barrier by themselves, and the
+//              MMA's warp orders them before its own reads. (Gathered by TMA, four rows a copy, a block of
+//              128 rows took 2400 cycles; by one warp's copies 1900.)
+//  warps 8-15  promotion: block scales are fp32, so every block's partial sums leave tensor
+//              memory to be added as acc += P_kb * (sA sW). A thread holds one row of 64 columns of
+//              each of the two boxes.
 // What bounds it with many rows is the cycle of an accumulator: MMA 512 cycles, hand-off, promotion,
-// hand-off, for two blocks of K by turns. So a promotion is kept short: REGS_EPI registers a
-// thread (the other warps give theirs up) hold the 128 sums and two reads of 32 columns; the scales lie
-// ready when the accumulator does.
+// hand-off, for two blocks of K by turns. So what lies between is kept short: scales are read by the promoting threads
+// themselves, groups of four blocks ahead (staged in shared memory they came 300 cycles late), and waits are few.
 // With few rows the bound is the weights' way from memory, and the promotion and the gather of rows that
 // are not there are left out. Where items are fewer than SMs (rows <= 32), a cluster shares an item's K.
 #include "qz_moe.cuh"
@@ -41,16 +41,13 @@ __device__ unsigned int g_moe_err;
 constexpr int BM = 128, BN = 256, BK = 128, STAGES = 4;
 constexpr int A_BYTES = BM * BK, HALF_BYTES = 128 * BK;
 constexpr int STAGE_BYTES = A_BYTES + 2 * HALF_BYTES;
-constexpr int EPI_WARPS = 8, THREADS = 128 + EPI_WARPS * 32;
-constexpr int REGS_FEED = 56, REGS_EPI = 224;     // 128 * 56 + 256 * 224 = 384 * 168, what the CTA is launched with
+constexpr int FEED_WARPS = 8, EPI_WARPS = 8, THREADS = (FEED_WARPS + EPI_WARPS) * 32;
+constexpr int REGS_FEED = 48, REGS_EPI = 208;     // 256 * 48 + 256 * 208 = 512 * 128, what the CTA is launched with
 constexpr int INFO = 4;                           // items in flight
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int STG_WARP = 32 * 128;                // a warp's output: 32 rows of 64 bf16
 constexpr int STG_OFF = STAGES * STAGE_BYTES;
-constexpr int SCALE_OFF = STG_OFF + EPI_WARPS * STG_WARP;
-constexpr int SCALE_BYTES = BM * 4 + 16;          // an accumulator's row scales, then its two boxes'
-constexpr int ROW_OFF = SCALE_OFF + 2 * SCALE_BYTES;
-constexpr int INFO_OFF = ROW_OFF + BM * 4;
+constexpr int INFO_OFF = STG_OFF + EPI_WARPS * STG_WARP;
 constexpr int BAR_OFF = INFO_OFF + INFO * 16;
 constexpr int BARS = 2 * STAGES + 4 + 2 * INFO;
 constexpr int SMEM_BYTES = BAR_OFF + BARS * 8 + 16 + 1024;
@@ -85,6 +82,20 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint32_t stage, uint32_t i
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5]; }"
                  ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(bar0), "r"(bar1) : "memory");
+}
+
+// The bounded wait of this kernel. 15 warps wait at a time, and each poll takes the shared-memory pipe that the scales'
+// reads and the arrivals need: few polls, with a long suspend hint.
+constexpr uint32_t kHintNs = 1000, kPolls = 1u << 21;
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kPolls; i++) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(bar), "r"(parity), "r"(kHintNs) : "memory");
+        if (ok) return true;
+    }
+    atomicExch(&g_moe_err, (unsigned int)QZ_ERR_TIMEOUT);
+    return false;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -138,16 +149,16 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
-            mbar_init(full(s), a.row_token ? 65 : 2);     // the weights' thread and the rows': one, or 64 that copy
+            mbar_init(full(s), a.row_token ? 129 : 2);    // the weights' thread and the rows': one, or 128 that copy
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; b++) {
-            mbar_init(tfull(b), 2);               // the MMAs and the scales
+            mbar_init(tfull(b), 1);
             mbar_init(tempty(b), EPI_WARPS);
         }
         for (int i = 0; i < INFO; i++) {
             mbar_init(ifull(i), 1);
-            mbar_init(iempty(i), 3 + EPI_WARPS);  // all warps but the one that hands them out
+            mbar_init(iempty(i), 2 + 4 + EPI_WARPS);
         }
         fence_barrier_init();
         prefetch_tmap(&tmA);
@@ -167,7 +178,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint32_t taken = 0;
     auto next_item = [&](int4& it) {
         const int i = taken % INFO;
-        if (!mbar_wait(ifull(i), (taken / INFO) & 1, &g_moe_err)) return false;
+        if (!warp_wait(ifull(i), (taken / INFO) & 1)) return false;
         it.x = info[i].x;
         it.y = info[i].y;
         it.z = info[i].z;
@@ -178,68 +189,71 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         return it.x >= 0;
     };
 
-    if (warp < 4) {
+    if (warp < FEED_WARPS) {
         reg_dec<REGS_FEED>();
         int4 item;                                 // expert, first row, rows, column tile
-        if ((warp & 1) == 0) {
-            // ------------------------------------------------ weights and rows
-            // Gathered rows: groups of 32 by turns to the two warps; lane l copies chunk l % 8 of every fourth row
-            // from l / 8 on. A row whose token is not there is any row here, the promotion writes zeros for it.
-            const int part = warp >> 1, c = lane & 7, sub = lane >> 3;
-            int* at = reinterpret_cast<int*>(smem + ROW_OFF) + part * 64;    // this warp's rows of the tile, in qA
-            const uint8_t* src = (a.tokens ? a.qA : a.qW) + 16 * c;
-            const uint32_t even = (c ^ sub) << 4, odd = (c ^ (4 + sub)) << 4;   // swizzle of rows sub, 4 + sub, 8 + sub, ...
+        if (warp == 0) {
+            // --------------------------------------------------------- weights
             uint32_t it = 0;
             bool ok = true;
             while (ok && next_item(item)) {
                 const int n0 = item.x * a.N + item.w * (SWIGLU ? 128 : BN);
                 const bool two = SWIGLU || item.w * BN + 128 < a.N;
-                const int boxes = (item.z + 31) / 32;
-                if (a.row_token) {
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const int r = 64 * i + 32 * part + lane, tok = r < item.z ? a.row_token[item.y + r] : 0;
-                        at[32 * i + (lane & 3) * 8 + (lane >> 2)] = tok >= 0 && tok < a.tokens ? tok : 0;
-                    }
-                    __syncwarp();
-                }
                 for (int kb = kb0; kb < kb1; kb++, it++) {
                     const int s = it % STAGES;
-                    ok = mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, &g_moe_err);
+                    ok = warp_wait(empty(s), ((it / STAGES) & 1) ^ 1);
                     if (!ok) break;
-                    const uint32_t stage = sbase + s * STAGE_BYTES;
-                    if (part == 0 && lane == 0) {
+                    if (lane == 0) {
+                        const uint32_t dst = sbase + s * STAGE_BYTES + A_BYTES;
                         mbar_arrive_expect_tx(full(s), two ? 2 * HALF_BYTES : HALF_BYTES);
-                        tma_load_2d(stage + A_BYTES, &tmB, kb * BK, n0, full(s));
-                        if (two) tma_load_2d(stage + A_BYTES + HALF_BYTES, &tmB, kb * BK, n0 + (SWIGLU ? a.N / 2 : 128), full(s));
+                        tma_load_2d(dst, &tmB, kb * BK, n0, full(s));
+                        if (two) tma_load_2d(dst + HALF_BYTES, &tmB, kb * BK, n0 + (SWIGLU ? a.N / 2 : 128), full(s));
                     }
                     __syncwarp();
-                    if (a.row_token) {
-                        const uint8_t* from = src + kb * BK;
-#pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const int r0 = 64 * i + 32 * part + sub;
-                            if (r0 - sub >= item.z) break;
-                            int4 tok[2];
-                            tok[0] = *reinterpret_cast<const int4*>(at + 32 * i + sub * 8);
-                            tok[1] = *reinterpret_cast<const int4*>(at + 32 * i + sub * 8 + 4);
-                            const int* k = reinterpret_cast<const int*>(tok);
-#pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                if (r0 - sub + 4 * j < item.z) cp_async16(stage + (r0 + 4 * j) * BK + (j & 1 ? odd : even), from + (int64_t)k[j] * a.K);
-                        }
-                        cp_async_arrive(full(s));
-                    } else if (part == 1) {
-                        if (lane == 0) mbar_arrive_expect_tx(full(s), boxes * 32 * BK);
-                        __syncwarp();
-                        if (lane < boxes) tma_load_2d(stage + lane * 32 * BK, &tmA, kb * BK, item.y + 32 * lane, full(s));
-                    }
                 }
             }
             // all copies into this CTA's shared memory have landed before it may exit
             for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; j++)
-                mbar_wait(empty(j % STAGES), (j / STAGES) & 1, &g_moe_err);
+                warp_wait(empty(j % STAGES), (j / STAGES) & 1);
+        } else if (warp >= 4) {
+            // ------------------------------------------------------------ rows
+            // Gathered: warp p has rows 32 p .. 32 p + 31, lane l copies chunk l % 8 of every fourth of them from
+            // l / 8 on. A row whose token is not there is any row here, the promotion writes zeros for it.
+            const int part = warp - 4, c = lane & 7, sub = lane >> 3;
+            const uint8_t* src = (a.tokens ? a.qA : a.qW) + 16 * c;
+            const uint32_t even = (c ^ sub) << 4, odd = (c ^ (4 + sub)) << 4;   // swizzle of rows sub, 4 + sub, 8 + sub, ...
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && next_item(item)) {
+                const int here = item.z - 32 * part;                            // rows from this warp's first on
+                int at[8];                                                      // this lane's rows, in qA
+                if (a.row_token) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const int tok = sub + 4 * j < here ? a.row_token[item.y + 32 * part + sub + 4 * j] : 0;
+                        at[j] = tok >= 0 && tok < a.tokens ? tok : 0;
+                    }
+                }
+                for (int kb = kb0; kb < kb1; kb++, it++) {
+                    const int s = it % STAGES;
+                    if (!a.row_token && part) continue;
+                    ok = warp_wait(empty(s), ((it / STAGES) & 1) ^ 1);
+                    if (!ok) break;
+                    const uint32_t dst = sbase + s * STAGE_BYTES;
+                    if (a.row_token) {
+                        const uint8_t* from = src + kb * BK;
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            if (4 * j < here) cp_async16(dst + (32 * part + sub + 4 * j) * BK + (j & 1 ? odd : even), from + (int64_t)at[j] * a.K);
+                        cp_async_arrive(full(s));
+                    } else {
+                        const int boxes = (item.z + 31) / 32;
+                        if (lane == 0) mbar_arrive_expect_tx(full(s), boxes * 32 * BK);
+                        __syncwarp();
+                        if (lane < boxes) tma_load_2d(dst + lane * 32 * BK, &tmA, kb * BK, item.y + 32 * lane, full(s));
+                    }
+                }
+            }
         } else if (warp == 1) {
             // ------------------------------------------------------------- MMA
             uint32_t it = 0;
@@ -249,7 +263,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const uint32_t idesc = two ? idesc_dense(0u, 0u, BM, BN) : idesc_dense(0u, 0u, BM, 128);
                 for (int kb = kb0; kb < kb1; kb++, it++) {
                     const int b = it & 1, s = it % STAGES;
-                    ok = mbar_wait(full(s), (it / STAGES) & 1, &g_moe_err) && mbar_wait(tempty(b), ((it >> 1) & 1) ^ 1, &g_moe_err);
+                    ok = warp_wait(full(s), (it / STAGES) & 1) && warp_wait(tempty(b), ((it >> 1) & 1) ^ 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (a.row_token) fence_proxy_async_smem();               // the gathered rows came by the generic proxy
@@ -258,8 +272,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
             }
             // the last accumulators are complete before tensor memory is released
-            if (it > 0) mbar_wait(tfull((it - 1) & 1), ((it - 1) >> 1) & 1, &g_moe_err);
-        } else {
+            if (it > 0) warp_wait(tfull((it - 1) & 1), ((it - 1) >> 1) & 1);
+        } else if (warp == 2) {
             // ----------------------------------------------------------- items
             // lane l: the row tiles before expert l * per; an item of the list is row tile p of an
             // expert's column tile n, p running first
@@ -273,18 +287,17 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (lane >= o) upto += v;
             }
             const int64_t total = (int64_t)__shfl_sync(0xffffffffu, upto, 31) * nt;
-            const int64_t first = (int64_t)(upto - mine) * nt;
-            uint32_t n = 0;
-            // the n-th item of this CTA, into the ring; x < 0: there is none
-            auto hand_out = [&](int4& v) {
+            const int first = upto - mine;
+            bool ok = true;
+            for (uint32_t n = 0; ok; n++) {
                 const int64_t i = blockIdx.x / splits + (int64_t)n * (gridDim.x / splits);
-                v = make_int4(-1, 0, 0, 0);
+                int4 v = make_int4(-1, 0, 0, 0);
                 // a cluster has one item: more than the host's bound come from offsets that do not ascend
                 if (i < total && (splits == 1 || n == 0)) {
                     // the lane whose experts hold the item, then the expert among them
-                    const uint32_t who = __ballot_sync(0xffffffffu, first <= i && mine > 0);
+                    const uint32_t who = __ballot_sync(0xffffffffu, (int64_t)first * nt <= i && mine > 0);
                     const int l = 31 - __clz(who);
-                    const int64_t base = __shfl_sync(0xffffffffu, first, l);
+                    const int64_t base = (int64_t)__shfl_sync(0xffffffffu, first, l) * nt;
                     const int e = l * per + lane;
                     const int2 r = lane < per && e < a.experts ? expert_rows(a, e) : make_int2(0, 0);
                     const int tiles = row_tiles(r);
@@ -306,8 +319,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     v.w = __shfl_sync(0xffffffffu, v.w, w);
                 }
                 const int slot = n % INFO;
-                if (!mbar_wait(iempty(slot), ((n / INFO) & 1) ^ 1, &g_moe_err)) return false;
-                if (lane == 0) {
+                ok = warp_wait(iempty(slot), ((n / INFO) & 1) ^ 1);
+                if (ok && lane == 0) {
                     info[slot].x = v.x;
                     info[slot].y = v.y;
                     info[slot].z = v.z;
@@ -315,58 +328,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     mbar_arrive(ifull(slot));
                 }
                 __syncwarp();
-                n++;
-                return true;
-            };
-            int4 next;
-            bool ok = hand_out(item) && (item.x < 0 || hand_out(next));
-            uint32_t it = 0;
-            while (ok && item.x >= 0) {
-                // lane l: the scales of rows l, l + 32, l + 64 and l + 96; four blocks of K a read where they are aligned
-                const bool two = SWIGLU || item.w * BN + 128 < a.N;
-                const float* sw = a.sW + ((size_t)item.x * (a.N / 128) + (SWIGLU ? item.w : 2 * item.w)) * nkb;
-                if (lane == 1 && two) sw += (size_t)(SWIGLU ? a.N / 256 : 1) * nkb;
-                const float* sa[4];
-                bool there[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int r = 32 * j + lane;
-                    const int tok = r >= item.z ? -1 : a.row_token ? a.row_token[item.y + r] : item.y + r;
-                    there[j] = tok >= 0 && tok < a.tokens;
-                    sa[j] = a.sA + (size_t)(there[j] ? tok : 0) * nkb;
-                }
-                const bool vec = ((nkb | kb0) & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sA) & 15) == 0;
-                for (int kb4 = kb0; kb4 < kb1 && ok; kb4 += 4) {
-                    float c[4][4], w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        if (vec && kb4 + 4 <= kb1 && there[j]) {
-                            *reinterpret_cast<float4*>(c[j]) = __ldg(reinterpret_cast<const float4*>(sa[j] + kb4));
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 4; u++) c[j][u] = there[j] && kb4 + u < kb1 ? __ldg(sa[j] + kb4 + u) : 0.0f;
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; u++) w[u] = lane < 2 && kb4 + u < kb1 ? __ldg(sw + kb4 + u) : 0.0f;
-#pragma unroll
-                    for (int u = 0; u < 4; u++) {
-                        if (kb4 + u >= kb1) break;
-                        const int b = it & 1;
-                        ok = mbar_wait(tempty(b), ((it >> 1) & 1) ^ 1, &g_moe_err);
-                        if (!ok) break;
-                        float* s = reinterpret_cast<float*>(smem + SCALE_OFF + b * SCALE_BYTES);
-#pragma unroll
-                        for (int j = 0; j < 4; j++) s[32 * j + lane] = c[j][u];
-                        if (lane < 2) s[BM + lane] = w[u];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(tfull(b));
-                        it++;
-                    }
-                }
-                if (!ok) break;
-                item = next;
-                if (item.x >= 0) ok = hand_out(next);
+                if (v.x < 0) break;
             }
         }
         if (splits > 1) {
@@ -376,55 +338,101 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     } else {
         // ------------------------------------------------- promotion and output
         reg_inc<REGS_EPI>();
-        const int q = warp & 3, h = (warp - 4) >> 2;          // lane quarter of tensor memory, half of each box
+        const int q = warp & 3, h = (warp - FEED_WARPS) >> 2;          // lane quarter of tensor memory, half of each box
         const int r = q * 32 + lane;                          // row of the tile
-        uint8_t* stg = smem + STG_OFF + (warp - 4) * STG_WARP;
+        uint8_t* stg = smem + STG_OFF + (warp - FEED_WARPS) * STG_WARP;
+        // Scales are read four blocks of K at a time and a group ahead, an item's first ones before the output of the item
+        // before it; its row's token a whole item ahead.
+        const bool vec = ((nkb | kb0) & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sW)) & 15) == 0;
+        const float *sa = a.sA, *sw = a.sW;
+        int up = 0, token = 0;                                // from the first box's weight scales to the second's; the row in qA
+        float4 na, nw0, nw1;                                  // a group in flight
+        auto read_group = [&](int kb) {
+            if (vec && kb + 4 <= kb1) {
+                na = __ldg(reinterpret_cast<const float4*>(sa + kb));
+                nw0 = __ldg(reinterpret_cast<const float4*>(sw + kb));
+                nw1 = __ldg(reinterpret_cast<const float4*>(sw + up + kb));
+            } else {
+                auto one = [&](const float* p, int i) { return kb + i < kb1 ? __ldg(p + kb + i) : 0.0f; };
+                na = make_float4(one(sa, 0), one(sa, 1), one(sa, 2), one(sa, 3));
+                nw0 = make_float4(one(sw, 0), one(sw, 1), one(sw, 2), one(sw, 3));
+                nw1 = make_float4(one(sw + up, 0), one(sw + up, 1), one(sw + up, 2), one(sw + up, 3));
+            }
+        };
+        auto row_of = [&](const int4& i) {                    // a row behind the tile's last repeats that one
+            const int row = i.y + min(r, i.z - 1);
+            return a.row_token ? a.row_token[row] : row;
+        };
+        auto begin = [&](const int4& i, int tok) {            // the item's first group; a token that is not there counts as any
+            const bool two = SWIGLU || i.w * BN + 128 < a.N;
+            sa = a.sA + (int64_t)(tok >= 0 && tok < a.tokens ? tok : 0) * nkb;
+            sw = a.sW + ((size_t)i.x * (a.N / 128) + (SWIGLU ? i.w : 2 * i.w)) * nkb;
+            up = two ? (SWIGLU ? a.N / 256 : 1) * nkb : 0;
+            if (a.tokens) read_group(kb0);
+        };
+        na = nw0 = nw1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         uint32_t it = 0;
         int done = 0;
         bool ok = true, synced = false;
-        int4 item;
-        while (ok && next_item(item)) {
+        int4 item, next;
+        bool more = next_item(next);
+        if (more) {
+            token = row_of(next);
+            begin(next, token);
+        }
+        while (ok && more) {
+            item = next;
+            const bool there = token >= 0 && token < a.tokens;
+            more = next_item(next);
+            if (more) token = row_of(next);
             const bool active = q * 32 < item.z;              // some row of the warp exists
             const bool two = SWIGLU || item.w * BN + 128 < a.N;
             float acc[128];                                   // 64 columns of the first box, 64 of the second
 #pragma unroll
             for (int i = 0; i < 128; i++) acc[i] = 0.0f;
+            float4 s0, s1;                                    // the group's scales of the two boxes
             for (int kb = kb0; kb < kb1; kb++, it++) {
                 const int b = it & 1;
-                ok = mbar_wait(tfull(b), (it >> 1) & 1, &g_moe_err);
+                if (((kb - kb0) & 3) == 0) {
+                    s0 = make_float4(na.x * nw0.x, na.y * nw0.y, na.z * nw0.z, na.w * nw0.w);
+                    s1 = make_float4(na.x * nw1.x, na.y * nw1.y, na.z * nw1.z, na.w * nw1.w);
+                    if (kb + 4 < kb1 && a.tokens) read_group(kb + 4);
+                }
+                ok = warp_wait(tfull(b), (it >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (active) {
                     const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + b * BN + h * 64;
-                    uint32_t x[32], y[32];
+                    uint32_t x[32];
                     tmem_ld32(t, x);
-                    tmem_ld32(t + 32, y);
-                    const float* s = reinterpret_cast<const float*>(smem + SCALE_OFF + b * SCALE_BYTES);
-                    const float c = s[r];
-                    const float2 w = *reinterpret_cast<const float2*>(s + BM);
-                    const float s0 = c * w.x, s1 = c * w.y;
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; i++) fma1(acc[i], x[i], s0);
-                    tmem_ld32(t + 128, x);
+                    for (int i = 0; i < 32; i++) fma1(acc[i], x[i], s0.x);
+                    tmem_ld32(t + 32, x);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; i++) fma1(acc[32 + i], y[i], s0);
-                    tmem_ld32(t + 160, y);
+                    for (int i = 0; i < 32; i++) fma1(acc[32 + i], x[i], s0.x);
+                    tmem_ld32(t + 128, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i++) fma1(acc[64 + i], x[i], s1.x);
+                    tmem_ld32(t + 160, x);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(tempty(b));                // all of it is in registers
 #pragma unroll
-                    for (int i = 0; i < 32; i++) fma1(acc[64 + i], x[i], s1);
-#pragma unroll
-                    for (int i = 0; i < 32; i++) fma1(acc[96 + i], y[i], s1);
+                    for (int i = 0; i < 32; i++) fma1(acc[96 + i], x[i], s1.x);
                 } else {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(tempty(b));
                 }
+                s0 = make_float4(s0.y, s0.z, s0.w, 0.0f);
+                s1 = make_float4(s1.y, s1.z, s1.w, 0.0f);
             }
             if (!ok) break;
+            if (more) begin(next, token);
             if (splits > 1) {
                 // the sums of an item's parts meet in rank 0, in the order of the ranks
                 cluster_sync();                               // its ring is free
@@ -451,10 +459,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             acc[4 * i + 3] += v.w;
                         }
             }
-            // a row whose token is not there was multiplied by 0, but what it was may be NaN
-            const int row = item.y + min(r, item.z - 1);
-            const int token = a.row_token ? a.row_token[row] : row;
-            if (token < 0 || token >= a.tokens) {
+            if (!there) {                                     // a row of zeros
 #pragma unroll
                 for (int i = 0; i < 128; i++) acc[i] = 0.0f;
             }
