@@ -49,7 +49,7 @@ constexpr int STG_WARP = 32 * 128;                // a warp's output: 32 rows of
 constexpr int STG_OFF = STAGES * STAGE_BYTES;
 constexpr int INFO_OFF = STG_OFF + EPI_WARPS * STG_WARP;
 constexpr int BAR_OFF = INFO_OFF + INFO * 16;
-constexpr int BARS = 2 * STAGES + 4 + 2 * INFO;
+constexpr int BARS = 2 * STAGES + 2 + 2 * INFO;
 constexpr int SMEM_BYTES = BAR_OFF + BARS * 8 + 16 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of a CTA");
 constexpr int SPLIT_ROWS = 32, MAX_SPLITS = 4;    // rows of a shared item: one warp's lanes
@@ -106,6 +106,9 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ int one(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ bool all(bool v) { return __all_sync(0xffffffffu, v); }
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -137,25 +140,22 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     auto full = [&](int s) { return bars + 8 * s; };
     auto empty = [&](int s) { return bars + 8 * (STAGES + s); };
     auto tfull = [&](int b) { return bars + 8 * (2 * STAGES + b); };
-    auto tempty = [&](int b) { return bars + 8 * (2 * STAGES + 2 + b); };
-    auto ifull = [&](int i) { return bars + 8 * (2 * STAGES + 4 + i); };
-    auto iempty = [&](int i) { return bars + 8 * (2 * STAGES + 4 + INFO + i); };
+    auto ifull = [&](int i) { return bars + 8 * (2 * STAGES + 2 + i); };
+    auto iempty = [&](int i) { return bars + 8 * (2 * STAGES + 2 + INFO + i); };
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // What a warp's lanes have in common goes through one(): loops and addresses that depend on it are then known to be
+    // the warp's, and the operands of its tensor instructions stay in uniform registers.
+    const int warp = one(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nkb = a.K / BK;
-    const int rank = splits > 1 ? (int)cluster_rank() : 0;
-    int kb0 = nkb * rank / splits, kb1 = nkb * (rank + 1) / splits;
-    asm volatile("" : "+r"(kb0), "+r"(kb1));      // else the quotients are formed anew in every loop over blocks (400 cycles each)
+    const int rank = splits > 1 ? one(cluster_rank()) : 0;
+    const int kb0 = one(nkb * rank / splits), kb1 = one(nkb * (rank + 1) / splits);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
-            mbar_init(full(s), a.row_token ? 129 : 2);    // the weights' thread and the rows': one, or 128 that copy
+            mbar_init(full(s), EPI_WARPS + (a.row_token ? 129 : 2));    // the accumulator; the weights' thread; the rows': one, or 128 that copy
             mbar_init(empty(s), 1);
         }
-        for (int b = 0; b < 2; b++) {
-            mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), EPI_WARPS);
-        }
+        for (int b = 0; b < 2; b++) mbar_init(tfull(b), 1);
         for (int i = 0; i < INFO; i++) {
             mbar_init(ifull(i), 1);
             mbar_init(iempty(i), 2 + 4 + EPI_WARPS);
@@ -171,19 +171,18 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = one(*tmem_slot);
     pdl_wait();
 
     // The next item (x < 0: no more); every warp but warp 3 takes each of them once.
     uint32_t taken = 0;
     auto next_item = [&](int4& it) {
         const int i = taken % INFO;
-        if (!warp_wait(ifull(i), (taken / INFO) & 1)) return false;
-        it.x = info[i].x;
-        it.y = info[i].y;
-        it.z = info[i].z;
-        it.w = info[i].w;
-        __syncwarp();
+        if (!all(warp_wait(ifull(i), (taken / INFO) & 1))) return false;
+        it.x = one(info[i].x);
+        it.y = one(info[i].y);
+        it.z = one(info[i].z);
+        it.w = one(info[i].w);
         if (lane == 0) mbar_arrive(iempty(i));
         taken++;
         return it.x >= 0;
@@ -201,7 +200,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const bool two = SWIGLU || item.w * BN + 128 < a.N;
                 for (int kb = kb0; kb < kb1; kb++, it++) {
                     const int s = it % STAGES;
-                    ok = warp_wait(empty(s), ((it / STAGES) & 1) ^ 1);
+                    ok = all(warp_wait(empty(s), ((it / STAGES) & 1) ^ 1));
                     if (!ok) break;
                     if (lane == 0) {
                         const uint32_t dst = sbase + s * STAGE_BYTES + A_BYTES;
@@ -237,7 +236,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 for (int kb = kb0; kb < kb1; kb++, it++) {
                     const int s = it % STAGES;
                     if (!a.row_token && part) continue;
-                    ok = warp_wait(empty(s), ((it / STAGES) & 1) ^ 1);
+                    ok = all(warp_wait(empty(s), ((it / STAGES) & 1) ^ 1));
                     if (!ok) break;
                     const uint32_t dst = sbase + s * STAGE_BYTES;
                     if (a.row_token) {
@@ -256,6 +255,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------- MMA
+            // One wait a block: its stage counts the promotion of the block two before it, which had the same
+            // accumulator, beside its operands. (With a barrier each the tensor core stood still 200 cycles a block: it takes
+            // instructions only a few ahead, and a wait behind them costs as much when it is over already.)
             uint32_t it = 0;
             bool ok = true;
             while (ok && next_item(item)) {
@@ -263,8 +265,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const uint32_t idesc = two ? idesc_dense(0u, 0u, BM, BN) : idesc_dense(0u, 0u, BM, 128);
                 for (int kb = kb0; kb < kb1; kb++, it++) {
                     const int b = it & 1, s = it % STAGES;
-                    ok = warp_wait(full(s), (it / STAGES) & 1) && warp_wait(tempty(b), ((it >> 1) & 1) ^ 1);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = all(warp_wait(full(s), (it / STAGES) & 1));
                     if (!ok) break;
                     if (a.row_token) fence_proxy_async_smem();               // the gathered rows came by the generic proxy
                     tc_fence_after();
@@ -371,6 +372,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (a.tokens) read_group(kb0);
         };
         na = nw0 = nw1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (lane == 0) {                                      // the first two blocks find their accumulators empty
+            mbar_arrive(full(0));
+            mbar_arrive(full(1));
+        }
         uint32_t it = 0;
         int done = 0;
         bool ok = true, synced = false;
@@ -398,7 +403,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     s1 = make_float4(na.x * nw1.x, na.y * nw1.y, na.z * nw1.z, na.w * nw1.w);
                     if (kb + 4 < kb1 && a.tokens) read_group(kb + 4);
                 }
-                ok = warp_wait(tfull(b), (it >> 1) & 1);
+                ok = all(warp_wait(tfull(b), (it >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 if (active) {
@@ -420,13 +425,13 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty(b));                // all of it is in registers
+                    if (lane == 0) mbar_arrive(full((it + 2) % STAGES));                // all of it is in registers
 #pragma unroll
                     for (int i = 0; i < 32; i++) fma1(acc[96 + i], x[i], s1.x);
                 } else {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty(b));
+                    if (lane == 0) mbar_arrive(full((it + 2) % STAGES));
                 }
                 s0 = make_float4(s0.y, s0.z, s0.w, 0.0f);
                 s1 = make_float4(s1.y, s1.z, s1.w, 0.0f);
