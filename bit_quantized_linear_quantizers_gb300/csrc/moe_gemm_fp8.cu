@@ -42,7 +42,7 @@ constexpr int BM = 128, BN = 256, BK = 128, STAGES = 4;
 constexpr int A_BYTES = BM * BK, HALF_BYTES = 128 * BK;
 constexpr int STAGE_BYTES = A_BYTES + 2 * HALF_BYTES;
 constexpr int FEED_WARPS = 8, EPI_WARPS = 8, THREADS = (FEED_WARPS + EPI_WARPS) * 32;
-constexpr int REGS_FEED = 48, REGS_EPI = 208;     // 256 * 48 + 256 * 208 = 512 * 128, what the CTA is launched with
+constexpr int REGS_FEED = 72, REGS_EPI = 184;     // 256 * 72 + 256 * 184 = 512 * 128, what the CTA is launched with
 constexpr int INFO = 4;                           // items in flight
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int STG_WARP = 32 * 128;                // a warp's output: 32 rows of 64 bf16
@@ -106,18 +106,12 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ int one(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int one(int v) { return __reduce_max_sync(0xffffffffu, v); }
 __device__ __forceinline__ bool all(bool v) { return __all_sync(0xffffffffu, v); }
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
 // An expert's rows, cut to those that exist.
 __device__ __forceinline__ int2 expert_rows(const MoeGemmArgs& a, int e) {
     const int R = (int)a.rows, b = min(max(a.offsets[e], 0), R);
@@ -147,8 +141,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     // the warp's, and the operands of its tensor instructions stay in uniform registers.
     const int warp = one(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nkb = a.K / BK;
-    const int rank = splits > 1 ? one(cluster_rank()) : 0;
-    const int kb0 = one(nkb * rank / splits), kb1 = one(nkb * (rank + 1) / splits);
+    const int rank = (int)(blockIdx.x % splits);                    // in the cluster
+    const int kb0 = nkb * rank / splits, kb1 = nkb * (rank + 1) / splits;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -593,7 +587,7 @@ qz_status moe_gemm_fp8_launch(const MoeGemmArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.x = splits;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
     const cudaError_t r = a.Y ? cudaLaunchKernelEx(&cfg, moe_gemm_kernel<false>, ta, tb, ty, a, nt, splits)
                               : cudaLaunchKernelEx(&cfg, moe_gemm_kernel<true>, ta, tb, ty, a, nt, splits);
     return r == cudaSuccess ? launch_status() : QZ_ERR_CUDA;
