@@ -28,12 +28,12 @@ namespace qz {
 
 namespace {
 
-constexpr int kWarps = 32, kThreads = kWarps * 32;
-constexpr int kAlone = 128;                                    // tokens that one CTA takes by itself
-constexpr int kMinTokens = 64, kMaxBlocks = 256;               // else: tokens a CTA at least, CTAs at most
-constexpr int kPlaceThreads = 512;
+constexpr int kThreads = 1024, kManyWarps = 16;                // of the selection: at most; of one among several CTAs
+constexpr int kAlone = 16;                                     // tokens that one CTA takes by itself
+constexpr int kMaxBlocks = 304;                                // two CTAs of kManyWarps an SM
+constexpr int kPlaceThreads = 512, kParts = 16;                // threads that share an expert's counts, at most
 constexpr uint32_t kFull = 0xffffffffu;
-static_assert(kThreads >= kMoeMaxExperts && kPlaceThreads >= kMoeMaxExperts, "a thread per expert");
+static_assert(kManyWarps * 32 >= kMoeMaxExperts && kPlaceThreads >= kMoeMaxExperts, "a thread per expert");
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_bits_to_f32(*p); }
@@ -52,7 +52,7 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 
 __device__ __forceinline__ float sigmoid(float l) {
     const float e = expf(-fabsf(l));
-    return __fdiv_rn(l >= 0.0f ? 1.0f : e, 1.0f + e);
+    return __fdividef(l >= 0.0f ? 1.0f : e, 1.0f + e);
 }
 __device__ __forceinline__ double sigmoid(double l) {
     const double e = exp(-fabs(l));
@@ -84,41 +84,50 @@ __device__ __forceinline__ void merge2(V& b, V& s, V ob, V os) {
 
 // How far two keys may seem from each other by rounding, over the difference that they have: in units of 2^-24 of the
 // largest score, twice: the argument of a softmax term's exponential up to 104 (one unit for each e-fold below
-// the largest), expf 4, the sum over 16 + 5 terms, product and reciprocal 3; a sigmoid has expf, sum and quotient.
+// the largest), expf 4, the sum over 16 + 5 terms, product and reciprocal 3; a sigmoid has 1.5 + 1 + 4.
 // The sum with the bias adds a unit of each key.
 __device__ __forceinline__ float margin(float most, float key, bool softmax) {
-    return most * ((softmax ? 2 * 132.0f : 2 * 8.0f) * 0x1p-24f) + fabsf(key) * 0x1p-22f;
+    return most * ((softmax ? 2 * 132.0f : 2 * 7.0f) * 0x1p-24f) + fabsf(key) * 0x1p-22f;
 }
 
-// The choice of one token in 64 bits, every term of it. Lane j gets the j-th expert, -1: none.
-template <typename T>
-__device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_moe_routing* rt, int lane, double* keys) {
+// The choice of one token in 64 bits, every term of it, EPL experts a lane. Lane j gets the j-th expert, -1: none.
+template <typename T, int EPL>
+__device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_moe_routing* rt, int lane) {
     const qz_moe_routing r = *rt;
-    double most = -FLT_MAX, sum = 0.0;
-    if (r.score == QZ_SCORE_SOFTMAX) {
-        for (int e = lane; e < r.experts; e += 32) most = fmax(most, (double)finite(load_logit(row + e)));
-        most = warp_most(most);
-        for (int e = lane; e < r.experts; e += 32) sum += exp((double)finite(load_logit(row + e)) - most);
-        sum = warp_sum(sum);
+    double key[EPL], most = -FLT_MAX, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; i++) {
+        const int e = lane + 32 * i;
+        key[i] = e < r.experts ? (double)finite(load_logit(row + e)) : (double)-INFINITY;
+        most = fmax(most, key[i]);
     }
-    auto key_of = [&](int e) {
-        const float l = finite(load_logit(row + e)), b = bias ? finite(bias[e]) : 0.0f;
-        if (l == -INFINITY || b == -INFINITY) return (double)-INFINITY;
-        return (r.score == QZ_SCORE_SOFTMAX ? exp((double)l - most) / sum : sigmoid((double)l)) + (double)b;
-    };
-    uint32_t kept = 0xffffffffu;
-    const int size = r.experts / r.groups;
+    const bool soft = r.score == QZ_SCORE_SOFTMAX;
+    if (soft) most = warp_most(most);
+#pragma unroll 1
+    for (int i = 0; i < EPL; i++) sum += soft ? exp(key[i] - most) : 0.0;
+    if (soft) sum = warp_sum(sum);
+#pragma unroll 1
+    for (int i = 0; i < EPL; i++) {
+        const int e = lane + 32 * i;
+        const float b = bias && e < r.experts ? finite(bias[e]) : 0.0f;
+        const bool open = key[i] > -INFINITY && b > -INFINITY;
+        const double s = soft ? exp(key[i] - most) / sum : sigmoid(key[i]);
+        key[i] = open ? s + (double)b : -INFINITY;
+    }
     if (r.groups > 1) {
+        const int size = r.experts / r.groups;
         double mine = -INFINITY;                               // lane g: the score of group g
         for (int g = 0; g < r.groups; g++) {
             double b = -INFINITY, s = -INFINITY;
-            for (int e = g * size + lane; e < (g + 1) * size; e += 32) merge2<double>(b, s, key_of(e), -INFINITY);
+#pragma unroll
+            for (int i = 0; i < EPL; i++)
+                if ((lane + 32 * i) / size == g) merge2<double>(b, s, key[i], -INFINITY);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 merge2<double>(b, s, __shfl_xor_sync(kFull, b, o), __shfl_xor_sync(kFull, s, o));
             if (lane == g) mine = r.group_best == 2 && s > -INFINITY ? b + s : b;
         }
-        kept = 0;
+        uint32_t kept = 0;
         for (int n = 0; n < r.top_groups; n++) {
             const double top = warp_most(mine);
             const uint32_t who = __ballot_sync(kFull, mine == top && top > -INFINITY);
@@ -126,29 +135,34 @@ __device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_
             kept |= who & -who;
             if (lane == __ffs(who) - 1) mine = -INFINITY;
         }
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            const int e = lane + 32 * i;
+            if (!(kept >> min(e / size, 31) & 1)) key[i] = -INFINITY;
+        }
+    }
+    if (!bias) {                                               // inside the groups logits decide
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (key[i] > -INFINITY) key[i] = (double)finite(load_logit(row + lane + 32 * i));
     }
     int chosen = -1;
-    double last = INFINITY;                                    // key and index of the choice before: the next is behind it
-    int last_e = -1;
     for (int j = 0; j < r.top_k; j++) {
         double best = -INFINITY;
         int at = INT_MAX;
-        for (int e = lane; e < r.experts; e += 32) {
-            if (!(kept >> (r.groups > 1 ? e / size : 0) & 1)) continue;
-            double k = key_of(e);
-            if (!bias && k > -INFINITY) k = (double)finite(load_logit(row + e));       // inside the groups logits decide
-            const bool behind = k < last || (k == last && e > last_e);
-            if (behind && k > best) {
-                best = k;
-                at = e;
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (key[i] > best) {
+                best = key[i];
+                at = lane + 32 * i;
             }
-        }
         const double top = warp_most(best);
         if (top == -INFINITY) break;
         at = __reduce_min_sync(kFull, best == top ? at : INT_MAX);
         if (lane == j) chosen = at;
-        last = top;
-        last_e = at;
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (lane + 32 * i == at) key[i] = -INFINITY;
     }
     return chosen;
 }
@@ -171,14 +185,42 @@ __device__ __noinline__ int sort_wide(const T* row, const float* bias, int id, i
     return got;
 }
 
+// A score for comparisons alone. The fast exponential is off by 2 + 1.16 |l| units in the last place, of which s (1 - s), at
+// most a quarter, reaches s: 1.5 units of 2^-24 of the largest score.
+__device__ __forceinline__ float key_sigmoid(float l) {
+    const float e = __expf(-fabsf(l));
+    return __fdividef(l >= 0.0f ? 1.0f : e, 1.0f + e);
+}
+
+// A lane's two best experts (register numbers a1, a2) of those behind (key ck, register ci): smaller keys, and equal ones
+// of larger index. A key of 0: there is none.
+template <int EPL>
+__device__ __forceinline__ void best_two(const uint32_t (&key)[EPL], uint32_t ck, int ci, uint32_t& b1, int& a1, uint32_t& b2, int& a2) {
+    b1 = b2 = 0;
+    a1 = a2 = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; i++) {
+        const uint32_t v = key[i] < ck || (key[i] == ck && i > ci) ? key[i] : 0u;
+        if (v > b1) {
+            b2 = b1;
+            a2 = a1;
+            b1 = v;
+            a1 = i;
+        } else if (v > b2) {
+            b2 = v;
+            a2 = i;
+        }
+    }
+}
+
 // The choice of one token. l: the lane's logits, finite or -inf.
-template <typename T, int EPL>
+template <typename T, int EPL, bool SIMPLE>
 __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL], const T* row, const float* bias,
                                     const qz_moe_routing& r, int lane, uint32_t* keys) {
-    const bool grouped = r.groups > 1, soft = r.score == QZ_SCORE_SOFTMAX;
+    const bool grouped = !SIMPLE && r.groups > 1, soft = r.score == QZ_SCORE_SOFTMAX;
     uint32_t key[EPL];
     float most = 1.0f;                                         // no score is larger
-    if (!bias && !grouped) {
+    if (SIMPLE || (!bias && !grouped)) {
 #pragma unroll
         for (int i = 0; i < EPL; i++) key[i] = l[i] == -INFINITY ? 0u : ordered(l[i]);
     } else {
@@ -196,7 +238,7 @@ __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL]
         }
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            const float v = soft ? s[i] * inv : sigmoid(l[i]);
+            const float v = soft ? s[i] * inv : key_sigmoid(l[i]);
             key[i] = l[i] == -INFINITY || b[i] == -INFINITY ? 0u : ordered(fminf(v + b[i], FLT_MAX));
         }
     }
@@ -236,32 +278,28 @@ __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL]
                 if (lane == first) mine = 0;
             }
         }
-        // without a bias and by one logit a group the comparison of the keys was that of scores, which may be equal in 32
-        // bits where the logits are not
-        if (close) return pick_wide<T>(row, bias, &r, lane, nullptr);
+        if (close) return pick_wide<T, EPL>(row, bias, &r, lane);
+        const float per = 1.0f / (float)size;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            const int e = lane + 32 * i;
-            if (!(kept >> min(e / size, 31) & 1)) key[i] = 0u;
+            // its group: e / size, exact for such small numbers half a step away from the next quotient
+            const int of = __float2int_rd(((float)(lane + 32 * i) + 0.5f) * per);
+            if (!(kept >> min(of, 31) & 1)) key[i] = 0u;
             else if (!bias && key[i]) key[i] = ordered(l[i]);  // inside the groups logits decide
         }
     }
     int chosen = -1, n = 0, more = INT_MAX;                    // more: choices wanted beyond the last one that was clear
     bool close = false;
     float last = 0.0f, kth = 0.0f;
+    // every lane's two best at hand: rarely more of the chosen lie in one lane, and it looks again
+    uint32_t b1, b2, ck = 0xffffffffu;
+    int a1, a2, ci = EPL, left = 2;
+    best_two<EPL>(key, ck, ci, b1, a1, b2, a2);
     for (int j = 0; j < 32; j++) {
-        if (j == r.top_k && !bias) break;
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        const uint32_t top = __reduce_max_sync(kFull, best);
+        if (j == r.top_k && (SIMPLE || !bias)) break;
+        const uint32_t top = __reduce_max_sync(kFull, b1);
         if (!top) break;
-        if (bias) {
+        if (!SIMPLE && bias) {
             const float v = unordered(top);
             const bool near = j > 0 && !(last - v > margin(most, fmaxf(fabsf(last), fabsf(v)), soft));
             if (j < r.top_k) close |= near;
@@ -272,15 +310,23 @@ __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL]
             if (j == r.top_k - 1) kth = v;
             if (j == 31) more = 0;
         }
-        const int e = __reduce_min_sync(kFull, best == top ? lane + 32 * at : INT_MAX);
+        const int e = __reduce_min_sync(kFull, b1 == top ? lane + 32 * a1 : INT_MAX);
         if (lane == j) chosen = e;
         n++;
-#pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (lane + 32 * i == e) key[i] = 0u;
+        if ((e & 31) == lane) {
+            ck = b1;
+            ci = a1;
+            b1 = b2;
+            a1 = a2;
+            left--;
+        }
+        if (__any_sync(kFull, left == 0) && left == 0) {
+            best_two<EPL>(key, ck, ci, b1, a1, b2, a2);
+            left = 2;
+        }
     }
-    if (close) {
-        if (soft || more == 0) return pick_wide<T>(row, bias, &r, lane, nullptr);
+    if (!SIMPLE && close) {
+        if (soft || more == 0) return pick_wide<T, EPL>(row, bias, &r, lane);
         chosen = sort_wide<T>(row, bias, chosen, n, lane);
     }
     return lane < r.top_k ? chosen : -1;
@@ -315,36 +361,64 @@ __device__ __forceinline__ float weight_of(const float (&l)[EPL], float l0, bool
     return there ? sigmoid(l0) * r.scale : 0.0f;
 }
 
-// Dynamic shared memory: counts [warps][experts], then with groups the keys of each warp [warps][experts + experts / 32].
+// Dynamic shared memory: counts [warps][experts], then with groups the keys of each warp.
 __host__ __device__ __forceinline__ int key_words(int experts) { return experts + (experts >> 5) + 1; }
+// A CTA's counts in the workspace: experts, rounded up to reads of four.
+__host__ __device__ __forceinline__ int count_words(int experts) { return (experts + 3) & ~3; }
 
-template <typename T, int EPL>
+// Exclusive sums over the CTA's threads, and the sum of all.
+__device__ __forceinline__ int scan(int mine, int* s_scan, int& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) s_scan[warp] = v;
+    __syncthreads();
+    const int w = lane < (int)(blockDim.x >> 5) ? s_scan[lane] : 0;
+    total = __reduce_add_sync(kFull, w);
+    return __reduce_add_sync(kFull, lane < warp ? w : 0) + v - mine;
+}
+
+// SIMPLE: neither a bias nor groups.
+template <typename T, int EPL, bool SIMPLE>
 __global__ void __launch_bounds__(kThreads)
 moe_select_kernel(const __grid_constant__ RouteArgs a, const int per_warp, int* __restrict__ block_counts) {
     extern __shared__ int s_dyn[];
-    __shared__ int s_scan[kWarps];
+    __shared__ int s_scan[kThreads / 32];
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.r.experts, k = a.r.top_k;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, E = a.r.experts, k = a.r.top_k;
+    const int tokens = (int)a.tokens;
     int* count = s_dyn + warp * E;                             // pairs per expert, then those of the warps before
-    uint32_t* keys = reinterpret_cast<uint32_t*>(s_dyn + kWarps * E) + warp * key_words(E);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(s_dyn + warps * E) + warp * key_words(E);
     const bool alone = gridDim.x == 1;
+    const float* bias = SIMPLE ? nullptr : a.bias;
     for (int e = lane; e < E; e += 32) count[e] = 0;
     __syncwarp();
-    int64_t live = a.tokens;
-    if (a.n_tokens) live = min(live, (int64_t)max(*a.n_tokens, 0));
+    const int live = a.n_tokens ? min(tokens, max(*a.n_tokens, 0)) : tokens;
     float b[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; i++) b[i] = a.bias && lane + 32 * i < E ? finite(a.bias[lane + 32 * i]) : 0.0f;
-    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * per_warp, t1 = min(t0 + per_warp, a.tokens);
-    for (int64_t t = t0; t < t1; t++) {
+    for (int i = 0; i < EPL; i++) b[i] = bias && lane + 32 * i < E ? finite(bias[lane + 32 * i]) : 0.0f;
+    const int t0 = (int)min(((int64_t)blockIdx.x * warps + warp) * per_warp, a.tokens), t1 = (int)min((int64_t)t0 + per_warp, a.tokens);
+    auto logits_of = [&](int t, float (&l)[EPL]) {
+        const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) l[i] = lane + 32 * i < E ? finite(load_logit(row + lane + 32 * i)) : -INFINITY;
+    };
+    float next[EPL];
+    if (t0 < min(t1, live)) logits_of(t0, next);
+    for (int t = t0; t < t1; t++) {
         int id = -1, rank = -1;
         float w = 0.0f;
         if (t < live) {
             const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
             float l[EPL];
 #pragma unroll
-            for (int i = 0; i < EPL; i++) l[i] = lane + 32 * i < E ? finite(load_logit(row + lane + 32 * i)) : -INFINITY;
-            id = pick<T, EPL>(l, b, row, a.bias, a.r, lane, keys);
+            for (int i = 0; i < EPL; i++) l[i] = next[i];
+            if (t + 1 < min(t1, live)) logits_of(t + 1, next);
+            id = pick<T, EPL, SIMPLE>(l, b, row, bias, a.r, lane, keys);
             const bool there = id >= 0;
             w = weight_of<EPL>(l, there ? finite(load_logit(row + id)) : 0.0f, there, a.r);
             // a token's choices are different experts: no two lanes meet at a counter
@@ -355,139 +429,133 @@ moe_select_kernel(const __grid_constant__ RouteArgs a, const int per_warp, int* 
             __syncwarp();
         }
         if (lane < k) {
-            a.ids[t * k + lane] = id;
-            a.weights[t * k + lane] = w;
-            a.token_row[t * k + lane] = rank;                  // among the warp's pairs of the expert
+            const uint32_t at = (uint32_t)t * k + lane;
+            a.ids[at] = id;
+            a.weights[at] = w;
+            a.token_row[at] = rank;                            // among the warp's pairs of the expert
         }
     }
     __syncthreads();
-    int mine = 0;                                              // thread e: the CTA's pairs of expert e
+    int mine = 0;                                              // thread e: the CTA's pairs of expert e (there is one for each)
     const int e = threadIdx.x;
     if (e < E) {
 #pragma unroll 8
-        for (int w = 0; w < kWarps; w++) {
-            const int c = s_dyn[w * E + e];
+        for (int w = 0; w < warps; w++) {
+            const int v = s_dyn[w * E + e];
             s_dyn[w * E + e] = mine;
-            mine += c;
+            mine += v;
         }
+        if (!alone) block_counts[(int64_t)blockIdx.x * count_words(E) + e] = mine;
+    } else if (!alone && e < count_words(E)) {
+        block_counts[(int64_t)blockIdx.x * count_words(E) + e] = 0;
     }
     int total = 0;
     if (alone) {
-        // offsets: exclusive sums over the experts
-        int v = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, v, o);
-            if (lane >= o) v += u;
-        }
-        if (lane == 31) s_scan[warp] = v;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < kWarps; w++) {
-            before += w < warp ? s_scan[w] : 0;
-            total += s_scan[w];
-        }
-        const int off = before + v - mine;
+        const int off = scan(mine, s_scan, total);
         if (e < E) {
             a.offsets[e] = off;
 #pragma unroll 8
-            for (int w = 0; w < kWarps; w++) s_dyn[w * E + e] += off;
+            for (int w = 0; w < warps; w++) s_dyn[w * E + e] += off;
         }
         if (e == 0) a.offsets[E] = total;
-    } else if (e < E) {
-        block_counts[(int64_t)blockIdx.x * E + e] = mine;
     }
     __syncthreads();
     // from ranks in the warp to ranks in the CTA, or rows
-    for (int64_t i = t0 * k + lane; i < t1 * k; i += 32) {
+    for (uint32_t i = (uint32_t)t0 * k + lane; i < (uint32_t)t1 * k; i += 32) {
         const int id = a.ids[i];
         if (id < 0) continue;
         const int row = count[id] + a.token_row[i];
         a.token_row[i] = row;
-        if (alone) a.row_token[row] = (int32_t)(i / k);
+        if (alone) a.row_token[row] = (int32_t)(i / (uint32_t)k);
     }
     if (alone)
-        for (int64_t i = total + threadIdx.x; i < a.tokens * k; i += kThreads) a.row_token[i] = -1;
+        for (uint32_t i = total + threadIdx.x; i < (uint32_t)tokens * k; i += blockDim.x) a.row_token[i] = -1;
     pdl_trigger();
 }
 
 // Rows of the pairs of one CTA of the selection, from the counts of all of them.
 __global__ void __launch_bounds__(kPlaceThreads)
 moe_place_kernel(const __grid_constant__ RouteArgs a, const int block_tokens, const int* __restrict__ block_counts) {
-    __shared__ int s_all[kPlaceThreads], s_before[kPlaceThreads];
+    __shared__ __align__(16) int s_all[kParts * kMoeMaxExperts], s_before[kParts * kMoeMaxExperts];
     __shared__ int s_base[kMoeMaxExperts];
     __shared__ int s_scan[kPlaceThreads / 32];
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.r.experts, k = a.r.top_k;
-    // `parts` threads share an expert's column of counts
-    const int parts = kPlaceThreads / E, part = threadIdx.x / E, e = threadIdx.x % E;
-    int all = 0, before = 0;
+    const int E = a.r.experts, words = count_words(E), quads = words >> 2;
+    const uint32_t k = a.r.top_k;
+    // `parts` threads share four experts' columns of counts
+    const int parts = min(kParts, kPlaceThreads / quads), part = threadIdx.x / quads, quad = threadIdx.x % quads;
+    // the first pair of each thread, in flight beside the counts
+    const uint32_t n = (uint32_t)a.tokens * k, i0 = (uint32_t)blockIdx.x * block_tokens * k, i1 = min(i0 + (uint32_t)block_tokens * k, n);
+    int id = -1, rank = 0;
+    if (i0 + threadIdx.x < i1) {
+        id = a.ids[i0 + threadIdx.x];
+        rank = a.token_row[i0 + threadIdx.x];
+    }
     if (part < parts) {
+        int4 all = make_int4(0, 0, 0, 0), before = all;
+        const int4* at = reinterpret_cast<const int4*>(block_counts) + part * quads + quad;
 #pragma unroll 8
-        for (int b = part; b < (int)gridDim.x; b += parts) {
-            const int c = block_counts[(int64_t)b * E + e];
-            before += b < (int)blockIdx.x ? c : 0;
-            all += c;
+        for (int b = part; b < (int)gridDim.x; b += parts, at += parts * quads) {
+            const int4 c = *at;
+            const int m = b < (int)blockIdx.x ? -1 : 0;
+            before = make_int4(before.x + (c.x & m), before.y + (c.y & m), before.z + (c.z & m), before.w + (c.w & m));
+            all = make_int4(all.x + c.x, all.y + c.y, all.z + c.z, all.w + c.w);
         }
+        reinterpret_cast<int4*>(s_all)[part * quads + quad] = all;
+        reinterpret_cast<int4*>(s_before)[part * quads + quad] = before;
     }
-    s_all[threadIdx.x] = all;
-    s_before[threadIdx.x] = before;
     __syncthreads();
-    all = before = 0;
-    if (threadIdx.x < E)
+    int all = 0, before = 0;
+    const int e = threadIdx.x;
+    if (e < E)
         for (int p = 0; p < parts; p++) {
-            all += s_all[p * E + threadIdx.x];
-            before += s_before[p * E + threadIdx.x];
+            all += s_all[p * words + e];
+            before += s_before[p * words + e];
         }
-    int v = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v += u;
-    }
-    if (lane == 31) s_scan[warp] = v;
-    __syncthreads();
-    int total = 0, warps_before = 0;
-#pragma unroll
-    for (int w = 0; w < kPlaceThreads / 32; w++) {
-        warps_before += w < warp ? s_scan[w] : 0;
-        total += s_scan[w];
-    }
-    const int off = warps_before + v - all;
-    if (threadIdx.x < E) s_base[threadIdx.x] = off + before;
+    int total;
+    const int off = scan(all, s_scan, total);
+    if (e < E) s_base[e] = off + before;
     if (blockIdx.x == 0) {
-        if (threadIdx.x < E) a.offsets[threadIdx.x] = off;
-        if (threadIdx.x == 0) a.offsets[E] = total;
+        if (e < E) a.offsets[e] = off;
+        if (e == 0) a.offsets[E] = total;
     }
     __syncthreads();
-    const int64_t n = a.tokens * k, i0 = (int64_t)blockIdx.x * block_tokens * k, i1 = min(i0 + (int64_t)block_tokens * k, n);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kPlaceThreads) {
-        const int id = a.ids[i];
-        if (id < 0) continue;
-        const int row = s_base[id] + a.token_row[i];
-        a.token_row[i] = row;
-        a.row_token[row] = (int32_t)(i / k);
+    for (uint32_t i = i0 + threadIdx.x; i < i1;) {
+        if (id >= 0) {
+            const int row = s_base[id] + rank;
+            a.token_row[i] = row;
+            a.row_token[row] = (int32_t)(i / k);
+        }
+        i += kPlaceThreads;
+        if (i < i1) {
+            id = a.ids[i];
+            rank = a.token_row[i];
+        }
     }
-    for (int64_t i = total + (int64_t)blockIdx.x * kPlaceThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kPlaceThreads) a.row_token[i] = -1;
+    for (uint32_t i = total + blockIdx.x * kPlaceThreads + threadIdx.x; i < n; i += gridDim.x * kPlaceThreads) a.row_token[i] = -1;
     pdl_trigger();
 }
 
-// Tokens a warp and CTAs. One CTA up to kAlone tokens; more CTAs than kMaxBlocks would read too many counts.
+// Warps a CTA, tokens a warp and CTAs. One CTA up to kAlone tokens; more CTAs than kMaxBlocks would read too many counts.
 struct Split {
-    int per_warp, blocks;
+    int warps, per_warp, blocks;
 };
-Split split_of(int64_t tokens) {
-    if (tokens <= kAlone) return {(int)std::max<int64_t>(1, (tokens + kWarps - 1) / kWarps), 1};
-    const int64_t block = std::max<int64_t>(kMinTokens, (tokens + kMaxBlocks - 1) / kMaxBlocks);
-    const int per_warp = (int)((block + kWarps - 1) / kWarps);
-    return {per_warp, (int)((tokens + (int64_t)per_warp * kWarps - 1) / ((int64_t)per_warp * kWarps))};
+Split split_of(int64_t tokens, int64_t experts) {
+    if (tokens <= kAlone) {
+        const int warps = (int)std::max<int64_t>((experts + 31) / 32, std::min<int64_t>(tokens, kThreads / 32));
+        return {warps, (int)std::max<int64_t>(1, (tokens + warps - 1) / warps), 1};
+    }
+    const int per_warp = (int)((tokens + (int64_t)kManyWarps * kMaxBlocks - 1) / ((int64_t)kManyWarps * kMaxBlocks));
+    return {kManyWarps, per_warp, (int)((tokens + (int64_t)per_warp * kManyWarps - 1) / ((int64_t)per_warp * kManyWarps))};
 }
 
 template <typename T, int EPL>
 qz_status select_kernel(const RouteArgs& a, const Split& s, int* counts, cudaStream_t st) {
-    const int words = kWarps * (a.r.experts + (a.r.groups > 1 ? key_words(a.r.experts) : 0));
-    if (words * 4 > 48 * 1024) QZ_TRY(opt_in_smem((const void*)moe_select_kernel<T, EPL>, words * 4));
-    return launch_pdl(moe_select_kernel<T, EPL>, dim3(s.blocks), dim3(kThreads), words * 4, st, a, s.per_warp, counts);
+    const bool simple = !a.bias && a.r.groups == 1;
+    const auto fn = simple ? moe_select_kernel<T, EPL, true> : moe_select_kernel<T, EPL, false>;
+    const int bytes = 4 * s.warps * (a.r.experts + (a.r.groups > 1 ? key_words(a.r.experts) : 0));
+    if (bytes > 48 * 1024) QZ_TRY(opt_in_smem((const void*)fn, bytes));
+    return launch_pdl(fn, dim3(s.blocks), dim3(s.warps * 32), bytes, st, a, s.per_warp, counts);
 }
 
 template <typename T>
@@ -502,16 +570,16 @@ qz_status select_launch(const RouteArgs& a, const Split& s, int* counts, cudaStr
 } // namespace
 
 size_t ws_moe_route(int64_t tokens, int64_t experts, int64_t) {
-    const Split s = split_of(tokens);
-    return s.blocks == 1 || experts < 1 ? 0 : (size_t)s.blocks * (size_t)experts * sizeof(int);
+    const Split s = split_of(tokens, experts);
+    return s.blocks == 1 || experts < 1 ? 0 : (size_t)s.blocks * count_words((int)experts) * sizeof(int);
 }
 
 qz_status moe_route_launch(const RouteArgs& a, qz_dtype lt, void* ws, cudaStream_t st) {
     int* counts = static_cast<int*>(ws);
-    const Split s = split_of(a.tokens);
+    const Split s = split_of(a.tokens, a.r.experts);
     QZ_TRY(lt == QZ_F32 ? select_launch<float>(a, s, counts, st) : select_launch<uint16_t>(a, s, counts, st));
     if (s.blocks == 1) return QZ_OK;
-    return launch_pdl(moe_place_kernel, dim3(s.blocks), dim3(kPlaceThreads), 0, st, a, s.per_warp * kWarps, (const int*)counts);
+    return launch_pdl(moe_place_kernel, dim3(s.blocks), dim3(kPlaceThreads), 0, st, a, s.per_warp * s.warps, (const int*)counts);
 }
 
 } // namespace qz
