@@ -954,6 +954,18 @@ def qz_attn_fp8_paged(q, cache: PagedKV, block_table, kv_lens, cu_q, max_q: int,
 
 # ------------------------------------------------- a block of experts in FP8
 
+def _matrix(x, name, d):
+    """(rows, columns, stride between rows) of a 2-D tensor with dense rows on device d."""
+    shape = x.shape
+    if len(shape) == 2 and x.get_device() == d:
+        rows, cols = shape
+        s0, s1 = x.stride()
+        if s1 == 1 or not rows or not cols:
+            return rows, cols, s0 if rows > 1 else max(cols, 1)
+    _on(x, name, d)
+    raise ValueError(f"{name}: expected a 2-D tensor with dense rows, got {tuple(shape)} with strides {tuple(x.stride())}")
+
+
 def qz_moe_route(logits, top_k: int, score: int = SCORE_SOFTMAX, renormalize: bool = True, scale: float = 1.0, bias=None,
                  groups: int = 1, top_groups: int = 1, group_best: int = 1, n_tokens=None, ids=None, weights=None,
                  offsets=None, row_token=None, token_row=None, ws=None, stream=None):
@@ -967,39 +979,44 @@ def qz_moe_route(logits, top_k: int, score: int = SCORE_SOFTMAX, renormalize: bo
             return qz_moe_route(logits, top_k, score, renormalize, scale, bias, groups, top_groups, group_best, n_tokens,
                                 ids, weights, offsets, row_token, token_row, ws)
     d = _device()
-    T, E, ld = _rows_cols_ld(logits)
+    T, E, ld = _matrix(logits, "logits", d)
     lt = _dtype_code(logits)
-    _on(logits, "logits", d)
     dev, n = logits.device, T * top_k
+    i32 = torch.int32
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        ids = torch.empty((T, top_k), dtype=i32, device=dev)
     if weights is None:
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     if offsets is None:
-        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+        offsets = torch.empty((E + 1,), dtype=i32, device=dev)
     if row_token is None:
-        row_token = torch.empty((n,), dtype=torch.int32, device=dev)
+        row_token = torch.empty((n,), dtype=i32, device=dev)
     if token_row is None:
-        token_row = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        token_row = torch.empty((T, top_k), dtype=i32, device=dev)
     r = _MoeRouting(E, top_k, score, 1 if renormalize else 0, scale, groups, top_groups, group_best)
-    args = (_opt(bias, "bias", d, torch.float32, E), None if n_tokens is None else _i32(n_tokens, "n_tokens", d, 1),
-            ctypes.byref(r), _i32(ids, "ids", d, n), _arg(weights, "weights", d, torch.float32, n),
-            _i32(offsets, "offsets", d, E + 1), _i32(row_token, "row_token", d, n), _i32(token_row, "token_row", d, n))
     buf, nb = _ws(ws, qz_workspace_size(OP_MOE_ROUTE, T, E, top_k), d)
-    st = lib.qz_moe_route(logits.data_ptr(), lt, T, ld, *args, _ptr(buf), nb, _raw_stream(None, d))
+    st = lib.qz_moe_route(logits.data_ptr(), lt, T, ld, None if bias is None else _arg(bias, "bias", d, torch.float32, E),
+                          None if n_tokens is None else _i32(n_tokens, "n_tokens", d, 1), r, _i32(ids, "ids", d, n),
+                          _arg(weights, "weights", d, torch.float32, n), _i32(offsets, "offsets", d, E + 1),
+                          _i32(row_token, "row_token", d, n), _i32(token_row, "token_row", d, n), _ptr(buf), nb,
+                          _raw_stream(None, d))
     if st:
         raise QZError(st, "qz_moe_route")
     return ids, weights, offsets, row_token, token_row
 
 
 def _experts(qA, sA, qW, sW, offsets, row_token, d):
-    if qW.dim() != 3 or qA.dim() != 2 or qA.shape[1] != qW.shape[2]:
-        raise ValueError(f"expected qA [tokens, K] and qW [experts, N, K], got {tuple(qA.shape)} and {tuple(qW.shape)}")
-    tokens, K = qA.shape
-    E, N, _ = qW.shape
-    rows = tokens if row_token is None else row_token.numel()
-    args = (_arg(qA, "qA", d, 1, tokens * K), _arg(sA, "sA", d, torch.float32, tokens * (K // 128)), tokens,
-            None if row_token is None else _i32(row_token, "row_token", d, rows), rows,
+    a, w = qA.shape, qW.shape
+    if len(w) != 3 or len(a) != 2 or a[1] != w[2]:
+        raise ValueError(f"expected qA [tokens, K] and qW [experts, N, K], got {tuple(a)} and {tuple(w)}")
+    tokens, K = a
+    E, N, _ = w
+    if row_token is None:
+        rows, p_row = tokens, None
+    else:
+        rows = row_token.numel()
+        p_row = _i32(row_token, "row_token", d, rows)
+    args = (_arg(qA, "qA", d, 1, tokens * K), _arg(sA, "sA", d, torch.float32, tokens * (K // 128)), tokens, p_row, rows,
             _i32(offsets, "offsets", d, E + 1), E, _arg(qW, "qW", d, 1, E * N * K),
             _arg(sW, "sW", d, torch.float32, E * (N // 128) * (K // 128)))
     return args, rows, N, K
@@ -1016,7 +1033,10 @@ def qz_moe_gemm_fp8(qA, sA, qW, sW, offsets, row_token=None, Y=None, stream=None
     args, rows, N, K = _experts(qA, sA, qW, sW, offsets, row_token, d)
     if Y is None:
         Y = torch.empty((rows, N), dtype=torch.bfloat16, device=qA.device)
-    st = lib.qz_moe_gemm_fp8(*args, _arg(Y, "Y", d, torch.bfloat16, rows * N), N, K, _raw_stream(None, d))
+        p_y = Y.data_ptr()
+    else:
+        p_y = _arg(Y, "Y", d, torch.bfloat16, rows * N)
+    st = lib.qz_moe_gemm_fp8(*args, p_y, N, K, _raw_stream(None, d))
     if st:
         raise QZError(st, "qz_moe_gemm_fp8")
     return Y
@@ -1064,34 +1084,42 @@ def qz_residual_rmsnorm(x, gamma=None, y=None, token_row=None, weights=None, alp
         with torch.cuda.stream(stream):
             return qz_residual_rmsnorm(x, gamma, y, token_row, weights, alpha, gamma_y, eps, out, normed, fp8)
     d = _device()
-    T, H, ldx = _rows_cols_ld(x)
-    xt = _dtype_code(x)
-    _on(x, "x", d)
+    T, H, ldx = _matrix(x, "x", d)
+    xt, dt, dev = _dtype_code(x), x.dtype, x.device
     block = None
     if y is not None:
         k = token_row.shape[1] if token_row is not None and token_row.dim() == 2 else (
             weights.shape[1] if weights is not None and weights.dim() == 2 else 1)
         block = _BlockOutput(y.data_ptr(), y.shape[0], _rows2(y, "y", d, H, torch.bfloat16), k,
                              None if token_row is None else _i32(token_row, "token_row", d, T * k),
-                             _opt(weights, "weights", d, torch.float32, T * k), alpha, _opt(gamma_y, "gamma_y", d, x.dtype, H))
+                             None if weights is None else _arg(weights, "weights", d, torch.float32, T * k), alpha,
+                             None if gamma_y is None else _arg(gamma_y, "gamma_y", d, dt, H))
     elif token_row is not None or weights is not None or gamma_y is not None:
         raise ValueError("token_row, weights and gamma_y belong to a block's output y")
+    ldo, p_out = H, None
     if out is True:
-        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    if normed is True:
-        normed = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    if fp8 is True:
-        fp8 = (torch.empty((T, H), dtype=torch.uint8, device=x.device),
-               torch.empty((T, H // 128), dtype=torch.float32, device=x.device))
-    codes, scales = fp8 if fp8 is not None else (None, None)
-    ldo = 0
-    if out is not None:
-        ldo = _rows2(out, "out", d, H, x.dtype)
+        out = torch.empty((T, H), dtype=dt, device=dev)
+        p_out = out.data_ptr()
+    elif out is not None:
+        ldo, p_out = _rows2(out, "out", d, H, dt), out.data_ptr()
         if out.shape[0] != T:
             raise ValueError(f"out: expected {T} rows, got {out.shape[0]}")
-    st = lib.qz_residual_rmsnorm(x.data_ptr(), xt, T, H, ldx, None if block is None else ctypes.byref(block), _ptr(out), ldo,
-                                 _opt(gamma, "gamma", d, x.dtype, H), eps, _opt(normed, "normed", d, torch.bfloat16, T * H),
-                                 _opt(codes, "codes", d, 1, T * H), _opt(scales, "scales", d, torch.float32, T * (H // 128)),
+    p_normed = None
+    if normed is True:
+        normed = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        p_normed = normed.data_ptr()
+    elif normed is not None:
+        p_normed = _arg(normed, "normed", d, torch.bfloat16, T * H)
+    codes = scales = p_codes = p_scales = None
+    if fp8 is True:
+        codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
+        scales = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+        p_codes, p_scales = codes.data_ptr(), scales.data_ptr()
+    elif fp8 is not None:
+        codes, scales = fp8
+        p_codes, p_scales = _arg(codes, "codes", d, 1, T * H), _arg(scales, "scales", d, torch.float32, T * (H // 128))
+    st = lib.qz_residual_rmsnorm(x.data_ptr(), xt, T, H, ldx, block, p_out, ldo,
+                                 None if gamma is None else _arg(gamma, "gamma", d, dt, H), eps, p_normed, p_codes, p_scales,
                                  _raw_stream(None, d))
     if st:
         raise QZError(st, "qz_residual_rmsnorm")
