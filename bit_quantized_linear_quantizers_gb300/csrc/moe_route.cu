@@ -8,9 +8,9 @@
 //
 // With a bias, and for groups, keys are rounded sums, and two that 32 bits cannot tell apart could change places. Every
 // comparison that decides something is checked against a bound on its rounding errors. Experts too close to
-// one another are compared again in 64 bits, a lane each (sort_wide; sigmoid only: a softmax needs all terms of its
-// sum again); a token whose groups are too close, or that has more such experts than lanes, is chosen in
-// 64 bits altogether (pick_wide). At 8000 tokens of 256 experts about one token in 200 is.
+// one another are compared again in 64 bits, a lane each (sort_wide), and so are the best of groups that are
+// (groups_wide). A softmax with a bias needs all terms of its sum again, and more such experts than lanes need all
+// keys: such a token is chosen in 64 bits altogether (pick_wide; 15 to 25 us, where the others take 3).
 //
 // The plan: the rows of an expert in the order of the tokens, whatever order CTAs run in. A
 // CTA counts its pairs per warp and expert and gives each pair its rank; the second kernel adds, per expert, the counts of
@@ -167,6 +167,50 @@ __device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_
     return chosen;
 }
 
+// The groups that are kept where some are too close to the border for 32 bits: those surely above it, and the best of
+// the near ones by their scores in 64 bits, of the keys that can be among their best. score: lane g has that of
+// group g; hi, lo: the last one kept and the first one not. Not for a softmax with a bias, whose terms need their sum.
+template <typename T>
+__device__ __noinline__ uint32_t groups_wide(const T* row, const float* bias, const qz_moe_routing* rt, int lane, const uint32_t* keys,
+                                             float score, float hi, float lo, float slack) {
+    const qz_moe_routing r = *rt;
+    const int size = r.experts / r.groups;
+    const bool open = score > -INFINITY, sure = open && score > hi + slack, near = open && !sure && score >= lo - slack;
+    const uint32_t surely = __ballot_sync(kFull, sure), nearly = __ballot_sync(kFull, near);
+    double most = -FLT_MAX;
+    if (r.score == QZ_SCORE_SOFTMAX) {
+        for (int e = lane; e < r.experts; e += 32) most = fmax(most, (double)finite(load_logit(row + e)));
+        most = warp_most(most);
+    }
+    double exact = -INFINITY;
+    for (uint32_t left = nearly; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        uint32_t b = 0, s = 0;
+        for (int e = g * size + lane; e < (g + 1) * size; e += 32) merge2<uint32_t>(b, s, keys[e + (e >> 5)], 0u);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) merge2<uint32_t>(b, s, __shfl_xor_sync(kFull, b, o), __shfl_xor_sync(kFull, s, o));
+        const float from = unordered(r.group_best == 2 && s ? s : b) - slack;
+        double eb = -INFINITY, es = -INFINITY;
+        for (int e = g * size + lane; e < (g + 1) * size; e += 32) {
+            const uint32_t k = keys[e + (e >> 5)];
+            if (!k || unordered(k) < from) continue;
+            const double l = (double)finite(load_logit(row + e));
+            merge2<double>(eb, es, (r.score == QZ_SCORE_SOFTMAX ? exp(l - most) : sigmoid(l)) + (bias ? (double)finite(bias[e]) : 0.0), -INFINITY);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) merge2<double>(eb, es, __shfl_xor_sync(kFull, eb, o), __shfl_xor_sync(kFull, es, o));
+        if (lane == g) exact = r.group_best == 2 && es > -INFINITY ? eb + es : eb;
+    }
+    int rank = __popc(surely);
+    for (uint32_t left = nearly; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        const double v = __shfl_sync(kFull, exact, g);
+        rank += v > exact || (v == exact && g < lane);
+    }
+    return surely | __ballot_sync(kFull, near && rank < r.top_groups);
+}
+
 // n candidates, one a lane, in the order of their keys in 64 bits: lane j gets the j-th.
 template <typename T>
 __device__ __noinline__ int sort_wide(const T* row, const float* bias, int id, int n, int lane) {
@@ -264,13 +308,18 @@ __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL]
             mine = ordered(r.group_best == 2 && second ? unordered(best) + unordered(second) : unordered(best));
         uint32_t kept = 0;
         float last = 0.0f;
-        bool close = false;
+        const uint32_t all = mine;
         for (int n = 0; n <= r.top_groups; n++) {
             const uint32_t top = __reduce_max_sync(kFull, mine);
             if (!top) break;
             const float v = unordered(top);
             if (n == r.top_groups) {
-                close = !(last - v > 2.0f * margin(most, fmaxf(fabsf(last), fabsf(v)), soft));
+                const float slack = 2.0f * margin(most, fmaxf(fabsf(last), fabsf(v)), soft);
+                if (!(last - v > slack)) {
+                    if (soft && bias) return pick_wide<T, EPL>(row, bias, &r, lane);
+                    const uint32_t u = __shfl_sync(kFull, all, min(lane, r.groups - 1) << share);
+                    kept = groups_wide<T>(row, bias, &r, lane, keys, lane < r.groups && u ? unordered(u) : -INFINITY, last, v, slack);
+                }
             } else {
                 const int first = __ffs(__ballot_sync(kFull, mine == top)) - 1;
                 kept |= 1u << (first >> share);
@@ -278,7 +327,6 @@ __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL]
                 if (lane == first) mine = 0;
             }
         }
-        if (close) return pick_wide<T, EPL>(row, bias, &r, lane);
         const float per = 1.0f / (float)size;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
