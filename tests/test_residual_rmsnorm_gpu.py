@@ -115,6 +115,16 @@ def test_rows_of_zeros_tiny_and_large_values():
     assert not got[2][0].any() and bool((got[3][0] == torch.tensor(1e-12, device="cuda") / torch.tensor(448.0, device="cuda")).all())
 
 
+def test_a_sum_of_squares_past_the_range_gives_zeros():
+    d = data(3, 256, 0, torch.float32, 15)
+    d["gamma_y"] = None
+    d["x"][1] *= 1e25                                            # squares past 3.4e38
+    for y in (d["y"], None):
+        got = qz.qz_residual_rmsnorm(d["x"], d["gamma"], y, normed=True, fp8=True)
+        assert not got[1][1].any() and not (got[2][1] & 0x7F).any()
+        assert bool(torch.isfinite(got[1].float()).all()) and bool(got[1][0].any())
+
+
 def test_nan_and_infinities_stay_in_their_row():
     d = data(8, 256, 2, torch.bfloat16, 14)
     d["token_row"] = torch.arange(16, dtype=torch.int32, device="cuda").view(8, 2)
