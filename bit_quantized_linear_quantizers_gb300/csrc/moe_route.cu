@@ -619,7 +619,7 @@ qz_status select_launch(const RouteArgs& a, const Split& s, int* counts, cudaStr
 
 size_t ws_moe_route(int64_t tokens, int64_t experts, int64_t) {
     const Split s = split_of(tokens, experts);
-    return s.blocks == 1 || experts < 1 ? 0 : (size_t)s.blocks * count_words((int)experts) * sizeof(int);
+    return s.blocks == 1 ? 0 : (size_t)s.blocks * count_words((int)experts) * sizeof(int);
 }
 
 qz_status moe_route_launch(const RouteArgs& a, qz_dtype lt, void* ws, cudaStream_t st) {

@@ -210,7 +210,8 @@ size_t qz_workspace_size(qz_op op, int64_t d0, int64_t d1, int64_t d2) {
     case QZ_OP_KV_WRITE_FP8_CHANNEL_ZP: return d0 >= 1 && d1 >= 1 && d2 >= 1 ? ws_kv_channel_zp(d0, d1, d2) : 0;
     case QZ_OP_COL_AMAX: return d0 >= 1 && d1 >= 1 ? ws_col_amax(d0, d1) : 0;
     case QZ_OP_ATTN_FP8_PAGED: return d0 >= 1 ? ws_attn_paged(d0, d1) : 0;
-    case QZ_OP_MOE_ROUTE: return d0 >= 0 && d0 < ((int64_t)1 << 31) && d1 <= kMoeMaxExperts ? ws_moe_route(d0, d1, d2) : 0;
+    case QZ_OP_MOE_ROUTE:
+        return d0 >= 0 && d0 < ((int64_t)1 << 31) && d1 >= 1 && d1 <= kMoeMaxExperts ? ws_moe_route(d0, d1, d2) : 0;
     case QZ_OP_PREPARE_FP4_SCALES:
         return d0 >= 1 && d0 <= (1 << 24) && d1 >= 1 && d1 <= (1 << 24) ? prepared_fp4_scale_bytes((int)d0, (int)d1, d2 != 0)
                                                                          : 0;

@@ -49,6 +49,13 @@ def test_route_arguments():
     assert qz.qz_workspace_size(qz.OP_MOE_ROUTE, 1 << 40, 64, 8) == 0
 
 
+def test_route_workspace_of_sizes_that_the_call_rejects():
+    for tokens in (0, 1, 16, 17, 100000, (1 << 31) - 1):
+        for experts in (-(1 << 40), -1, 0, 513, 1 << 40):
+            assert qz.qz_workspace_size(qz.OP_MOE_ROUTE, tokens, experts, 1) == 0
+    assert qz.qz_workspace_size(qz.OP_MOE_ROUTE, (1 << 31) - 1, 512, 1) <= 304 * 512 * 4
+
+
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_expert_product_validation(swiglu):
     f = qz.lib.qz_moe_gemm_fp8_swiglu if swiglu else qz.lib.qz_moe_gemm_fp8
