@@ -302,10 +302,11 @@ __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL]
             for (int e = g * size + (lane & (lanes - 1)); e < (g + 1) * size; e += lanes) merge2<uint32_t>(best, second, keys[e + (e >> 5)], 0u);
         for (int o = lanes >> 1; o > 0; o >>= 1)
             merge2<uint32_t>(best, second, __shfl_xor_sync(kFull, best, o), __shfl_xor_sync(kFull, second, o));
-        // a group's score as an ordered integer, in its first lane
+        // a group's score as an ordered integer, in its first lane; finite, so that differences are numbers: two that the
+        // limit makes equal are compared in 64 bits
         uint32_t mine = 0;
         if (g < r.groups && (lane & (lanes - 1)) == 0 && best)
-            mine = ordered(r.group_best == 2 && second ? unordered(best) + unordered(second) : unordered(best));
+            mine = ordered(r.group_best == 2 && second ? fmaxf(fminf(unordered(best) + unordered(second), FLT_MAX), -FLT_MAX) : unordered(best));
         uint32_t kept = 0;
         float last = 0.0f;
         const uint32_t all = mine;

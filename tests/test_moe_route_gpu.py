@@ -106,6 +106,26 @@ def test_masked_logits_and_biases():
     check(logits, k, sigmoid=True, bias=bias)
 
 
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("big", [math.inf, torch.finfo(torch.float32).max, 2.0 ** 127])
+@pytest.mark.parametrize("T", [3, 200])
+def test_group_scores_past_the_range_of_fp32(sigmoid, big, T):
+    """Two keys of a group whose sum is infinite in 32 bits: more such groups than are kept, as many, fewer; and the
+    same below zero, where the group stays open."""
+    g = gen(8)
+    logits = torch.randn((T, 64), generator=g, device="cuda")
+    for n in (1, 2, 3, 8):
+        for sign in (1.0, -1.0) if math.isfinite(big) else (1.0,):
+            bias = torch.zeros(64, device="cuda")
+            bias.view(8, 8)[8 - n:, 2:4] = sign * big
+            check(logits, 4, sigmoid, bias=bias, groups=8, top_groups=2, group_best=2)
+            bias.view(8, 8)[8 - n:] = sign * big
+            check(logits, 6, sigmoid, bias=bias, groups=8, top_groups=2, group_best=2)
+    bias = torch.zeros(64, device="cuda")
+    bias.view(8, 8)[:, 0] = big                                   # one such key a group: in 64 bits too, all sums are the same
+    check(logits, 4, sigmoid, bias=bias, groups=8, top_groups=2, group_best=2)
+
+
 def test_scores_that_underflow_keep_their_ratios():
     g = gen(4)
     logits = torch.randn((40, 32), generator=g, device="cuda") - 300.0
