@@ -49,7 +49,7 @@ constexpr int STG_WARP = 32 * 128;                // a warp's output: 32 rows of
 constexpr int STG_OFF = STAGES * STAGE_BYTES;
 constexpr int INFO_OFF = STG_OFF + EPI_WARPS * STG_WARP;
 constexpr int BAR_OFF = INFO_OFF + INFO * 16;
-constexpr int BARS = 2 * STAGES + 2 + 2 * INFO;
+constexpr int BARS = 2 * STAGES + 2 + 2 * INFO + 4;
 constexpr int SMEM_BYTES = BAR_OFF + BARS * 8 + 16 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of a CTA");
 constexpr int SPLIT_ROWS = 32, MAX_SPLITS = 4;    // rows of a shared item: one warp's lanes
@@ -140,6 +140,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     auto tfull = [&](int b) { return bars + 8 * (2 * STAGES + b); };
     auto ifull = [&](int i) { return bars + 8 * (2 * STAGES + 2 + i); };
     auto iempty = [&](int i) { return bars + 8 * (2 * STAGES + 2 + INFO + i); };
+    auto peaks = [&](int q) { return bars + 8 * (2 * STAGES + 2 + 2 * INFO + q); };
 
     // What a warp's lanes have in common goes through one(): loops and addresses that depend on it are then known to be
     // the warp's, and the operands of its tensor instructions stay in uniform registers.
@@ -158,6 +159,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(ifull(i), 1);
             mbar_init(iempty(i), 2 + 4 + EPI_WARPS);
         }
+        for (int q = 0; q < 4; q++) mbar_init(peaks(q), EPI_WARPS / 4);
         fence_barrier_init();
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
@@ -479,7 +481,11 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     }
                 }
                 peak[h * 128 + r] = am;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                // the two warps of these rows meet, with a limit: the other may have given up
+                __syncwarp();
+                if (lane == 0) mbar_arrive(peaks(q));
+                ok = all(warp_wait(peaks(q), done & 1));
+                if (!ok) break;
                 if (r < item.z) {
                     const float sc = div1(fmaxf(fmaxf(am, peak[(h ^ 1) * 128 + r]), kAmaxMin), Recip(kFp8Max));
                     const Recip d(sc);
