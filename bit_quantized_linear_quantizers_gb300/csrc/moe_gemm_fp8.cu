@@ -65,6 +65,15 @@ __device__ __forceinline__ void fma1(float& acc, uint32_t v, float s) {
     asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
 }
 
+// g / (1 + exp(-g)) in six instructions: 2^x and 1/x of the special-function unit in their forms without subnormals. exp(-g)
+// is 0 from g = 88 on, where 1 + exp(-g) is 1 long since, and the reciprocal is 0 above 2^126, where g's share is nothing.
+__device__ __forceinline__ float silu(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r;
+}
+
 // One block of K: D = A B^T of 128 x 128-byte and 256 x 128-byte tiles behind one another at `stage`, K = 32 bytes an
 // MMA, then arrivals on two barriers. The warp issues it converged, through an elected lane: operands of a branch of
 // one lane are moved to the uniform registers anew for every instruction (490 cycles a block so).
@@ -476,7 +485,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (active) {
 #pragma unroll
                     for (int i = 0; i < 64; i++) {
-                        acc[i] = __fdividef(acc[i], 1.0f + __expf(-acc[i])) * acc[64 + i];
+                        acc[i] = silu(acc[i]) * acc[64 + i];
                         am = fmaxf(am, fabsf(acc[i]));
                     }
                 }
