@@ -60,24 +60,15 @@ template <int REGS> __device__ __forceinline__ void reg_inc() { asm volatile("se
 template <int REGS> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 
 // A thread's sums: 64 columns of the first box, 64 of the second. add: += v * s for 32 of them from AT on; volatile, so
-// that it stays behind the wait for the reads of v. Paired instructions take half the issue slots, where the pairs stay in
-// place for the whole item: 398 -> 376 us for 4001 tokens by 2 of 8 experts [4096, 14336]. In SwiGLU's kernel they do not
-// (registers are moved or spilled: 318 -> 340), so that one adds lane by lane.
-template <bool PAIRED> struct Sums;
-template <> struct Sums<false> {
-    float a[128];
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < 128; i++) a[i] = 0.0f;
-    }
-    template <int AT> __device__ __forceinline__ void add(const uint32_t (&v)[32], float s) {
-#pragma unroll
-        for (int i = 0; i < 32; i++) asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(a[AT + i]) : "f"(__uint_as_float(v[i])), "f"(s));
-    }
-    __device__ __forceinline__ float (&values())[128] { return a; }
-};
-template <> struct Sums<true> {
+// that it stays behind the wait for the reads of v. Paired instructions take half the issue slots: lane by lane it was 396
+// instead of 374 us for 4001 tokens by 2 of 8 experts [4096, 14336], 318 instead of 308 for 65536 rows with SwiGLU. (The
+// pairs stay in place for a whole item: formed anew from floats for every block, they cost more than they save.)
+struct Sums {
     uint64_t a[64];
+    struct Values {
+        float v[128];
+        __device__ __forceinline__ float& operator[](int i) { return v[i]; }
+    };
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < 64; i++) a[i] = 0;
@@ -90,10 +81,6 @@ template <> struct Sums<true> {
             asm volatile("{ .reg .b64 x; mov.b64 x, {%1, %2}; fma.rn.f32x2 %0, x, %3, %0; }"
                          : "+l"(a[AT / 2 + i]) : "r"(v[2 * i]), "r"(v[2 * i + 1]), "l"(s2));
     }
-    struct Values {
-        float v[128];
-        __device__ __forceinline__ float& operator[](int i) { return v[i]; }
-    };
     __device__ __forceinline__ Values values() const {
         Values o;
 #pragma unroll
@@ -438,7 +425,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (more) token = row_of(next);
             const bool active = q * 32 < item.z;              // some row of the warp exists
             const bool two = SWIGLU || item.w * BN + 128 < a.N;
-            Sums<!SWIGLU> sums;
+            Sums sums;
             sums.zero();
             float4 s0, s1;                                    // the group's scales of the two boxes
             for (int kb = kb0; kb < kb1; kb++, it++) {
@@ -456,19 +443,19 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     uint32_t x[32];
                     tmem_ld32(t, x);
                     tmem_wait_ld();
-                    sums.template add<0>(x, s0.x);
+                    sums.add<0>(x, s0.x);
                     tmem_ld32(t + 32, x);
                     tmem_wait_ld();
-                    sums.template add<32>(x, s0.x);
+                    sums.add<32>(x, s0.x);
                     tmem_ld32(t + 128, x);
                     tmem_wait_ld();
-                    sums.template add<64>(x, s1.x);
+                    sums.add<64>(x, s1.x);
                     tmem_ld32(t + 160, x);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full((it + 2) % STAGES));                // all of it is in registers
-                    sums.template add<96>(x, s1.x);
+                    sums.add<96>(x, s1.x);
                 } else {
                     tc_fence_before();
                     __syncwarp();
@@ -478,7 +465,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 s1 = make_float4(s1.y, s1.z, s1.w, 0.0f);
             }
             if (!ok) break;
-            auto&& acc = sums.values();
+            Sums::Values acc = sums.values();
             if (more) begin(next, token);
             if (splits > 1) {
                 // the sums of an item's parts meet in rank 0, in the order of the ranks
