@@ -166,3 +166,21 @@ def test_the_same_plan_on_every_call():
         b = qz.qz_moe_route(logits, 8)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
     np.testing.assert_array_equal(a[3].cpu().numpy(), ref.plan(a[0].cpu().numpy(), 256)[1])
+
+
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 33])
+def test_smallest_and_largest_shapes(T):
+    """One expert, every expert chosen, groups of one, groups that are no power of two, 512 experts."""
+    g = gen(9 + T)
+
+    def rand(*s):
+        return torch.randn(s, generator=g, device="cuda")
+
+    check(rand(T, 1), 1)
+    check(rand(T, 16), 16)
+    check(rand(T, 2), 1, sigmoid=True, bias=rand(2))
+    check(rand(T, 32), 1, groups=32, top_groups=32)
+    check(rand(T, 33), 3, groups=11, top_groups=2, group_best=2)
+    check(rand(T, 34), 5, sigmoid=True, bias=0.01 * rand(34), groups=17, top_groups=3, group_best=2)
+    check(rand(T, 512), 16, sigmoid=True, renorm=False, groups=2, top_groups=1)
+    check(rand(T, 512), 16, sigmoid=True, bias=0.1 * rand(512), groups=32, top_groups=1, group_best=2)
