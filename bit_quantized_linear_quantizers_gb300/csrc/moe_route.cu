@@ -169,17 +169,17 @@ __device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_
 }
 
 // The groups that are kept where some are too close to the border for 32 bits: those surely above it, and the best of
-// the near ones by their scores in 64 bits, of the keys that can be among their best. score: lane g has that of
-// group g; hi, lo: the last one kept and the first one not. Not for a softmax with a bias, whose terms need their sum.
+// the near ones by their scores in 64 bits, of the keys that can be among their best. Lane g says of group g whether
+// it is sure or near; largest: no score is larger. Not for a softmax with a bias, whose terms need their sum.
 template <typename T>
 __device__ __noinline__ uint32_t groups_wide(const T* row, const float* bias, const qz_moe_routing* rt, int lane, const uint32_t* keys,
-                                             float score, float hi, float lo, float slack) {
+                                             bool sure, bool near, float largest) {
     const qz_moe_routing r = *rt;
     const int size = r.experts / r.groups;
-    const bool open = score > -INFINITY, sure = open && score > hi + slack, near = open && !sure && score >= lo - slack;
+    const bool soft = r.score == QZ_SCORE_SOFTMAX;
     const uint32_t surely = __ballot_sync(kFull, sure), nearly = __ballot_sync(kFull, near);
     double most = -FLT_MAX;
-    if (r.score == QZ_SCORE_SOFTMAX) {
+    if (soft) {
         for (int e = lane; e < r.experts; e += 32) most = fmax(most, (double)finite(load_logit(row + e)));
         most = warp_most(most);
     }
@@ -190,13 +190,15 @@ __device__ __noinline__ uint32_t groups_wide(const T* row, const float* bias, co
         for (int e = g * size + lane; e < (g + 1) * size; e += 32) merge2<uint32_t>(b, s, keys[e + (e >> 5)], 0u);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) merge2<uint32_t>(b, s, __shfl_xor_sync(kFull, b, o), __shfl_xor_sync(kFull, s, o));
-        const float from = unordered(r.group_best == 2 && s ? s : b) - slack;
+        const float from = unordered(r.group_best == 2 && s ? s : b);
         double eb = -INFINITY, es = -INFINITY;
         for (int e = g * size + lane; e < (g + 1) * size; e += 32) {
             const uint32_t k = keys[e + (e >> 5)];
-            if (!k || unordered(k) < from) continue;
+            if (!k) continue;
+            const float v = unordered(k);
+            if (from - v > margin(largest, fmaxf(fabsf(from), fabsf(v)), soft)) continue;
             const double l = (double)finite(load_logit(row + e));
-            merge2<double>(eb, es, (r.score == QZ_SCORE_SOFTMAX ? exp(l - most) : sigmoid(l)) + (bias ? (double)finite(bias[e]) : 0.0), -INFINITY);
+            merge2<double>(eb, es, (soft ? exp(l - most) : sigmoid(l)) + (bias ? (double)finite(bias[e]) : 0.0), -INFINITY);
         }
         __syncwarp();
 #pragma unroll
@@ -303,31 +305,34 @@ __device__ __forceinline__ int pick(const float (&l)[EPL], const float (&b)[EPL]
             for (int e = g * size + (lane & (lanes - 1)); e < (g + 1) * size; e += lanes) merge2<uint32_t>(best, second, keys[e + (e >> 5)], 0u);
         for (int o = lanes >> 1; o > 0; o >>= 1)
             merge2<uint32_t>(best, second, __shfl_xor_sync(kFull, best, o), __shfl_xor_sync(kFull, second, o));
-        // a group's score as an ordered integer, in its first lane; finite, so that differences are numbers: two that the
-        // limit makes equal are compared in 64 bits
+        // a group's score in its first lane, finite, so that differences are numbers: two that the limit makes equal are
+        // compared in 64 bits. It is off by the roundings of its keys, which may be far larger than their sum.
+        const bool open = g < r.groups && (lane & (lanes - 1)) == 0 && best;
+        float score = 0.0f, off = 0.0f;
         uint32_t mine = 0;
-        if (g < r.groups && (lane & (lanes - 1)) == 0 && best)
-            mine = ordered(r.group_best == 2 && second ? fmaxf(fminf(unordered(best) + unordered(second), FLT_MAX), -FLT_MAX) : unordered(best));
+        if (open) {
+            const float k1 = unordered(best), k2 = r.group_best == 2 && second ? unordered(second) : 0.0f;
+            score = fmaxf(fminf(k1 + k2, FLT_MAX), -FLT_MAX);
+            off = margin(most, fminf(fabsf(k1) + fabsf(k2), FLT_MAX), soft);
+            mine = ordered(score);
+        }
         uint32_t kept = 0;
-        float last = 0.0f;
-        const uint32_t all = mine;
-        for (int n = 0; n <= r.top_groups; n++) {
+        for (int n = 0; n < r.top_groups; n++) {
             const uint32_t top = __reduce_max_sync(kFull, mine);
             if (!top) break;
-            const float v = unordered(top);
-            if (n == r.top_groups) {
-                const float slack = 2.0f * margin(most, fmaxf(fabsf(last), fabsf(v)), soft);
-                if (!(last - v > slack)) {
-                    if (soft && bias) return pick_wide<T, EPL>(row, bias, &r, lane);
-                    const uint32_t u = __shfl_sync(kFull, all, min(lane, r.groups - 1) << share);
-                    kept = groups_wide<T>(row, bias, &r, lane, keys, lane < r.groups && u ? unordered(u) : -INFINITY, last, v, slack);
-                }
-            } else {
-                const int first = __ffs(__ballot_sync(kFull, mine == top)) - 1;
-                kept |= 1u << (first >> share);
-                last = v;
-                if (lane == first) mine = 0;
-            }
+            const int first = __ffs(__ballot_sync(kFull, mine == top)) - 1;
+            kept |= 1u << (first >> share);
+            if (lane == first) mine = 0;
+        }
+        // the least that a kept group may have, and the most that another one may
+        const bool in = open && (kept >> g & 1);
+        const float least = unordered(__reduce_min_sync(kFull, in ? ordered(score - off) : kFull));
+        const uint32_t other = __reduce_max_sync(kFull, open && !in ? ordered(score + off) : 0u);
+        if (other && !(least > unordered(other))) {
+            if (soft && bias) return pick_wide<T, EPL>(row, bias, &r, lane);
+            const bool sure = in && score - off > unordered(other), near = open && !sure && (in || score + off >= least);
+            const uint32_t which = (sure ? 1u : 0u) | (near ? 2u : 0u), of = __shfl_sync(kFull, which, min(lane, r.groups - 1) << share);
+            kept = groups_wide<T>(row, bias, &r, lane, keys, lane < r.groups && (of & 1), lane < r.groups && (of & 2), most);
         }
         const float per = 1.0f / (float)size;
 #pragma unroll
