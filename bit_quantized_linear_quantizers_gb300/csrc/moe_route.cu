@@ -226,9 +226,10 @@ __device__ __noinline__ int sort_wide(const T* row, const float* bias, int id, i
         rank += k > key || (k == key && e < id);
     }
     int got = -1;
-    for (int i = 0; i < n; i++)
-        if (__shfl_sync(kFull, rank, i) == lane) got = __shfl_sync(kFull, id, i);
-        else (void)__shfl_sync(kFull, id, i);
+    for (int i = 0; i < n; i++) {
+        const int place = __shfl_sync(kFull, rank, i), e = __shfl_sync(kFull, id, i);
+        if (place == lane) got = e;
+    }
     return got;
 }
 
