@@ -91,7 +91,7 @@ __device__ __forceinline__ float margin(float most, float key, bool softmax) {
     return most * ((softmax ? 2 * 132.0f : 2 * 7.0f) * 0x1p-24f) + fabsf(key) * 0x1p-22f;
 }
 
-// The choice of one token in 64 bits, every term of it, EPL experts a lane. Lane j gets the j-th expert, -1: none.
+// The choice of one token with a bias in 64 bits, every term of it, EPL experts a lane. Lane j gets the j-th expert, -1: none.
 template <typename T, int EPL>
 __device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_moe_routing* rt, int lane) {
     const qz_moe_routing r = *rt;
@@ -110,7 +110,7 @@ __device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_
 #pragma unroll 1
     for (int i = 0; i < EPL; i++) {
         const int e = lane + 32 * i;
-        const float b = bias && e < r.experts ? finite(bias[e]) : 0.0f;
+        const float b = e < r.experts ? finite(bias[e]) : 0.0f;
         const bool open = key[i] > -INFINITY && b > -INFINITY;
         const double s = soft ? exp(key[i] - most) / sum : sigmoid(key[i]);
         key[i] = open ? s + (double)b : -INFINITY;
@@ -141,11 +141,6 @@ __device__ __noinline__ int pick_wide(const T* row, const float* bias, const qz_
             const int e = lane + 32 * i;
             if (!(kept >> min(e / size, 31) & 1)) key[i] = -INFINITY;
         }
-    }
-    if (!bias) {                                               // inside the groups logits decide
-#pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (key[i] > -INFINITY) key[i] = (double)finite(load_logit(row + lane + 32 * i));
     }
     int chosen = -1;
     for (int j = 0; j < r.top_k; j++) {
