@@ -527,7 +527,7 @@ moe_select_kernel(const __grid_constant__ RouteArgs a, const int per_warp, int* 
 // Rows of the pairs of one CTA of the selection, from the counts of all of them.
 __global__ void __launch_bounds__(kPlaceThreads)
 moe_place_kernel(const __grid_constant__ RouteArgs a, const int block_tokens, const int* __restrict__ block_counts) {
-    __shared__ __align__(16) int s_all[kParts * kMoeMaxExperts], s_before[kParts * kMoeMaxExperts];
+    __shared__ int4 s_all[kPlaceThreads], s_before[kPlaceThreads];       // one each for the threads that share the counts
     __shared__ int s_base[kMoeMaxExperts];
     __shared__ int s_scan[kPlaceThreads / 32];
     pdl_wait();
@@ -552,16 +552,16 @@ moe_place_kernel(const __grid_constant__ RouteArgs a, const int block_tokens, co
             before = make_int4(before.x + (c.x & m), before.y + (c.y & m), before.z + (c.z & m), before.w + (c.w & m));
             all = make_int4(all.x + c.x, all.y + c.y, all.z + c.z, all.w + c.w);
         }
-        reinterpret_cast<int4*>(s_all)[part * quads + quad] = all;
-        reinterpret_cast<int4*>(s_before)[part * quads + quad] = before;
+        s_all[part * quads + quad] = all;
+        s_before[part * quads + quad] = before;
     }
     __syncthreads();
     int all = 0, before = 0;
     const int e = threadIdx.x;
     if (e < E)
         for (int p = 0; p < parts; p++) {
-            all += s_all[p * words + e];
-            before += s_before[p * words + e];
+            all += reinterpret_cast<const int*>(s_all)[p * words + e];
+            before += reinterpret_cast<const int*>(s_before)[p * words + e];
         }
     int total;
     const int off = scan(all, s_scan, total);
