@@ -223,16 +223,22 @@ def qz_selftest_bounded_wait(polls: int, stream=None):
 
 
 class Workspace:
-    """A reusable device scratch buffer (torch-allocated) grown on demand."""
+    """A reusable device scratch buffer (torch-allocated) grown on demand. Calls that may run at the same time, replayed
+    graphs among them, need one each. What it outgrows stays allocated as long as it lives: graphs that were captured
+    with it still write there. (It grows to twice its size at least, so all of that is less than the last buffer.)"""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self.outgrown = []
 
     def get(self, nbytes: int):
         if nbytes == 0:
             return None
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.buf is not None:
+                self.outgrown.append(self.buf)
+                nbytes = max(nbytes, 2 * self.buf.numel())
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device or "cuda")
         return self.buf
 
