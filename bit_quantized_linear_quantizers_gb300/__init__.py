@@ -1083,8 +1083,8 @@ def qz_residual_rmsnorm(x, gamma=None, y=None, token_row=None, weights=None, alp
     """r = x + alpha * z and its RMSNorm n = r * gamma / sqrt(mean(r^2) + eps), in one pass. z: the block's output y
     (bf16 [tokens, hidden]), or with token_row [tokens, k] (and weights [tokens, k], fp32) the sum of that many rows of
     y; gamma_y: z is normed before it is added. x: fp32 or bf16 [tokens, hidden], gammas of its type.
-    out: True allocates r in x's type, a tensor takes it (x itself may), None leaves it out; normed: the same for n in
-    bf16; fp8: the same for n's E4M3 codes and scales per 128 columns, a pair of tensors or True.
+    out: True allocates r in x's type, a tensor takes it (x itself may), None or False leaves it out; normed: the same for
+    n in bf16; fp8: the same for n's E4M3 codes and scales per 128 columns, a pair of tensors or True.
     Returns (r, normed, codes, scales), None where left out."""
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -1106,7 +1106,9 @@ def qz_residual_rmsnorm(x, gamma=None, y=None, token_row=None, weights=None, alp
     if out is True:
         out = torch.empty((T, H), dtype=dt, device=dev)
         p_out = out.data_ptr()
-    elif out is not None:
+    elif out is None or out is False:
+        out = None
+    else:
         ldo, p_out = _rows2(out, "out", d, H, dt), out.data_ptr()
         if out.shape[0] != T:
             raise ValueError(f"out: expected {T} rows, got {out.shape[0]}")
@@ -1114,14 +1116,16 @@ def qz_residual_rmsnorm(x, gamma=None, y=None, token_row=None, weights=None, alp
     if normed is True:
         normed = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         p_normed = normed.data_ptr()
-    elif normed is not None:
+    elif normed is None or normed is False:
+        normed = None
+    else:
         p_normed = _arg(normed, "normed", d, torch.bfloat16, T * H)
     codes = scales = p_codes = p_scales = None
     if fp8 is True:
         codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
         scales = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
         p_codes, p_scales = codes.data_ptr(), scales.data_ptr()
-    elif fp8 is not None:
+    elif fp8 is not None and fp8 is not False:
         codes, scales = fp8
         p_codes, p_scales = _arg(codes, "codes", d, 1, T * H), _arg(scales, "scales", d, torch.float32, T * (H // 128))
     st = lib.qz_residual_rmsnorm(x.data_ptr(), xt, T, H, ldx, block, p_out, ldo,
