@@ -84,12 +84,12 @@ qz_status qz_residual_rmsnorm(const void* x, qz_dtype xt, int64_t tokens, int hi
                               uint16_t* normed, uint8_t* codes, float* scales, void* stream) {
     if ((xt != QZ_F32 && xt != QZ_BF16) || tokens < 0 || hidden < 1) return QZ_ERR_INVALID_ARG;
     if (!std::isfinite(eps) || eps <= 0.0f) return QZ_ERR_INVALID_ARG;
-    if ((codes == nullptr) != (scales == nullptr) || (!gamma && (normed || codes))) return QZ_ERR_INVALID_ARG;
-    if (!x_out && !normed && !codes) return QZ_ERR_INVALID_ARG;
     if (hidden % 8 || hidden > 16384 || (codes && hidden % 128) || tokens >= kMaxRows) return QZ_ERR_SHAPE;
     if (block && (block->k < 1 || block->rows < 0 || !std::isfinite(block->alpha))) return QZ_ERR_INVALID_ARG;
     if (block && (block->k > kMoeMaxTopK || block->rows >= kMaxRows)) return QZ_ERR_SHAPE;
-    if (tokens == 0) return QZ_OK;
+    if (tokens == 0) return QZ_OK;                // tensors of no elements have null pointers
+    if ((codes == nullptr) != (scales == nullptr) || (!gamma && (normed || codes))) return QZ_ERR_INVALID_ARG;
+    if (!x_out && !normed && !codes) return QZ_ERR_INVALID_ARG;
     if (!x || ldx < hidden || (x_out && ldo < hidden)) return QZ_ERR_INVALID_ARG;
     if (block && ((block->rows && !block->y) || block->ldy < hidden)) return QZ_ERR_INVALID_ARG;
     if (block && !block->token_row && block->rows < tokens * block->k) return QZ_ERR_INVALID_ARG;
