@@ -626,8 +626,8 @@ typedef struct qz_moe_routing {
  *   ids[t, :] = the top_k open experts by key, in descending order (without bias by logit,
  *   which orders them alike); ties, of groups too, go to the lowest index
  *   weights[t, j] = scale * s[ids[t, j]], divided by the sum over j where renormalize is set
- * Keys are compared as in 64 bits, where 32 would decide otherwise too. Where fewer than
- * top_k experts are open, the rest of the token's ids is -1 with weight 0.
+ * Keys are compared as in 64 bits, where 32 would decide otherwise too; weights are fp32 throughout, good to
+ * some units of 2^-24. Where fewer than top_k experts are open, the rest of the token's ids is -1 with weight 0.
  * n_tokens: nullable device int32; tokens from *n_tokens on are padding of a fixed-size step:
  * all their ids are -1.
  * The plan of the products: the pairs (t, j) with ids[t, j] = e have the rows offsets[e] ..
@@ -647,13 +647,16 @@ qz_status qz_moe_route(const void* logits, qz_dtype lt, int64_t tokens, int64_t 
  * qz_moe_gemm_fp8:        Y[r, :] = bf16_rne(P[r, :]), Y bf16 [rows, N]
  * qz_moe_gemm_fp8_swiglu: N = 2 I, rows 0 .. I-1 of a weight are the gate's, the others the up
  *   projection's: h = g * u / (1 + exp(-g)) with g = P[r, i], u = P[r, I + i] in fp32, encoded as
- *   qz_quantize_fp8(GROUP_1x128) encodes h: y_codes [rows, I], y_scales fp32 [rows, I/128]
+ *   qz_quantize_fp8(GROUP_1x128) encodes h: y_codes [rows, I], y_scales fp32 [rows, I/128]. h is good to 10 * 2^-24
+ *   of itself for any g (exp and the quotient are the GPU's approximations, corrected), 0 where exp(-g) passes 2^126
  * qA: E4M3 [tokens, K], sA: fp32 [tokens, K/128] (qz_quantize_fp8 GROUP_1x128, or
  * qz_residual_rmsnorm). qW: E4M3 [experts, N, K], sW: fp32 [experts, N/128, K/128]
  * (qz_quantize_fp8 BLOCK_128x128 on the weights as one tensor of experts * N rows).
  * offsets: device int32 [experts + 1], ascending, as qz_moe_route writes them; what lies outside
  * 0 .. rows is cut off. Rows of no expert are not written. A row whose row_token lies outside
  * 0 .. tokens-1 is a row of zeros. A NaN in a row of qA or sA reaches that row alone.
+ * The same call gives the same bits. With more than 32 rows a row's bits depend on its own inputs alone; with up to 32
+ * several CTAs may share its K, and its sums then have another order than in a call of other sizes.
  * Shapes: experts 1..512, rows and tokens < 2^31, experts * N < 2^31, K % 128 == 0, N % 128 == 0 (I % 128 == 0).
  * Alignment: qA, qW, outputs 16 B, the others 4 B. rows == 0 is a no-op. No workspace. */
 qz_status qz_moe_gemm_fp8(const uint8_t* qA, const float* sA, int64_t tokens, const int32_t* row_token, int64_t rows,
@@ -679,13 +682,13 @@ typedef struct qz_block_output {
  *   z[t] = sum_j weights[t, j] * y[token_row[t, j]];  with block->gamma: z *= block->gamma / sqrt(mean(z^2) + eps)
  *   r = x + alpha * z (r = x where block is NULL);  n = r * gamma / sqrt(mean(r^2) + eps)
  * x: [tokens, hidden] of type xt, rows ldx elements apart. x_out: nullable, r in xt, rows ldo
- * apart; it may be x itself. gamma: nullable [hidden] of type xt; without it there are no n and no
- * codes. normed: nullable, n in bf16, dense. codes, scales: nullable together, n as
+ * apart; it may be x itself (but nothing else that the call reads). gamma: nullable [hidden] of type xt; without
+ * it there are no n and no codes. normed: nullable, n in bf16, dense. codes, scales: nullable together, n as
  * qz_quantize_fp8(GROUP_1x128) encodes it: [tokens, hidden] and fp32 [tokens, hidden/128].
- * All sums are fp32 and n, its codes and x_out come from the unrounded fp32 r, each rounded once. A
- * row whose sum of squares passes fp32's range gives n = 0, one with an infinity or NaN gives NaN;
- * neither reaches another row.
- * Shapes: hidden % 8 == 0, 8..16384; hidden % 128 == 0 with codes. eps finite, > 0. tokens < 2^31.
+ * All sums are fp32 and n, its codes and x_out come from the unrounded fp32 r, each rounded once (n is r times the
+ * rounded reciprocal of the root, times gamma). A row of r whose sum of squares passes fp32's range gives n = 0, one with
+ * infinities the same but NaN in their places, one with a NaN gives NaN; none of them reaches another row.
+ * Shapes: hidden % 8 == 0, 8..16384; hidden % 128 == 0 with codes. eps finite, > 0. tokens < 2^31; tokens == 0 is a no-op.
  * Alignment: x, x_out, y, gammas, normed, codes 16 B, ldx, ldo, ldy multiples of 16 bytes, the others 4 B. */
 qz_status qz_residual_rmsnorm(const void* x, qz_dtype xt, int64_t tokens, int hidden, int64_t ldx,
                               const qz_block_output* block, void* x_out, int64_t ldo, const void* gamma, float eps,
