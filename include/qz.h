@@ -685,9 +685,9 @@ typedef struct qz_block_output {
  * apart; it may be x itself (but nothing else that the call reads). gamma: nullable [hidden] of type xt; without
  * it there are no n and no codes. normed: nullable, n in bf16, dense. codes, scales: nullable together, n as
  * qz_quantize_fp8(GROUP_1x128) encodes it: [tokens, hidden] and fp32 [tokens, hidden/128].
- * All sums are fp32 and n, its codes and x_out come from the unrounded fp32 r, each rounded once (n is r times the
- * rounded reciprocal of the root, times gamma). A row of r whose sum of squares passes fp32's range gives n = 0, one with
- * infinities the same but NaN in their places, one with a NaN gives NaN; none of them reaches another row.
+ * All sums are fp32 and n, its codes and x_out come from the unrounded fp32 r, each rounded once. A row of r whose sum of
+ * squares passes fp32's range gives n = 0, one with infinities the same but NaN in their places, one with a NaN
+ * gives NaN; none of them reaches another row.
  * Shapes: hidden % 8 == 0, 8..16384; hidden % 128 == 0 with codes. eps finite, > 0. tokens < 2^31; tokens == 0 is a no-op.
  * Alignment: x, x_out, y, gammas, normed, codes 16 B, ldx, ldo, ldy multiples of 16 bytes, the others 4 B. */
 qz_status qz_residual_rmsnorm(const void* x, qz_dtype xt, int64_t tokens, int hidden, int64_t ldx,
