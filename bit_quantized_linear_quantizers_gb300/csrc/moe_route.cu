@@ -606,7 +606,7 @@ qz_status select_kernel(const RouteArgs& a, const Split& s, int* counts, cudaStr
     const bool simple = !a.bias && a.r.groups == 1;
     const auto fn = simple ? moe_select_kernel<T, EPL, true> : moe_select_kernel<T, EPL, false>;
     const int bytes = 4 * s.warps * (a.r.experts + (a.r.groups > 1 ? key_words(a.r.experts) : 0));
-    if (bytes > 48 * 1024) QZ_TRY(opt_in_smem((const void*)fn, bytes));
+    if (bytes > 40 * 1024) QZ_TRY(opt_in_smem((const void*)fn, bytes));         // the 48 KB of a launch hold the static arrays too
     return launch_pdl(fn, dim3(s.blocks), dim3(s.warps * 32), bytes, st, a, s.per_warp, counts);
 }
 

@@ -48,3 +48,13 @@ def test_groups_of_few_open_experts_beside_large_keys(big):
     for top in (2, 4):
         check(logits, 4, sigmoid=True, bias=bias, groups=8, top_groups=top, group_best=2)
         check(logits, 4, sigmoid=True, bias=bias, groups=8, top_groups=top, group_best=1)
+
+
+@pytest.mark.parametrize("E, G, T", [(378, 7, 16), (378, 27, 700), (403, 13, 15), (403, 31, 40), (377, 13, 50), (379, 1, 50), (512, 32, 33)])
+def test_sizes_around_the_default_limit_of_shared_memory(E, G, T):
+    """16 warps' counts and keys of 378 experts are 48 KB, which with the kernel's own arrays is more than a launch has without asking."""
+    g = gen(E + T)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    check(logits, 6, sigmoid=True, bias=bias, groups=G, top_groups=min(G, 3), group_best=2)
+    check(logits, 6, groups=G, top_groups=min(G, 3), group_best=2)
