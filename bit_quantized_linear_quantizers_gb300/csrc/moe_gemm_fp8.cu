@@ -21,8 +21,10 @@
 //  warps 8-15  promotion: block scales are fp32, so every block's partial sums leave tensor
 //              memory to be added as acc += P_kb * (sA sW). A thread holds one row of 64 columns of
 //              each of the two boxes.
-// What bounds it with many rows is the cycle of an accumulator: MMA 512 cycles, hand-off, promotion,
-// hand-off, for two blocks of K by turns. So what lies between is kept short: scales are read by the promoting threads
+// With many rows neither the tensor pipe, L2 nor shared memory is at its limit. The cycle of an accumulator (MMA 512 cycles,
+// hand-off, promotion, hand-off, about 1200), two blocks of K by turns, gives 660 cycles a block, which this loop takes with
+// operands that lie there already; with rows, scales and items on their way it takes 860 (960 with SwiGLU), and where those
+// 200 to 300 go is not known. What lies between is kept short: scales are read by the promoting threads
 // themselves, groups of four blocks ahead (staged in shared memory they came 300 cycles late), and waits are few.
 // With few rows the bound is the weights' way from memory, and the promotion and the gather of rows that
 // are not there are left out. Where items are fewer than SMs (rows <= 32), a cluster shares an item's K.

@@ -17,8 +17,8 @@
 // the CTAs before it and the rows of the experts before it. Up to kAlone tokens are one CTA and one launch.
 //
 // What bounds it: for few tokens the chain of about 100 cycles per chosen expert, two launches, and the latency of the
-// counts between them; for many the issue of about 500 instructions a token (16384 of 128 experts: 18 us), 2200 with a bias
-// and groups (8000 of 256 experts: 36 us). The bytes are little.
+// counts between them; for many the issue of about 500 instructions a token (16384 of 128 experts: 18 us), 2100 with a bias
+// and groups (8000 of 256 experts: 33 us). The bytes are little.
 #include "qz_moe.cuh"
 
 #include <algorithm>
